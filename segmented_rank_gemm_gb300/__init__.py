@@ -6,12 +6,16 @@ C ABI declared in ``include/lora_layer.h``; ``segmented_rank_gemm_gb300.lora`` i
 thin ctypes binding with the same names.  Importing the binding raises if the library
 has not been built: there is no CPU fallback.
 
+``segmented_rank_gemm_gb300.kv`` (a paged 4-bit key/value cache, the attention over it, block
+tables and slot maps; ``include/lora_kv.h``) and ``segmented_rank_gemm_gb300.norm`` (the
+residual norm; ``include/lora_norm.h``) are the steps between a decoder block's projections.
+
 ``segmented_rank_gemm_gb300.workloads`` (seeded synthetic inputs) imports without the
 library.
 """
 import importlib
 
-__all__ = ["lora", "workloads", "build"]
+__all__ = ["lora", "kv", "norm", "workloads", "build"]
 
 
 def __getattr__(name):

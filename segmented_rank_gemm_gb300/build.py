@@ -54,8 +54,8 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "lora_layer.h"),
-                                      os.path.abspath(__file__)]
+        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(ROOT, "include", "*.h")) + [
+            os.path.abspath(__file__)]
 
 
 def up_to_date(lib: str = LIB_PATH) -> bool:

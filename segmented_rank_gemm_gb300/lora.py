@@ -1,5 +1,6 @@
 """ctypes binding of the layer's C ABI (``include/lora_layer.h``) and of the adapter cache
-over it (``include/lora_residency.h``).
+over it (``include/lora_residency.h``).  It loads the library for the whole package; the
+calls of the 4-bit key/value cache and of the norm are in ``kv.py`` and ``norm.py``.
 
 The functions below carry the C names and only marshal arguments: torch tensors become
 raw pointers, torch streams become ``cudaStream_t`` handles, and a negative status
@@ -29,14 +30,21 @@ LORA_ECUDA, LORA_ENOMEM, LORA_ESTATE, LORA_ETIMEOUT = -5, -6, -7, -8
 LORA_ENOENT, LORA_ECAPACITY, LORA_EBOUNDS = -9, -10, -11
 
 # every entry point declared in include/lora_layer.h
-ABI_FUNCTIONS = ("lora_layer_create", "lora_layer_create_pooled", "lora_layer_create_fp8",
-                 "lora_get_pool_usage",
-                 "load_adapter_slot", "load_adapter_slot_composed",
-                 "unload_adapter_slot",
-                 "set_batch_segments", "lora_forward", "lora_forward_host", "lora_get_status",
-                 "lora_get_segments", "lora_set_trace_events", "lora_set_gemm_plan",
-                 "lora_last_error", "lora_layer_destroy", "lora_build_segments_static",
-                 "lora_wait_selftest", "lora_get_launch_count")
+LAYER_FUNCTIONS = ("lora_layer_create", "lora_layer_create_pooled", "lora_layer_create_fp8",
+                   "lora_get_pool_usage",
+                   "load_adapter_slot", "load_adapter_slot_composed",
+                   "unload_adapter_slot",
+                   "set_batch_segments", "lora_forward", "lora_forward_host", "lora_get_status",
+                   "lora_get_segments", "lora_set_trace_events", "lora_set_gemm_plan",
+                   "lora_last_error", "lora_layer_destroy", "lora_build_segments_static",
+                   "lora_wait_selftest", "lora_get_launch_count")
+# every entry point declared in include/lora_kv.h
+KV_FUNCTIONS = ("lora_kv_maps", "lora_kv_release", "lora_kv_cache_create", "lora_kv_append",
+                "lora_kv_read", "lora_kv_attend", "lora_kv_get_status", "lora_kv_cache_bytes",
+                "lora_kv_last_error", "lora_kv_cache_destroy")
+# every entry point declared in include/lora_norm.h
+NORM_FUNCTIONS = ("lora_rms_norm",)
+ABI_FUNCTIONS = LAYER_FUNCTIONS + KV_FUNCTIONS + NORM_FUNCTIONS
 # every entry point declared in include/lora_residency.h
 CACHE_FUNCTIONS = ("lora_cache_create", "lora_cache_add", "lora_cache_add_composed",
                    "lora_cache_remove",
@@ -91,7 +99,7 @@ def _load() -> ctypes.CDLL:
     L.lora_last_error.restype = ctypes.c_char_p
     L.lora_layer_destroy.argtypes = [vp]
     L.lora_layer_destroy.restype = None
-    for name in ABI_FUNCTIONS:
+    for name in LAYER_FUNCTIONS:
         if name not in ("lora_last_error", "lora_layer_destroy"):
             getattr(L, name).restype = i32
     i64 = ctypes.c_int64
@@ -115,6 +123,26 @@ def _load() -> ctypes.CDLL:
                  "lora_cache_map_batch", "lora_cache_prefetch", "lora_cache_slot_of",
                  "lora_cache_get_stats", "lora_cache_sync"):
         getattr(L, name).restype = i32
+    L.lora_kv_maps.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                               vp, vp]
+    L.lora_kv_release.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp]
+    L.lora_kv_cache_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, i32, f32, f32, vp]
+    L.lora_kv_append.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp]
+    L.lora_kv_read.argtypes = [vp, vp, i32, vp, vp, vp]
+    L.lora_kv_attend.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, f32, vp, i32,
+                                 vp]
+    L.lora_kv_get_status.argtypes = [vp, vp]
+    L.lora_kv_cache_bytes.argtypes = [vp]
+    L.lora_kv_cache_bytes.restype = i64
+    L.lora_kv_last_error.argtypes = [vp]
+    L.lora_kv_last_error.restype = ctypes.c_char_p
+    L.lora_kv_cache_destroy.argtypes = [vp]
+    L.lora_kv_cache_destroy.restype = None
+    for name in ("lora_kv_maps", "lora_kv_release", "lora_kv_cache_create", "lora_kv_append",
+                 "lora_kv_read", "lora_kv_attend", "lora_kv_get_status"):
+        getattr(L, name).restype = i32
+    L.lora_rms_norm.argtypes = [vp, i32, vp, i32, vp, f32, i32, i32, i32, vp, i32, vp, vp, vp, vp]
+    L.lora_rms_norm.restype = i32
     return L
 
 

@@ -1,0 +1,62 @@
+"""ctypes binding of the root-mean-square norm with the residual's addition
+(``include/lora_norm.h``)."""
+from __future__ import annotations
+
+import torch
+
+from .lora import LORA_BF16, LORA_EINVAL, LORA_F32, LoraError, _stream, library
+
+_lib = library()
+_DTYPES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+
+
+def _bad(what: str):
+    raise LoraError(LORA_EINVAL, what)
+
+
+def _rows(name: str, t, like) -> int:
+    """The row distance of a CUDA tensor of the shape and type of ``like``."""
+    if t.dtype != like.dtype or not t.is_cuda or t.shape != like.shape:
+        _bad("%s must be a CUDA tensor of x's type and shape" % name)
+    row, one = t.stride()
+    T, K = t.shape
+    if K > 1 and one != 1:
+        _bad("%s: the elements of a row must be dense" % name)
+    return row if T > 1 else max(row, K)  # one row has no distance
+
+
+def _dense(name: str, t, dtype, shape) -> int:
+    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+        _bad("%s must be a contiguous CUDA tensor %s of %s" % (name, shape, dtype))
+    return t.data_ptr()
+
+
+def lora_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, xq=None, sx=None,
+                  stream=None) -> None:
+    """h = x + residual; y = h rsqrt(mean(h^2) + eps) weight over the rows of x [T, K] (bf16 or
+    fp32).  Outputs, each optional: ``residual_out`` (h; may be ``residual``), ``y``, and
+    ``xq`` (float8_e4m3fn) with its row scales ``sx`` [T] (fp32)."""
+    if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda:
+        _bad("x must be a CUDA tensor [T, K] of bf16 or fp32")
+    T, K = x.shape
+    ldx = _rows("x", x, x)
+    ldr = _rows("residual", residual, x) if residual is not None else 0
+    ldh = _rows("residual_out", residual_out, x) if residual_out is not None else 0
+    rc = _lib.lora_rms_norm(
+        x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+        _dense("weight", weight, x.dtype, (K,)), eps, T, K, _DTYPES[x.dtype],
+        None if residual_out is None else residual_out.data_ptr(), ldh,
+        None if y is None else _dense("y", y, x.dtype, (T, K)),
+        None if xq is None else _dense("xq", xq, torch.float8_e4m3fn, (T, K)),
+        None if sx is None else _dense("sx", sx, torch.float32, (T,)), _stream(stream))
+    if rc < 0:
+        raise LoraError(rc, "lora_rms_norm")
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, xq=None, sx=None,
+             stream=None):
+    """``lora_rms_norm`` returning y; ``y`` is allocated if not given."""
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    lora_rms_norm(x, weight, eps, residual, residual_out, y, xq, sx, stream)
+    return y
