@@ -13,19 +13,23 @@
 // instructions a pair and the products go to the tensor cores (mma.sync 16x8x16: a decode step
 // has 1 to 8 columns a group, far from the 128 rows a tcgen05 tile wants, and its operand A comes
 // from the registers that decoded it, without a trip through shared or tensor memory):
-//   S^T tile = K (16 tokens x 16 dimensions) Q^T,    K and Q in bf16
-//   O^T tile = V^T (16 dimensions x 16 tokens) P^T,  V and P in fp16
-// K's decoded values n s have at most 7 significant bits, exact in bf16, and q stays as it came.
-// V's are exact in fp16 (times 2^-5); p is rounded to fp16 (relative error 2^-11, in 2^-6 .. 2^14
-// around the reference 2^6 it is normal down to 2^-20 of the maximum) while l sums the fp32 p.
+//   S^T tile = K (16 tokens x 16 dimensions) Q^T
+//   O^T tile = V^T (16 dimensions x 16 tokens) P^T
+// in fp16 with fp32 accumulation.  K's and V's decoded values n s 2^-5 are exact in fp16.  A query
+// row is scaled by the power of two that brings its largest element to 2^9 .. 2^10, which its 8
+// significant bits survive down to 2^-23 of that.  p is rounded to fp16 (relative error 2^-11;
+// with the reference at 2^6 it is a normal number down to 2^-20 of the maximum) while l sums
+// the fp32 p.
 //
-// Decoding, per pair of 4-bit codes n in two halves of a register: n OR the bits of 2^k gives
-// 2^k + n, and one fused multiply-add (2^k + n) s - (2^k + 8) s = (n - 8) s, exact because
-// (2^k + 8) s has at most 11 (fp16) or 8 (bf16) significant bits.
+// Decoding, per pair of 4-bit codes n in two halves of a register: n OR the bits of 1024 gives
+// 1024 + n (1024 + 16 n for the next code up), and one fused multiply-add
+// (1024 + n) s - 1032 s = (n - 8) s, exact because 1032 s = 8 129 s has at most 11 significant
+// bits.  One shift serves the two other codes of a half: 9 instructions for 8 codes.
 //
 // Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs
 // and those into equal ranges for their warps, so that one long request fills the GPU and many
-// short ones balance.  Each warp is independent: it runs its own ring of bulk copies (a tile of
+// short ones balance.  A group counts kSetup units besides its tiles, about what its queries'
+// load and its output cost.  Each warp is independent: it runs its own ring of bulk copies (a tile of
 // one head is one contiguous 4.6 KB, two of them for 16-position pages) and keeps its group's
 // state in registers.  A group cut by a range's end leaves (m, l, O) pieces, joined by the CTA
 // and, between CTAs, by the last one to arrive, in the order of the pieces: results do not
@@ -47,7 +51,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;    // positions of a tile
 constexpr int kStages = 3;   // tiles of a warp's ring
-constexpr int kMinTiles = 8; // tiles of a CTA's range, at least
+constexpr int kSetup = 2;    // units a group counts before its tiles
+constexpr int kMinSpan = 8;  // units of a CTA's range, at least
 constexpr int kCtasPerSm = 2;
 constexpr float kRef = 6.f;    // p is 2^kRef at the reference
 constexpr float kSlack = 8.f;  // how far (in powers of two) a score may exceed the reference
@@ -59,14 +64,10 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+// (a & mask) | bits, one instruction (written out: two immediates are else split in two).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
   return r;
 }
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
@@ -89,6 +90,48 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Each half of v twice.
+__device__ __forceinline__ uint32_t both_lo(uint32_t v) { return prmt(v, v, 0x1010); }
+__device__ __forceinline__ uint32_t both_hi(uint32_t v) { return prmt(v, v, 0x3232); }
+// a * b + c of two floats at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// The scales of 4-bit codes, for a pair's low (s0, c0) and next (s1, c1) codes.
+struct Decode {
+  uint32_t s0, c0, s1, c1;
+};
+__device__ __forceinline__ Decode decode_scales(uint32_t s) {  // two e4m3 values as fp16
+  Decode d;
+  d.s0 = mul_f16x2(s, 0x28002800u);     // s 2^-5
+  d.c0 = mul_f16x2(d.s0, 0xE408E408u);  // -1032 s 2^-5
+  d.s1 = mul_f16x2(d.s0, 0x2C002C00u);  // s 2^-9
+  d.c1 = mul_f16x2(d.s0, 0xD480D480u);  // -72 s 2^-5
+  return d;
+}
+// The four pairs of codes of y: nibbles i of both halves.
+__device__ __forceinline__ void decode4(uint32_t y, const Decode& d, uint32_t (&o)[4]) {
+  const uint32_t y8 = y >> 8;
+  o[0] = fma_f16x2(and_or(y, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
+  o[1] = fma_f16x2(and_or(y, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
+  o[2] = fma_f16x2(and_or(y8, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
+  o[3] = fma_f16x2(and_or(y8, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -99,19 +142,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// a / b of non-negative values, in 32 bits where they fit (a 64-bit division takes longer than a
+// load from L2).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // ---- requests, groups and the sequence of tiles ----
@@ -144,36 +187,41 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   return r;
 }
 
-__device__ __forceinline__ long long request_tiles(const Request& r, int heads) {
-  return static_cast<long long>(r.tiles) * r.col_tiles * heads;
+__device__ __forceinline__ long long request_units(const Request& r, int heads) {
+  return static_cast<long long>(r.tiles + kSetup) * r.col_tiles * heads;
 }
 
-// A position in the sequence of tiles: request, head, column tile, tile (fastest last).
+// A position in the sequence of tiles: request, head, column tile, tile (fastest last), and
+// the tile's unit: a group's tiles come after its kSetup units.
 template <int NT>
 struct Cursor {
   Request r;
   int b, head, col, tile;
-  __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem) {
+  long long unit;
+  // The first tile at or after unit `at`, the rem-th of request b_.
+  __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at) {
     b = b_;
     r = load_request<NT>(a, b, false);
-    tile = static_cast<int>(rem % r.tiles);
-    const long long g = rem / r.tiles;
-    col = static_cast<int>(g % r.col_tiles);
-    head = static_cast<int>(g / r.col_tiles);
+    const int per = r.tiles + kSetup;
+    const long long group = quotient(rem, per);
+    const int off = static_cast<int>(rem - group * per);
+    tile = max(0, off - kSetup);
+    unit = at + max(0, kSetup - off);
+    head = static_cast<int>(quotient(group, r.col_tiles));
+    col = static_cast<int>(group - static_cast<long long>(head) * r.col_tiles);
   }
-  // Moves to the next tile; true if that begins another group.  Not past the last one.
-  __device__ __forceinline__ bool next(const KvAttendArgs& a) {
-    if (++tile < r.tiles) return false;
+  // Moves to the next group.  Not past the last one.
+  __device__ __forceinline__ void next_group(const KvAttendArgs& a) {
+    unit += r.tiles - tile + kSetup;
     tile = 0;
-    if (++col < r.col_tiles) return true;
+    if (++col < r.col_tiles) return;
     col = 0;
-    if (++head < a.pages.heads) return true;
+    if (++head < a.pages.heads) return;
     head = 0;
     do {
       ++b;
       r = load_request<NT>(a, b, false);
     } while (r.col_tiles == 0);
-    return true;
   }
 };
 
@@ -185,15 +233,16 @@ constexpr int piece_floats() {
 }
 
 struct PieceInfo {
-  long long group;  // first tile of the group in the sequence, -1: none
+  long long group;  // unit of the group's first tile, -1: none
   int tiles;        // of the group
-  int b, head, col;
+  int cols;         // its columns
+  int row0, head, first_col;
 };
 
 template <int D, int NT>
 struct State {
   float o[D / 16][NT][4];  // [dimension pair][column tile][fragment]
-  float m[NT][2], l[NT][2];
+  float2 m[NT], l[NT];     // of the fragment's two columns
 };
 
 // Columns' rows in q and out: the element offset of column c, or -1.
@@ -221,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   __shared__ long long start_rem[kWarps];
   __shared__ int start_b[kWarps];
   __shared__ PieceInfo info[kWarps * 2];
-  __shared__ int last_cta;
+  __shared__ int last_cta[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -245,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b)
-    mine += request_tiles(load_request<NT>(a, b, blockIdx.x == 0), heads);
+    mine += request_units(load_request<NT>(a, b, blockIdx.x == 0), heads);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -263,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const long long span = max(static_cast<long long>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+  const long long span = max(static_cast<long long>(kMinSpan), quotient(total + gridDim.x - 1, gridDim.x));
   const long long cta_lo = span * blockIdx.x, cta_hi = min(total, cta_lo + span);
   if (cta_lo >= total) return;
   const long long wspan = (cta_hi - cta_lo + kWarps - 1) / kWarps;
@@ -274,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       long long rem = at - before;
       int b = b0;
       for (;; ++b) {
-        const long long n = request_tiles(load_request<NT>(a, b, false), heads);
+        if (b == b1 - 1) break;  // the run's last: what is left is its own
+        const long long n = request_units(load_request<NT>(a, b, false), heads);
         if (rem < n) break;
         rem -= n;
       }
@@ -293,12 +343,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     uint8_t* const my_ring = ring + warp * kStages * kTileBytes;
     uint64_t* const bar = full[warp];
     Cursor<NT> in, at;
-    in.start(a, start_b[warp], start_rem[warp]);
+    in.start(a, start_b[warp], start_rem[warp], w_lo);
     at = in;
-    const int n = static_cast<int>(w_hi - w_lo);
     const int shift = a.pages.page_shift;
+    const uint32_t page_bytes = static_cast<uint32_t>(kBlock) << (shift - 4);  // of one head
+    const size_t page_stride = static_cast<size_t>(page_bytes) * heads;
+    const int in_page = (1 << shift) / kTile - 1;  // mask of a tile's place in its page
 
-    // page ids of 32 consecutive tiles of the request being fetched, one tile a lane
+    // page ids of 32 consecutive tiles of the request being fetched, one tile a lane (two
+    // pages a tile where a page is half of one)
     int ids_b = -1, ids_tile = 0, id0 = 0, id1 = 0;
     bool dead = false;
     auto fetch_ids = [&]() {
@@ -307,398 +360,452 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
       const int32_t* row = a.table + static_cast<size_t>(in.b) * a.max_blocks;
       const int pos = (ids_tile + lane) * kTile;
-      const int i0 = min(pos >> shift, last), i1 = min((pos + kKvBlock) >> shift, last);
       const bool some = in.r.kv > 0;
-      id0 = some ? __ldg(row + i0) : 0;
-      id1 = some ? __ldg(row + i1) : 0;
-      if (static_cast<unsigned>(id0) >= static_cast<unsigned>(a.pages.num_pages) ||
-          static_cast<unsigned>(id1) >= static_cast<unsigned>(a.pages.num_pages)) {
+      id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
+      id1 = some ? __ldg(row + min((pos + kKvBlock) >> shift, last)) : 0;
+      const unsigned pages = a.pages.num_pages;
+      if (static_cast<unsigned>(id0) >= pages || static_cast<unsigned>(id1) >= pages) {
         atomicOr(a.err, LORA_ERRF_BAD_ID);
-        if (static_cast<unsigned>(id0) >= static_cast<unsigned>(a.pages.num_pages)) id0 = 0;
-        if (static_cast<unsigned>(id1) >= static_cast<unsigned>(a.pages.num_pages)) id1 = 0;
+        if (static_cast<unsigned>(id0) >= pages) id0 = 0;
+        if (static_cast<unsigned>(id1) >= pages) id1 = 0;
       }
     };
-    auto issue = [&](int u) {  // fetch tile `in` as the warp's u-th
+    const uint8_t* in_base = nullptr;  // the head's part of page 0
+    int in_stage = 0;
+    auto begin_run = [&]() {
       if (in.b != ids_b || (in.tile & ~31) != ids_tile) fetch_ids();
+      in_base = a.pages.base + static_cast<size_t>(in.head) * page_bytes;
+    };
+    auto issue = [&]() {  // fetch tile `in` into its stage
       const int p0 = __shfl_sync(0xffffffffu, id0, in.tile & 31);
-      const int p1 = __shfl_sync(0xffffffffu, id1, in.tile & 31);
+      const int p1 = shift == 4 ? __shfl_sync(0xffffffffu, id1, in.tile & 31) : 0;
       if (lane == 0) {
-        uint8_t* dst = my_ring + (u % kStages) * kTileBytes;
-        uint64_t* b = bar + u % kStages;
-        mbar_arrive_expect_tx(b, kTileBytes);
-        const int blk = (in.tile * kTile & ((1 << shift) - 1)) / kKvBlock;
+        uint8_t* dst = my_ring + in_stage * kTileBytes;
+        mbar_arrive_expect_tx(bar + in_stage, kTileBytes);
+        const uint8_t* src = in_base + p0 * page_stride;
         if (shift > 4) {
-          bulk_load_g2s(dst, a.pages.base + a.pages.block(p0, in.head, blk), kTileBytes, b);
+          bulk_load_g2s(dst, src + (in.tile & in_page) * kTileBytes, kTileBytes, bar + in_stage);
         } else {
-          bulk_load_g2s(dst, a.pages.base + a.pages.block(p0, in.head, 0), kBlock, b);
-          bulk_load_g2s(dst + kBlock, a.pages.base + a.pages.block(p1, in.head, 0), kBlock, b);
+          bulk_load_g2s(dst, src, kBlock, bar + in_stage);
+          bulk_load_g2s(dst + kBlock, in_base + p1 * page_stride, kBlock, bar + in_stage);
+        }
+      }
+      in_stage = in_stage == kStages - 1 ? 0 : in_stage + 1;
+    };
+    bool more = in.unit < w_hi;  // `in` is a tile to fetch
+    auto fetch = [&]() {         // fetch it and move on
+      if (!more) return;
+      issue();
+      if (in.tile + 1 < in.r.tiles) {
+        ++in.tile;
+        more = ++in.unit < w_hi;
+        if (more && (in.tile & 31) == 0) begin_run();
+      } else {
+        more = in.unit + 1 + kSetup < w_hi;
+        if (more) {
+          in.next_group(a);
+          begin_run();
         }
       }
     };
-
-    int issued = 0;
-    for (; issued < kStages && issued < n; ++issued) {
-      if (issued) in.next(a);
-      issue(issued);
-    }
+    if (more) begin_run();
+    for (int i = 0; i < kStages; ++i) fetch();
 
     uint32_t qf[KT][NT][2];
-    int lim[NT][2], lim_lo = 0, lim_hi = 0;
+    int lim[NT][2];
+    float2 unit[NT];  // from products to scores in units of log2(e)
     State<D, NT> st;
     const int ta = kv_frag_token(g);  // tokens of fragment rows g and g + 8: ta, ta + 8
-    const int tv = ((t & 1) | (t >> 1) << 1);
-    bool fresh = true;
-    long long group = w_lo - at.tile;
+    const int tv = (t & 1) | (t >> 1) << 1;
+    const int G = a.q_heads / heads;
+    int stage = 0, phase = 0;
 
-    for (int u = 0; u < n; ++u) {
-      if (fresh) {
-        // the group's queries, the last position each column sees, and an empty state
-        const int G = a.q_heads / heads;
+    while (at.unit < w_hi) {
+      // the group's queries, the last position each column sees, and an empty state
+      const long long group = at.unit - at.tile;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const long long off = column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + g, a.ldq);
-          const uint4* src =
-              reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off + t * (D / 4));
+      for (int nt = 0; nt < NT; ++nt) {
+        const long long off = column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + g, a.ldq);
+        const uint4* src =
+            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off + t * (D / 4));
+        uint4 v[KW];
+        float top = 0.f;
 #pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const uint4 v = off >= 0 ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
-            qf[2 * w][nt][0] = prmt(v.x, v.z, 0x5410);
-            qf[2 * w][nt][1] = prmt(v.x, v.z, 0x7632);
-            qf[2 * w + 1][nt][0] = prmt(v.y, v.w, 0x5410);
-            qf[2 * w + 1][nt][1] = prmt(v.y, v.w, 0x7632);
-          }
+        for (int w = 0; w < KW; ++w) {
+          v[w] = off >= 0 ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            // (a column past the last has zero queries and is not written: any limit does)
-            const int c = at.col * 8 * NT + nt * 8 + 2 * t + j;
-            lim[nt][j] = at.r.kv - at.r.q_len + min(c / G, at.r.q_len - 1);
-            st.m[nt][j] = kNone;
-            st.l[nt][j] = 0.f;
-          }
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
         }
-        lim_lo = at.r.kv - at.r.q_len + at.col * 8 * NT / G;
-        lim_hi = at.r.kv - at.r.q_len + min(at.r.q_len * G - 1, at.col * 8 * NT + 8 * NT - 1) / G;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e with top 2^e in [2^9, 2^10); rows of zeros, infinities or tiny values keep e in range
+        const int e = top > 0.f && top < INFINITY
+                          ? min(120, 9 + 127 - static_cast<int>(__float_as_uint(top) >> 23))
+                          : 0;
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e + 127) << 23), a.scale_log2);
 #pragma unroll
-        for (int m = 0; m < KT; ++m)
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+          // words x, y hold dimensions 0..3 of the eight, z, w 4..7: pairs (i, i + 4)
+          qf[2 * w][nt][0] = pack_f16x2(bf16_lo(x[0]) * up, bf16_lo(x[2]) * up);
+          qf[2 * w][nt][1] = pack_f16x2(bf16_hi(x[0]) * up, bf16_hi(x[2]) * up);
+          qf[2 * w + 1][nt][0] = pack_f16x2(bf16_lo(x[1]) * up, bf16_lo(x[3]) * up);
+          qf[2 * w + 1][nt][1] = pack_f16x2(bf16_hi(x[1]) * up, bf16_hi(x[3]) * up);
+        }
+        // (never 0, so that a masked score stays -inf)
+        const float down =
+            fmaxf(32.f * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
+        unit[nt].x = __shfl_sync(0xffffffffu, down, 8 * t);
+        unit[nt].y = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) st.o[m][nt][j] = 0.f;
-        fresh = false;
+        for (int j = 0; j < 2; ++j) {
+          // (a column past the last has zero queries and is not written: any limit does)
+          const int c = at.col * 8 * NT + nt * 8 + 2 * t + j;
+          lim[nt][j] = at.r.kv - at.r.q_len + min(c / G, at.r.q_len - 1);
+        }
+        st.m[nt] = make_float2(kNone, kNone);
+        st.l[nt] = make_float2(0.f, 0.f);
       }
-
-      if (!dead && !mbar_wait(bar + u % kStages, (u / kStages) & 1, a.err)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      const int pos0 = at.tile * kTile;
-      if (pos0 <= lim_hi) {
-        const uint8_t* tile = my_ring + (u % kStages) * kTileBytes;
-        float s[2][NT][4];
+      const int lim_lo = at.r.kv - at.r.q_len + at.col * 8 * NT / G;
+      const int lim_hi =
+          at.r.kv - at.r.q_len + min(at.r.q_len * G - 1, at.col * 8 * NT + 8 * NT - 1) / G;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint8_t* blk = tile + k * kBlock;
-          uint32_t kw[2][KW], sc[2][KW / 2];
-          if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(blk + ta * 64 + 16 * t);
-            const uint4 y = *reinterpret_cast<const uint4*>(blk + (ta + 8) * 64 + 16 * t);
-            kw[0][0] = x.x, kw[0][1] = x.y, kw[0][2] = x.z, kw[0][3] = x.w;
-            kw[1][0] = y.x, kw[1][1] = y.y, kw[1][2] = y.z, kw[1][3] = y.w;
-            const uint32_t b4 = *reinterpret_cast<const uint32_t*>(blk + kv_k_scales(D) + lane * 4);
-            sc[0][0] = prmt(b4, 0u, 0x4040) << 4;
-            sc[0][1] = prmt(b4, 0u, 0x4141) << 4;
-            sc[1][0] = prmt(b4, 0u, 0x4242) << 4;
-            sc[1][1] = prmt(b4, 0u, 0x4343) << 4;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(blk + ta * 32 + 8 * t);
-            const uint2 y = *reinterpret_cast<const uint2*>(blk + (ta + 8) * 32 + 8 * t);
-            kw[0][0] = x.x, kw[0][1] = x.y;
-            kw[1][0] = y.x, kw[1][1] = y.y;
-            const uint32_t b2 = *reinterpret_cast<const uint16_t*>(blk + kv_k_scales(D) + lane * 2);
-            sc[0][0] = prmt(b2, 0u, 0x4040) << 4;
-            sc[1][0] = prmt(b2, 0u, 0x4141) << 4;
-          }
-          uint32_t bias[2][KW / 2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int p = 0; p < KW / 2; ++p) {
-              // e4m3's exponent and mantissa as bf16's, rescaled by 2^120: exact
-              sc[r][p] = mul_bf16x2(sc[r][p], 0x7B807B80u);
-              bias[r][p] = mul_bf16x2(sc[r][p], 0xC308C308u);  // -136 s
-            }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[k][nt][j] = 0.f;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            uint32_t v[2][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                v[r][i] = fma_bf16x2((kw[r][w] >> (4 * i) & 0x000F000Fu) | 0x43004300u, sc[r][w / 2],
-                                     bias[r][w / 2]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(s[k][nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][nt][0],
-                       qf[2 * w][nt][1]);
-              mma_bf16(s[k][nt], v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][nt][0],
-                       qf[2 * w + 1][nt][1]);
-            }
-          }
-        }
-
-        // scores in units of log2(e); positions a column does not see
-        bool over = false;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[k][nt][j] *= a.scale_log2;
-        if (pos0 + kTile - 1 > lim_lo) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (pos0 + k * kKvBlock + ta + (j >> 1) * 8 > lim[nt][j & 1])
-                  s[k][nt][j] = -INFINITY;
-        }
+      for (int m = 0; m < KT; ++m)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float top = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]),
-                                    fmaxf(s[1][nt][j], s[1][nt][j + 2]));
-            over |= top > st.m[nt][j] + (kRef + kSlack);
-          }
-        if (__any_sync(0xffffffffu, over)) {
+          for (int j = 0; j < 4; ++j) st.o[m][nt][j] = 0.f;
+
+      const int count = static_cast<int>(min(static_cast<long long>(at.r.tiles - at.tile), w_hi - at.unit));
+      for (int i = 0; i < count; ++i) {
+        if (!dead && !mbar_wait(bar + stage, phase, a.err)) dead = true;
+        const int pos0 = (at.tile + i) * kTile;
+        if (pos0 <= lim_hi) {
+          const uint8_t* tile = my_ring + stage * kTileBytes;
+          float2 s[2][NT][2];  // [block][column tile][row g, row g + 8]
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int k = 0; k < 2; ++k) {
+            const uint8_t* blk = tile + k * kBlock;
+            uint32_t kw[2][KW], sc[2];  // sc: the row's scales as fp16
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(blk + ta * 64 + 16 * t);
+              const uint4 y = *reinterpret_cast<const uint4*>(blk + (ta + 8) * 64 + 16 * t);
+              kw[0][0] = x.x, kw[0][1] = x.y, kw[0][2] = x.z, kw[0][3] = x.w;
+              kw[1][0] = y.x, kw[1][1] = y.y, kw[1][2] = y.z, kw[1][3] = y.w;
+              const uint32_t b4 = *reinterpret_cast<const uint32_t*>(blk + kv_k_scales(D) + lane * 4);
+              sc[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b4));
+              sc[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(b4 >> 16));
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(blk + ta * 32 + 8 * t);
+              const uint2 y = *reinterpret_cast<const uint2*>(blk + (ta + 8) * 32 + 8 * t);
+              kw[0][0] = x.x, kw[0][1] = x.y;
+              kw[1][0] = y.x, kw[1][1] = y.y;
+              const uint32_t both = e4m3x2_to_f16x2(
+                  *reinterpret_cast<const uint16_t*>(blk + kv_k_scales(D) + lane * 2));
+              sc[0] = both_lo(both);
+              sc[1] = both_hi(both);
+            }
+            float acc[NT][4] = {};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]),
-                                fmaxf(s[1][nt][j], s[1][nt][j + 2]));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              const float m = fmaxf(st.m[nt][j], top - kRef);
-              const float f = ex2(st.m[nt][j] - m);
-              st.m[nt][j] = m;
-              st.l[nt][j] *= f;
+            for (int p = 0; p < KW / 2; ++p) {  // the lane's scale groups
+              Decode dec[2];
 #pragma unroll
-              for (int d = 0; d < KT; ++d) {
-                st.o[d][nt][j] *= f;
-                st.o[d][nt][j + 2] *= f;
+              for (int r = 0; r < 2; ++r)
+                dec[r] = decode_scales(D == 128 ? (p ? both_hi(sc[r]) : both_lo(sc[r])) : sc[r]);
+#pragma unroll
+              for (int w = 2 * p; w < 2 * p + 2; ++w) {
+                uint32_t v[2][4];
+                decode4(kw[0][w], dec[0], v[0]);
+                decode4(kw[1][w], dec[1], v[1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_f16(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][nt][0],
+                          qf[2 * w][nt][1]);
+                  mma_f16(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][nt][0],
+                          qf[2 * w + 1][nt][1]);
+                }
               }
             }
-        }
-
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint8_t* blk = tile + k * kBlock;
-          uint32_t pf[NT][2];
+            for (int nt = 0; nt < NT; ++nt) {
+              s[k][nt][0] = make_float2(acc[nt][0], acc[nt][1]);
+              s[k][nt][1] = make_float2(acc[nt][2], acc[nt][3]);
+            }
+          }
+
+          if (pos0 + kTile - 1 > lim_lo) {  // positions a column does not see
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int pos = pos0 + k * kKvBlock + ta + r * 8;
+                  if (pos > lim[nt][0]) s[k][nt][r].x = -INFINITY;
+                  if (pos > lim[nt][1]) s[k][nt][r].y = -INFINITY;
+                }
+          }
+          float2 top[NT];
+          bool over = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              p[j] = ex2(s[k][nt][j] - st.m[nt][j & 1]);
-              st.l[nt][j & 1] += p[j];
-            }
-            pf[nt][0] = transpose_8x8(pack_f16x2(p[0], p[1]));
-            pf[nt][1] = transpose_8x8(pack_f16x2(p[2], p[3]));
+            top[nt].x = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
+            top[nt].y = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
+            top[nt].x *= unit[nt].x;
+            top[nt].y *= unit[nt].y;
+            over |= top[nt].x > st.m[nt].x + (kRef + kSlack) || top[nt].y > st.m[nt].y + (kRef + kSlack);
           }
-          // V: lane group t's four tokens, this lane's LD dimensions
-          uint32_t vw[4][VW], vs;
+          if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int token = (tv ^ (i & 1)) | (i & 1) << 2 | (i >> 1) << 3;
-            if constexpr (D == 128) {
-              const uint2 x = *reinterpret_cast<const uint2*>(blk + kv_v_codes(D) + token * 64 +
-                                                              ((8 * g) ^ ((t >> 1) << 5)));
-              vw[i][0] = x.x, vw[i][1] = x.y;
-            } else {
-              vw[i][0] = *reinterpret_cast<const uint32_t*>(blk + kv_v_codes(D) + token * 32 + 4 * g);
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int d = 4; d <= 16; d <<= 1) {
+                top[nt].x = fmaxf(top[nt].x, __shfl_xor_sync(0xffffffffu, top[nt].x, d));
+                top[nt].y = fmaxf(top[nt].y, __shfl_xor_sync(0xffffffffu, top[nt].y, d));
+              }
+              const float2 m = make_float2(fmaxf(st.m[nt].x, top[nt].x - kRef),
+                                           fmaxf(st.m[nt].y, top[nt].y - kRef));
+              const float fx = ex2(st.m[nt].x - m.x), fy = ex2(st.m[nt].y - m.y);
+              st.m[nt] = m;
+              st.l[nt].x *= fx;
+              st.l[nt].y *= fy;
+#pragma unroll
+              for (int d = 0; d < KT; ++d) {
+                st.o[d][nt][0] *= fx;
+                st.o[d][nt][1] *= fy;
+                st.o[d][nt][2] *= fx;
+                st.o[d][nt][3] *= fy;
+              }
             }
           }
-          vs = *reinterpret_cast<const uint32_t*>(blk + kv_v_scales(D) +
-                                                  ((D == 128 ? g : g >> 1) * 4 + t) * 4);
-          uint32_t v[2][LD];  // [token pair][dimension]
+
 #pragma unroll
-          for (int pr = 0; pr < 2; ++pr) {
-            const uint32_t s0 = mul_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(vs >> (16 * pr))),
-                                          0x28002800u);        // s 2^-5
-            const uint32_t c0 = mul_f16x2(s0, 0xE408E408u);    // -1032 s 2^-5
-            const uint32_t s1 = mul_f16x2(s0, 0x2C002C00u);    // s 2^-9
-            const uint32_t c1 = mul_f16x2(s0, 0xD480D480u);    // -72 s 2^-5
+          for (int k = 0; k < 2; ++k) {
+            const uint8_t* blk = tile + k * kBlock;
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 minus = make_float2(-st.m[nt].x, -st.m[nt].y);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float2 x = fma2(s[k][nt][r], unit[nt], minus);
+                const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                st.l[nt] = add2(st.l[nt], p);
+                pf[nt][r] = transpose_8x8(pack_f16x2(p.x, p.y));
+              }
+            }
+            // V: lane group t's four tokens, this lane's LD dimensions
+            uint32_t vw[4][VW], vs;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int token = (tv ^ (r & 1)) | (r & 1) << 2 | (r >> 1) << 3;
+              if constexpr (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2*>(blk + kv_v_codes(D) + token * 64 +
+                                                                ((8 * g) ^ ((t >> 1) << 5)));
+                vw[r][0] = x.x, vw[r][1] = x.y;
+              } else {
+                vw[r][0] = *reinterpret_cast<const uint32_t*>(blk + kv_v_codes(D) + token * 32 + 4 * g);
+              }
+            }
+            vs = *reinterpret_cast<const uint32_t*>(blk + kv_v_scales(D) +
+                                                    ((D == 128 ? g : g >> 1) * 4 + t) * 4);
+            const Decode dec[2] = {
+                decode_scales(e4m3x2_to_f16x2(static_cast<uint16_t>(vs))),
+                decode_scales(e4m3x2_to_f16x2(static_cast<uint16_t>(vs >> 16)))};
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t y = prmt(vw[2 * pr][w], vw[2 * pr + 1][w], hf ? 0x7632 : 0x5410);
-                const uint32_t y8 = y >> 8;
-                uint32_t* o = v[pr] + w * 8 + hf * 4;
-                o[0] = fma_f16x2((y & 0x000F000Fu) | 0x64006400u, s0, c0);
-                o[1] = fma_f16x2((y & 0x00F000F0u) | 0x64006400u, s1, c1);
-                o[2] = fma_f16x2((y8 & 0x000F000Fu) | 0x64006400u, s0, c0);
-                o[3] = fma_f16x2((y8 & 0x00F000F0u) | 0x64006400u, s1, c1);
+              for (int hf = 0; hf < 2; ++hf) {  // 4 of the word's dimensions
+                uint32_t v[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  decode4(prmt(vw[2 * r][w], vw[2 * r + 1][w], hf ? 0x7632 : 0x5410), dec[r], v[r]);
+                const int m = w * 4 + hf * 2;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_f16(st.o[m][nt], v[0][0], v[0][1], v[1][0], v[1][1], pf[nt][0], pf[nt][1]);
+                  mma_f16(st.o[m + 1][nt], v[0][2], v[0][3], v[1][2], v[1][3], pf[nt][0], pf[nt][1]);
+                }
               }
           }
-#pragma unroll
-          for (int m = 0; m < KT; ++m)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(st.o[m][nt], v[0][2 * m], v[0][2 * m + 1], v[1][2 * m], v[1][2 * m + 1],
-                      pf[nt][0], pf[nt][1]);
         }
-      }
 
-      // the stage is free: every lane has read it
-      __syncwarp();
-      if (issued < n && !dead) {
-        in.next(a);
-        issue(issued);
-        ++issued;
+        // the stage is free: every lane has read it
+        __syncwarp();
+        if (stage == kStages - 1) {
+          stage = 0;
+          phase ^= 1;
+        } else {
+          ++stage;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (!dead) fetch();
       }
+      const bool whole = at.tile + count == at.r.tiles && group >= w_lo;
 
-      const bool group_ends = at.tile == at.r.tiles - 1;
-      if (group_ends || u == n - 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) {
+          st.l[nt].x += __shfl_xor_sync(0xffffffffu, st.l[nt].x, d);
+          st.l[nt].y += __shfl_xor_sync(0xffffffffu, st.l[nt].y, d);
+        }
+      if (whole) {
+        const float back = 32.f * a.v_scale;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float l = st.l[nt][j];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            st.l[nt][j] = l;
+            const long long off =
+                column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + 2 * t + j, a.ldo);
+            if (off < 0) continue;
+            const float l = j ? st.l[nt].y : st.l[nt].x;
+            const float f = l == 0.f ? 0.f : back / l;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
+#pragma unroll
+            for (int w = 0; w < LD / 8; ++w) {
+              uint32_t x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[i] = pack_bf16x2(st.o[4 * w + i][nt][j] * f, st.o[4 * w + i][nt][j + 2] * f);
+              dst[w] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
           }
-        if (group_ends && group >= w_lo) {
-          const float unit = 32.f * a.v_scale;
+      } else {
+        // a piece: slot 0 began before this warp's range, slot 1 goes on after it
+        const int slot = group < w_lo ? 0 : 1;
+        float* piece = warp_pieces + slot * piece_floats<D, NT>();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const long long off =
-                  column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + 2 * t + j, a.ldo);
-              if (off < 0) continue;
-              const float f = st.l[nt][j] == 0.f ? 0.f : unit / st.l[nt][j];
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
-#pragma unroll
-              for (int w = 0; w < LD / 8; ++w) {
-                uint32_t x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  x[i] = pack_bf16x2(st.o[4 * w + i][nt][j] * f, st.o[4 * w + i][nt][j + 2] * f);
-                dst[w] = make_uint4(x[0], x[1], x[2], x[3]);
-              }
+          for (int j = 0; j < 2; ++j) {
+            const int c = nt * 8 + 2 * t + j;
+            if (g == 0) {
+              piece[c] = j ? st.m[nt].y : st.m[nt].x;
+              piece[8 * NT + c] = j ? st.l[nt].y : st.l[nt].x;
             }
-        } else {
-          // a piece: slot 0 began before this warp's range, slot 1 goes on after it
-          const int slot = group < w_lo ? 0 : 1;
-          float* piece = warp_pieces + slot * piece_floats<D, NT>();
+            float* o = piece + 16 * NT + c * D + g * LD;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int c = nt * 8 + 2 * t + j;
-              if (g == 0) {
-                piece[c] = st.m[nt][j];
-                piece[8 * NT + c] = st.l[nt][j];
-              }
-              float* o = piece + 16 * NT + c * D + g * LD;
-#pragma unroll
-              for (int m = 0; m < KT; m += 2)
-                *reinterpret_cast<float4*>(o + 2 * m) =
-                    make_float4(st.o[m][nt][j], st.o[m][nt][j + 2], st.o[m + 1][nt][j],
-                                st.o[m + 1][nt][j + 2]);
-            }
-          if (lane == 0) info[warp * 2 + slot] = PieceInfo{group, at.r.tiles, at.b, at.head, at.col};
-        }
+            for (int m = 0; m < KT; m += 2)
+              *reinterpret_cast<float4*>(o + 2 * m) =
+                  make_float4(st.o[m][nt][j], st.o[m][nt][j + 2], st.o[m + 1][nt][j],
+                              st.o[m + 1][nt][j + 2]);
+          }
+        if (lane == 0)
+          info[warp * 2 + slot] =
+              PieceInfo{group, at.r.tiles, min(8 * NT, at.r.q_len * G - at.col * 8 * NT), at.r.row0,
+                        at.head, at.col * 8 * NT};
       }
-      if (u + 1 < n && at.next(a)) {
-        fresh = true;
-        group = w_lo + u + 1;
-      }
+      if (at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi) break;
+      at.next_group(a);
     }
     if (dead)  // copies still in flight write this CTA's shared memory: let them land
-      for (int i = 0; i < kStages; ++i) mbar_wait(bar + i, ((issued - 1) / kStages) & 1, a.err);
+      for (int i = 0; i < kStages; ++i) mbar_wait(bar + i, phase, a.err);
   }
   __syncthreads();
 
-  // Join the pieces, in the order of the sequence.  dst: the CTA's piece (then O, m and l), or
-  // the output.
-  auto join = [&](auto piece_of, int n, const PieceInfo& gi, float* dst) {
-    Request r = load_request<NT>(a, gi.b, false);
-    const float unit = 32.f * a.v_scale;
-    for (int e = tid; e < 8 * NT * (D / 4); e += kThreads) {
-      const int c = e / (D / 4), d = e % (D / 4) * 4;
-      const long long off = column_offset<NT>(a, r, gi.head, gi.col, c, a.ldo);
-      if (off < 0) continue;
-      float m = kNone;
-      for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(piece_of(i) + c));
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < n; ++i) {
-        const float* p = piece_of(i);
-        const float f = ex2(__ldcg(p + c) - m);
-        l += f * __ldcg(p + 8 * NT + c);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 16 * NT + c * D + d));
-        o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+  // Join column c of n pieces, in the order of the sequence, into dst (a piece) or the output:
+  // one warp, the weights 2^(m_i - max m) one piece a lane, then the weighted sum, whose loads
+  // do not wait for one another.
+  constexpr int NC = 8 * NT, kPiece = piece_floats<D, NT>(), VL = D / 32;
+  const auto join_column = [&](auto piece_of, int n, const PieceInfo& gi, int c, float* dst) {
+    float m = kNone;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(piece_of(i) + c));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f, o[VL] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < n) {
+        const float* p = piece_of(i0 + lane);
+        f = ex2(__ldcg(p + c) - m);
+        l += f * __ldcg(p + NC + c);
       }
-      if (dst) {
-        if (d == 0) {
-          dst[c] = m;
-          dst[8 * NT + c] = l;
+      const int some = min(32, n - i0);
+#pragma unroll 8
+      for (int k = 0; k < some; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k);
+        const float* p = piece_of(i0 + k) + 2 * NC + c * D + lane * VL;
+        if constexpr (VL == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+          o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+          o[0] += w * x.x, o[1] += w * x.y;
         }
-        *reinterpret_cast<float4*>(dst + 16 * NT + c * D + d) = o;
-      } else {
-        const float f = l == 0.f ? 0.f : unit / l;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off + d) =
-            make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
       }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (dst) {
+      if (lane == 0) {
+        dst[c] = m;
+        dst[NC + c] = l;
+      }
+#pragma unroll
+      for (int i = 0; i < VL; i += 2)
+        *reinterpret_cast<float2*>(dst + 2 * NC + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
+    } else {
+      const int G = a.q_heads / heads, token = (gi.first_col + c) / G;
+      const float f = l == 0.f ? 0.f : 32.f * a.v_scale / l;
+      uint32_t* out = reinterpret_cast<uint32_t*>(
+          static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(gi.row0 + token) * a.ldo +
+          (gi.head * G + gi.first_col + c - token * G) * D + lane * VL);
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) out[i / 2] = pack_bf16x2(o[i] * f, o[i + 1] * f);
+    }
   };
-  constexpr int kPiece = piece_floats<D, NT>();
+  // The groups that several warps share, their columns dealt to the warps.  Those that other
+  // CTAs share too become pieces of this CTA: 0 began before it, 1 goes on after it.
   float* const cta_warp_pieces = a.pieces + static_cast<size_t>(gridDim.x) * 2 * kPiece +
                                  static_cast<size_t>(blockIdx.x) * kWarps * 2 * kPiece;
+  int shared_group[2] = {-1, -1}, item = 0;
   for (int i = 0; i < kWarps * 2;) {
-    const PieceInfo gi = info[i];
-    if (gi.group < 0) {
+    if (info[i].group < 0) {
       ++i;
       continue;
     }
-    int idx[kWarps * 2], n = 0, j = i;
-    for (; j < kWarps * 2; ++j) {
-      if (info[j].group < 0) continue;
-      if (info[j].group != gi.group) break;
-      idx[n++] = j;
+    // its pieces: slot 0 or 1 of this warp, and slot 0 of the warps after it
+    const PieceInfo gi = info[i];
+    const int piece0 = i;
+    int n = 1;
+    while ((piece0 & ~1) + 2 * n < kWarps * 2 && info[(piece0 & ~1) + 2 * n].group == gi.group) ++n;
+    i = (n == 1 ? piece0 : (piece0 & ~1) + 2 * (n - 1)) + 1;
+    float* dst = nullptr;
+    if (gi.group < cta_lo || gi.group + gi.tiles > cta_hi) {
+      const int k = gi.group < cta_lo ? 0 : 1;
+      shared_group[k] = piece0;
+      dst = a.pieces + static_cast<size_t>(blockIdx.x * 2 + k) * kPiece;
     }
-    i = j;
-    const auto warp_piece = [&](int k) { return cta_warp_pieces + idx[k] * kPiece; };
-    const long long end = gi.group + gi.tiles;
-    if (gi.group >= cta_lo && end <= cta_hi) {
-      join(warp_piece, n, gi, nullptr);
-      continue;
-    }
-    const int first = static_cast<int>(gi.group / span), last = static_cast<int>((end - 1) / span);
-    join(warp_piece, n, gi, a.pieces + (blockIdx.x * 2 + (gi.group < cta_lo ? 0 : 1)) * static_cast<size_t>(kPiece));
+    for (int c = 0; c < gi.cols; ++c, ++item)
+      if (item % kWarps == warp)
+        join_column([&](int k) { return cta_warp_pieces + (k == 0 ? piece0 : (piece0 & ~1) + 2 * k) * kPiece; },
+                    n, gi, c, dst);
+  }
+  if (shared_group[0] < 0 && shared_group[1] < 0) return;
+  // The last CTA to arrive joins the CTAs' pieces: the first CTA's piece 1, then pieces 0.
+  __threadfence();
+  __syncthreads();
+  if (tid < 2 && shared_group[tid] >= 0) {
+    const PieceInfo gi = info[shared_group[tid]];
+    const int first = static_cast<int>(quotient(gi.group, span));
+    const int others = static_cast<int>(quotient(gi.group + gi.tiles - 1, span)) - first;
+    last_cta[tid] = atomicAdd(a.arrivals + first, 1) == others;
+    if (last_cta[tid]) a.arrivals[first] = 0;
     __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      const int seen = atomicAdd(a.arrivals + first, 1);
-      last_cta = seen == last - first;
-      if (last_cta) a.arrivals[first] = 0;
-      __threadfence();
-    }
-    __syncthreads();
-    if (last_cta)
-      join([&](int k) { return a.pieces + (k == 0 ? first * 2 + 1 : (first + k) * 2) * static_cast<size_t>(kPiece); },
-           last - first + 1, gi, nullptr);
-    __syncthreads();
+  }
+  __syncthreads();
+  item = 0;
+  for (int k = 0; k < 2; ++k) {
+    if (shared_group[k] < 0 || !last_cta[k]) continue;
+    const PieceInfo gi = info[shared_group[k]];
+    const int first = static_cast<int>(quotient(gi.group, span));
+    const int n = static_cast<int>(quotient(gi.group + gi.tiles - 1, span)) - first + 1;
+    for (int c = 0; c < gi.cols; ++c, ++item)
+      if (item % kWarps == warp)
+        join_column([&](int x) { return a.pieces + static_cast<size_t>(x == 0 ? first * 2 + 1 : (first + x) * 2) * kPiece; },
+                    n, gi, c, nullptr);
   }
 }
 

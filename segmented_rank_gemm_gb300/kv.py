@@ -15,6 +15,7 @@ import torch
 from .lora import LORA_EINVAL, LoraError, _stream, library
 
 _lib = library()
+_I32, _BF16 = torch.int32, torch.bfloat16
 
 
 def _bad(what: str):
@@ -23,14 +24,14 @@ def _bad(what: str):
 
 def _i32(name: str, t, n: int) -> int:
     """The address of a contiguous CUDA int32 tensor of at least n elements."""
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
         _bad("%s must be a contiguous CUDA int32 tensor of at least %d elements" % (name, n))
     return t.data_ptr()
 
 
 def _rows(name: str, t, shape) -> int:
     """The row distance of a CUDA bf16 tensor [T, heads, dim] whose rows are dense."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != shape:
+    if t.dtype is not _BF16 or not t.is_cuda or t.shape != shape:
         _bad("%s must be a CUDA bf16 tensor of shape %s, not %s %s" % (name, shape, t.dtype,
                                                                      tuple(t.shape)))
     row, head, one = t.stride()

@@ -153,8 +153,15 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
+# The current stream's handle without a torch.cuda.Stream object around it (0.4 us a call on a
+# Grace host, where building the object takes 3 us: as long as a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

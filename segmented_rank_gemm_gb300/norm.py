@@ -14,19 +14,19 @@ def _bad(what: str):
     raise LoraError(LORA_EINVAL, what)
 
 
-def _rows(name: str, t, like) -> int:
-    """The row distance of a CUDA tensor of the shape and type of ``like``."""
-    if t.dtype != like.dtype or not t.is_cuda or t.shape != like.shape:
+def _rows(name: str, t, dtype, shape) -> int:
+    """The row distance of a CUDA tensor [T, K] whose rows are dense."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
         _bad("%s must be a CUDA tensor of x's type and shape" % name)
     row, one = t.stride()
-    T, K = t.shape
+    T, K = shape
     if K > 1 and one != 1:
         _bad("%s: the elements of a row must be dense" % name)
     return row if T > 1 else max(row, K)  # one row has no distance
 
 
 def _dense(name: str, t, dtype, shape) -> int:
-    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
         _bad("%s must be a contiguous CUDA tensor %s of %s" % (name, shape, dtype))
     return t.data_ptr()
 
@@ -36,18 +36,19 @@ def lora_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, xq=N
     """h = x + residual; y = h rsqrt(mean(h^2) + eps) weight over the rows of x [T, K] (bf16 or
     fp32).  Outputs, each optional: ``residual_out`` (h; may be ``residual``), ``y``, and
     ``xq`` (float8_e4m3fn) with its row scales ``sx`` [T] (fp32)."""
-    if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda:
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or dtype not in _DTYPES:
         _bad("x must be a CUDA tensor [T, K] of bf16 or fp32")
-    T, K = x.shape
-    ldx = _rows("x", x, x)
-    ldr = _rows("residual", residual, x) if residual is not None else 0
-    ldh = _rows("residual_out", residual_out, x) if residual_out is not None else 0
+    T, K = shape
+    ldx = _rows("x", x, dtype, shape)
+    ldr = _rows("residual", residual, dtype, shape) if residual is not None else 0
+    ldh = _rows("residual_out", residual_out, dtype, shape) if residual_out is not None else 0
     rc = _lib.lora_rms_norm(
         x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
-        _dense("weight", weight, x.dtype, (K,)), eps, T, K, _DTYPES[x.dtype],
+        _dense("weight", weight, dtype, (K,)), eps, T, K, _DTYPES[dtype],
         None if residual_out is None else residual_out.data_ptr(), ldh,
-        None if y is None else _dense("y", y, x.dtype, (T, K)),
-        None if xq is None else _dense("xq", xq, torch.float8_e4m3fn, (T, K)),
+        None if y is None else _dense("y", y, dtype, shape),
+        None if xq is None else _dense("xq", xq, torch.float8_e4m3fn, shape),
         None if sx is None else _dense("sx", sx, torch.float32, (T,)), _stream(stream))
     if rc < 0:
         raise LoraError(rc, "lora_rms_norm")
