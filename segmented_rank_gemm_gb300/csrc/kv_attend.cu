@@ -21,11 +21,6 @@
 // with the reference at 2^6 it is a normal number down to 2^-20 of the maximum) while l sums
 // the fp32 p.
 //
-// Decoding, per pair of 4-bit codes n in two halves of a register: n OR the bits of 1024 gives
-// 1024 + n (1024 + 16 n for the next code up), and one fused multiply-add
-// (1024 + n) s - 1032 s = (n - 8) s, exact because 1032 s = 8 129 s has at most 11 significant
-// bits.  One shift serves the two other codes of a half: 9 instructions for 8 codes.
-//
 // Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs
 // and those into equal ranges for their warps, so that one long request fills the GPU and many
 // short ones balance.  A group counts kSetup units besides its tiles, about what its queries'
@@ -40,6 +35,7 @@
 
 #include <algorithm>
 
+#include "kv_decode.cuh"
 #include "kv_kernels.h"
 #include "lora_common.cuh"
 #include "lora_kernels.h"
@@ -58,88 +54,9 @@ constexpr float kRef = 6.f;    // p is 2^kRef at the reference
 constexpr float kSlack = 8.f;  // how far (in powers of two) a score may exceed the reference
 constexpr float kNone = -1.7e38f;
 
-// ---- small instructions ----
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-// (a & mask) | bits, one instruction (written out: two immediates are else split in two).
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
-  return r;
-}
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Each half of v twice.
-__device__ __forceinline__ uint32_t both_lo(uint32_t v) { return prmt(v, v, 0x1010); }
-__device__ __forceinline__ uint32_t both_hi(uint32_t v) { return prmt(v, v, 0x3232); }
-// a * b + c of two floats at once.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-// The scales of 4-bit codes, for a pair's low (s0, c0) and next (s1, c1) codes.
-struct Decode {
-  uint32_t s0, c0, s1, c1;
-};
-__device__ __forceinline__ Decode decode_scales(uint32_t s) {  // two e4m3 values as fp16
-  Decode d;
-  d.s0 = mul_f16x2(s, 0x28002800u);     // s 2^-5
-  d.c0 = mul_f16x2(d.s0, 0xE408E408u);  // -1032 s 2^-5
-  d.s1 = mul_f16x2(d.s0, 0x2C002C00u);  // s 2^-9
-  d.c1 = mul_f16x2(d.s0, 0xD480D480u);  // -72 s 2^-5
-  return d;
-}
-// The four pairs of codes of y: nibbles i of both halves.
-__device__ __forceinline__ void decode4(uint32_t y, const Decode& d, uint32_t (&o)[4]) {
-  const uint32_t y8 = y >> 8;
-  o[0] = fma_f16x2(and_or(y, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
-  o[1] = fma_f16x2(and_or(y, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
-  o[2] = fma_f16x2(and_or(y8, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
-  o[3] = fma_f16x2(and_or(y8, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
-}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -150,12 +67,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// a / b of non-negative values, in 32 bits where they fit (a 64-bit division takes longer than a
-// load from L2).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
 
 // ---- requests, groups and the sequence of tiles ----
 struct Request {
@@ -183,7 +94,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
   const int G = a.q_heads / a.pages.heads;
   r.tiles = max(1, (r.kv + kTile - 1) / kTile);
-  r.col_tiles = (r.q_len * G + 8 * NT - 1) / (8 * NT);
+  r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + 8 * NT - 1) / (8 * NT);
   return r;
 }
 
@@ -455,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         }
         // (never 0, so that a masked score stays -inf)
         const float down =
-            fmaxf(32.f * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
+            fmaxf(kKvUnit * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
         unit[nt].x = __shfl_sync(0xffffffffu, down, 8 * t);
         unit[nt].y = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
@@ -652,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
           st.l[nt].y += __shfl_xor_sync(0xffffffffu, st.l[nt].y, d);
         }
       if (whole) {
-        const float back = 32.f * a.v_scale;
+        const float back = kKvUnit * a.v_scale;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -748,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         *reinterpret_cast<float2*>(dst + 2 * NC + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.q_heads / heads, token = (gi.first_col + c) / G;
-      const float f = l == 0.f ? 0.f : 32.f * a.v_scale / l;
+      const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
       uint32_t* out = reinterpret_cast<uint32_t*>(
           static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(gi.row0 + token) * a.ldo +
           (gi.head * G + gi.first_col + c - token * G) * D + lane * VL);

@@ -127,7 +127,8 @@ struct lora_kv_cache {
   int max_requests = 0, device = 0, num_sms = 0;
   float k_scale = 1.f, v_scale = 1.f;
   float* pieces = nullptr;      // attention's partial results
-  int32_t* arrivals = nullptr;  // attention's arrival counts (zero between calls)
+  float* prompt_pieces = nullptr;
+  int32_t* arrivals = nullptr;  // attention's arrival counts, both kernels' (zero between calls)
   int32_t* err = nullptr;
   char last_error[256] = "";
 };
@@ -136,6 +137,9 @@ namespace {
 
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxRequests = 16384;
+// Rows a cache head (query rows times q_heads / kv_heads) up to which a request's attention runs
+// in the kernel for few rows.
+constexpr int kFewRows = 16;
 
 int fail(lora_kv_cache* c, int code, const char* fmt, ...) {
   if (c) {
@@ -154,7 +158,7 @@ int fail(lora_kv_cache* c, int code, const char* fmt, ...) {
   } while (0)
 
 void free_all(lora_kv_cache* c) {
-  void* ptrs[] = {c->pages.base, c->pieces, c->arrivals, c->err};
+  void* ptrs[] = {c->pages.base, c->pieces, c->prompt_pieces, c->arrivals, c->err};
   for (void* p : ptrs)
     if (p) cudaFree(p);
 }
@@ -194,12 +198,14 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
   int rc = LORA_OK;
   if (cudaMalloc(&c->pages.base, c->bytes) != cudaSuccess ||
       cudaMalloc(&c->pieces, floats * sizeof(float)) != cudaSuccess ||
-      cudaMalloc(&c->arrivals, kKvMaxCtas * sizeof(int32_t)) != cudaSuccess ||
+      cudaMalloc(&c->prompt_pieces, kv_prompt_workspace_floats(c->num_sms, head_dim) *
+                                        sizeof(float)) != cudaSuccess ||
+      cudaMalloc(&c->arrivals, 2 * kKvMaxCtas * sizeof(int32_t)) != cudaSuccess ||
       cudaMalloc(&c->err, sizeof(int32_t)) != cudaSuccess) {
     cudaGetLastError();
     rc = LORA_ENOMEM;
   } else if (cudaMemsetAsync(c->pages.base, 0, c->bytes, stream) != cudaSuccess ||
-             cudaMemsetAsync(c->arrivals, 0, kKvMaxCtas * sizeof(int32_t), stream) != cudaSuccess ||
+             cudaMemsetAsync(c->arrivals, 0, 2 * kKvMaxCtas * sizeof(int32_t), stream) != cudaSuccess ||
              cudaMemsetAsync(c->err, 0, sizeof(int32_t), stream) != cudaSuccess ||
              cudaStreamSynchronize(stream) != cudaSuccess) {
     rc = LORA_ECUDA;
@@ -290,9 +296,14 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.ldo = ldo;
   a.pieces = c->pieces;
   a.arrivals = c->arrivals;
+  a.few_rows = kFewRows;
+  a.prompt_pieces = c->prompt_pieces;
+  a.prompt_arrivals = c->arrivals + kKvMaxCtas;
   a.err = c->err;
   a.num_sms = c->num_sms;
   KV_CUDA(c, launch_kv_attend(a, static_cast<cudaStream_t>(stream)));
+  if (static_cast<long long>(max_q) * (q_heads / heads) > kFewRows)
+    KV_CUDA(c, launch_kv_prompt(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;
 }
 

@@ -1,0 +1,104 @@
+// kv_decode.cuh -- the 4-bit cache's values in registers, and the small instructions the
+// attention kernels share.
+//
+// Decoding, per pair of 4-bit codes n in two halves of a register: n OR the bits of 1024 gives
+// 1024 + n (1024 + 16 n for the next code up), and one fused multiply-add
+// (1024 + n) s - 1032 s = (n - 8) s, exact in fp16 because 1032 s = 8 129 s has at most 11
+// significant bits.  One shift serves the two other codes of a half: 9 instructions for 8 codes.
+// Values are scaled by 2^-5, which keeps 1032 s within fp16 (s <= 448) and n s exact (s is a
+// multiple of 2^-9).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lora {
+
+constexpr float kKvUnit = 32.f;  // decoded values times this are the cache's (before its scale)
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// (a & mask) | bits, one instruction (written out: two immediates are else split in two).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Each half of v twice.
+__device__ __forceinline__ uint32_t both_lo(uint32_t v) { return prmt(v, v, 0x1010); }
+__device__ __forceinline__ uint32_t both_hi(uint32_t v) { return prmt(v, v, 0x3232); }
+// a * b + c of two floats at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// The scales of 4-bit codes, for a pair's low (s0, c0) and next (s1, c1) codes.
+struct Decode {
+  uint32_t s0, c0, s1, c1;
+};
+__device__ __forceinline__ Decode decode_scales(uint32_t s) {  // two e4m3 values as fp16
+  Decode d;
+  d.s0 = mul_f16x2(s, 0x28002800u);     // s 2^-5
+  d.c0 = mul_f16x2(d.s0, 0xE408E408u);  // -1032 s 2^-5
+  d.s1 = mul_f16x2(d.s0, 0x2C002C00u);  // s 2^-9
+  d.c1 = mul_f16x2(d.s0, 0xD480D480u);  // -72 s 2^-5
+  return d;
+}
+// The four pairs of codes of y: nibbles i of both halves.
+__device__ __forceinline__ void decode4(uint32_t y, const Decode& d, uint32_t (&o)[4]) {
+  const uint32_t y8 = y >> 8;
+  o[0] = fma_f16x2(and_or(y, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
+  o[1] = fma_f16x2(and_or(y, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
+  o[2] = fma_f16x2(and_or(y8, 0x000F000Fu, 0x64006400u), d.s0, d.c0);
+  o[3] = fma_f16x2(and_or(y8, 0x00F000F0u, 0x64006400u), d.s1, d.c1);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// a / b of non-negative values, in 32 bits where they fit (a 64-bit division takes longer than a
+// load from L2).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+}  // namespace lora

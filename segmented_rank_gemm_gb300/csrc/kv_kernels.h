@@ -1,5 +1,5 @@
 // kv_kernels.h -- the 4-bit cache's layout in memory and the launchers of its kernels
-// (kv_cache.cu: the object, append and read; kv_attend.cu: attention).
+// (kv_cache.cu: the object, append and read; kv_attend.cu and kv_prompt.cu: attention).
 //
 // Pages hold blocks of 16 tokens of one head:
 //     page -> head -> block of 16 positions -> { K codes | K scales | V codes | V scales }
@@ -88,6 +88,10 @@ struct KvAttendArgs {
   int ldo;
   float* pieces;      // partial results of a group that several warps or CTAs share
   int32_t* arrivals;  // [kKvMaxCtas] CTAs done with the group that starts in a CTA (zeroed)
+  // Requests with more rows a cache head than this go to the kernel for many rows.
+  int few_rows;
+  float* prompt_pieces;      // that kernel's workspaces
+  int32_t* prompt_arrivals;  // [kKvMaxCtas] (zeroed)
   int32_t* err;
   int num_sms;
 };
@@ -96,5 +100,8 @@ constexpr int kKvMaxCtas = 1024;
 // Floats of the partial results' workspace.
 size_t kv_attend_workspace_floats(int num_sms, int D);
 cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream);
+// The kernel for requests of many rows (kv_prompt.cu); it leaves the other rows alone.
+size_t kv_prompt_workspace_floats(int num_sms, int D);
+cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream);
 
 }  // namespace lora
