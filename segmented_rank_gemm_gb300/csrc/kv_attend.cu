@@ -92,7 +92,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
     r.kv = min(max(r.kv, 0), cap);
   }
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
-  const int G = a.q_heads / a.pages.heads;
+  const int G = a.group;
   r.tiles = max(1, (r.kv + kTile - 1) / kTile);
   r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + 8 * NT - 1) / (8 * NT);
   return r;
@@ -160,10 +160,10 @@ struct State {
 template <int NT>
 __device__ __forceinline__ long long column_offset(const KvAttendArgs& a, const Request& r, int head,
                                                    int col_tile, int c, int ld) {
-  const int G = a.q_heads / a.pages.heads;
+  const int G = a.group;
   const int col = col_tile * 8 * NT + c;
   if (col >= r.q_len * G) return -1;
-  const int token = col / G;
+  const int token = a.token_of(col);
   return static_cast<long long>(r.row0 + token) * ld +
          static_cast<long long>(head * G + (col - token * G)) * a.pages.D;
 }
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     State<D, NT> st;
     const int ta = kv_frag_token(g);  // tokens of fragment rows g and g + 8: ta, ta + 8
     const int tv = (t & 1) | (t >> 1) << 1;
-    const int G = a.q_heads / heads;
+    const int G = a.group;
     int stage = 0, phase = 0;
 
     while (at.unit < w_hi) {
@@ -373,14 +373,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         for (int j = 0; j < 2; ++j) {
           // (a column past the last has zero queries and is not written: any limit does)
           const int c = at.col * 8 * NT + nt * 8 + 2 * t + j;
-          lim[nt][j] = at.r.kv - at.r.q_len + min(c / G, at.r.q_len - 1);
+          lim[nt][j] = at.r.kv - at.r.q_len + min(a.token_of(c), at.r.q_len - 1);
         }
         st.m[nt] = make_float2(kNone, kNone);
         st.l[nt] = make_float2(0.f, 0.f);
       }
-      const int lim_lo = at.r.kv - at.r.q_len + at.col * 8 * NT / G;
+      const int lim_lo = at.r.kv - at.r.q_len + a.token_of(at.col * 8 * NT);
       const int lim_hi =
-          at.r.kv - at.r.q_len + min(at.r.q_len * G - 1, at.col * 8 * NT + 8 * NT - 1) / G;
+          at.r.kv - at.r.q_len + a.token_of(min(at.r.q_len * G - 1, at.col * 8 * NT + 8 * NT - 1));
 #pragma unroll
       for (int m = 0; m < KT; ++m)
 #pragma unroll
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       for (int i = 0; i < VL; i += 2)
         *reinterpret_cast<float2*>(dst + 2 * NC + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
-      const int G = a.q_heads / heads, token = (gi.first_col + c) / G;
+      const int G = a.group, token = a.token_of(gi.first_col + c);
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
       uint32_t* out = reinterpret_cast<uint32_t*>(
           static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(gi.row0 + token) * a.ldo +

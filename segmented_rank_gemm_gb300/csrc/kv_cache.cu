@@ -290,6 +290,8 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.B = B;
   a.T = T;
   a.max_q = max_q;
+  a.group = q_heads / heads;
+  a.group_magic = static_cast<uint32_t>((1ull << 32) / a.group + 1);
   a.scale_log2 = scale * c->k_scale * 1.44269504088896341f;
   a.v_scale = c->v_scale;
   a.out = out;

@@ -82,6 +82,12 @@ struct KvAttendArgs {
   int ldq, q_heads;
   const int32_t *q_offsets, *kv_len, *table;
   int max_blocks, B, T, max_q;
+  int group;             // q_heads / kv_heads
+  uint32_t group_magic;  // floor(2^32 / group) + 1 (unused for 1)
+  // c / group of a row c < 2^26: c (magic group - 2^32) < 2^32 as magic group - 2^32 <= group <= 64.
+  __device__ __forceinline__ int token_of(int c) const {
+    return group == 1 ? c : static_cast<int>(__umulhi(static_cast<uint32_t>(c), group_magic));
+  }
   float scale_log2;  // softmax scale times k_scale times log2(e)
   float v_scale;
   void* out;
