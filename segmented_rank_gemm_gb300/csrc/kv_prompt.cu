@@ -6,22 +6,25 @@
 // half of 128 rows,
 //     S = Q K^T,   P = 2^(S unit - m),   l += sum P,   O += P V
 // with a running reference m per row that moves only when a score exceeds it by 2^8 (O / l does
-// not depend on m), fp16 operands and fp32 accumulators.  As in the kernel for few rows,
-// decoded K and V are exact in fp16, queries are scaled by a power of two a row, and P is rounded
-// to fp16 under a sum of its fp32 values.
+// not depend on m) and fp32 accumulators.  K is decoded to bf16 and V to fp16, both exactly; the
+// queries stay as they came, in bf16, and P is rounded to fp16 under a sum of its fp32 values.
 //
-// Bound: the tensor cores, 4 D operations a score.  One CTA per SM, its warps in four roles:
+// Bound: the tensor cores, 4 D operations a score.  One CTA per SM, its warps in roles that meet
+// at barriers in shared memory:
 //   warps 0-3, 4-7   softmax of the rows 0..127 and 128..255, one row a thread: S from tensor
 //                    memory, P back to it (the PV product takes P from there), O at the end
 //   warps 8-11       decode a tile's K and V to shared memory in the 128-byte swizzled K-major
 //                    layout (V transposed: its 8 x 8 blocks are transposed while they are decoded, by
-//                    pairing two tokens' codes before they are extracted)
-//   warps 12, 13     issue the products of a half each: PV and the next QK of one half run while
-//                    the other half's softmax does
-//   warp 14          fetches packed tiles by bulk copies, kRaw tiles ahead
-// 256 rows share one decoding.  Tensor memory holds S of two tiles and O of both halves
-// (2 x 2 x 64 + 2 x 128 columns at D = 128), so that the softmax finds the next S done; P takes
-// the first columns of its S, and the next S but one waits for the product that reads it.
+//                    pairing two tokens' codes before they are extracted), and load the queries
+//   warps 12, 13     issue the PV products of a half each
+//   warp 14          issues the QK products, the halves in turn
+//   warp 15          walks the CTA's work, announces it to the others a segment at a time, and fetches
+//                    packed tiles by bulk copies, kRaw tiles ahead
+// 256 rows share one decoding.  Tensor memory holds three tiles of S (the halves take them in turn),
+// P and O of both halves: 192 + 64 + 256 columns at D = 128.  What costs time here are the hops
+// between roles, 300 to 500 cycles each from a commit to the waiting thread's next instruction: a
+// product takes 256 (PV) or 384 (QK).  With three S, the next one is under way when a softmax has
+// read its own, and with P beside S rather than in its place no QK waits for a PV.
 //
 // Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs; a cut
 // within kSnap of a group's edge (in parts of a range) moves there.  A group that is still cut
@@ -51,18 +54,50 @@ constexpr float kSlack = 8.f;   // how far (in powers of two) a score may exceed
 constexpr float kNone = -1.7e38f;
 constexpr int kTmemCols = 512;
 
-// Instruction descriptor, kind::f16: D fp32, A and B fp16, both K-major.
+// Instruction descriptor, kind::f16: D fp32, A and B fp16 (idesc_bf16_f32: bf16), both K-major.
 constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16.
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// Products and commits for a whole warp to call, in convergent code, with `leader` set in one lane,
+// which issues: descriptors then stay in uniform registers (a branch around them would cost a
+// move to one for every operand of every product).
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t one;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one;
+}
+// D[tmem] (+)= A * B[smem]^T, kind::f16, A in shared memory (descriptor) or tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -75,6 +110,21 @@ __device__ __forceinline__ void setmaxnreg_inc() {
 template <int N>
 __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Whether a barrier's phase is complete, without waiting.  A wait, even for a phase long complete,
+// takes about 160 cycles from its instruction to the branch on its result; asked for ahead of
+// other work, the answer costs nothing.
+__device__ __forceinline__ uint32_t mbar_peek(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
 }
 
 // ---- requests, groups and the sequence of tiles ----
@@ -176,8 +226,8 @@ struct Cursor {
   }
 };
 
-// A CTA's range of the sequence, walked by every role alike, a segment (one group's tiles
-// tile .. tile + count - 1) at a time.
+// A CTA's range of the sequence, walked a segment (one group's tiles tile .. tile + count - 1) at a
+// time.
 struct Walk {
   Cursor at;
   long long end;
@@ -197,10 +247,18 @@ struct Walk {
     count = static_cast<int>(min(static_cast<long long>(at.tiles), end - at.unit));
     return true;
   }
-  // Half 1 has rows.
-  __device__ __forceinline__ bool second_half() const {
-    return at.r.rows - at.part * kRows > kRows / 2;
-  }
+};
+// A segment as the roles see it.
+struct Segment {
+  int count;      // tiles; 0: there is no more
+  int tile;       // the first, in the group
+  int tiles;      // of the group
+  int rows;       // of the group, at most 256
+  int first_row;  // its first row in the request
+  int row0;       // the request's first row in q and out
+  int see;        // token t of the request sees positions 0 .. see + t
+  int head;
+  long long unit;  // of the group's first tile
 };
 
 // Floats of a piece: m, l [256], O [256][D].
@@ -219,50 +277,54 @@ struct Smem {
   static constexpr int kScratch = kRaws + kRaw * kRawTile;
   static constexpr int kBytes = kScratch + 8 * 2048 + 1024;  // + alignment
 };
+constexpr int kSegments = 4;       // announced ahead
+constexpr int kSegmentReaders = 15;  // warps
+
+// The barriers; [phase] of a ring or of a half's tiles.  (arrivals)
+struct Barriers {
+  uint64_t seg_full[kSegments], seg_empty[kSegments];  // (1) (kSegmentReaders)
+  uint64_t raw_full[kRaw], raw_empty[kRaw];            // (bytes) (128)
+  uint64_t k_full[kStages], k_empty[kStages];          // (128) (commit)
+  uint64_t v_full[kStages], v_empty[kStages];          // (128) (2: a commit a half)
+  uint64_t q_full[2], q_free;                          // (128) (commit of a segment's last QK)
+  // S: full by a half's own tiles (a half without rows in a segment would lose count of a place's
+  // phases), of which up to three are ahead of its softmax; read by place.
+  uint64_t s_full[2][3], s_read[3];                    // (commit) (128)
+  uint64_t p_full[2], pv_done[2];                      // (128) (commit)
+  uint64_t meet, idle[3];                              // (256) (commit)
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) {
   using L = Smem<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* const sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
-  // The barriers of a half's tiles alternate: a wait is then for the barrier's latest phase or the
-  // one under way, never two phases back.
-  __shared__ uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2];  // [half][tile parity]
-  __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw];
-  __shared__ uint64_t idle[2], meet;
+  __shared__ Barriers bar;
+  __shared__ Segment segments[kSegments];
   __shared__ uint32_t tmem_holder;
   __shared__ long long scan[kThreads / 32], cut_rem[2];
-  __shared__ float row_unit[kRows];  // a row's factor from products to scores in units of log2(e)
   __shared__ int cut_b[2];
-  __shared__ Cursor cuts[2];
   __shared__ int last_cta;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.pages.heads, G = a.group;
 
+  if (warp == 12) tmem_alloc(&tmem_holder, kTmemCols);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(&pv_done[i][k], 1);
-        mbar_init(&s_full[i][k], 1);
-        mbar_init(&p_full[i][k], 128);
-      }
-    }
+    for (int i = 0; i < kSegments; ++i) mbar_init(&bar.seg_full[i], 1), mbar_init(&bar.seg_empty[i], kSegmentReaders);
+    for (int i = 0; i < kRaw; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 128);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&k_empty[i], 2);
-      mbar_init(&v_full[i], 128);
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&bar.k_full[i], 128), mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 128), mbar_init(&bar.v_empty[i], 2);
     }
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 128);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(&bar.q_full[i], 128), mbar_init(&bar.p_full[i], 128), mbar_init(&bar.pv_done[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bar.s_full[0][i], 1), mbar_init(&bar.s_full[1][i], 1);
+      mbar_init(&bar.s_read[i], 128), mbar_init(&bar.idle[i], 1);
     }
-    mbar_init(&idle[0], 1);
-    mbar_init(&idle[1], 1);
-    mbar_init(&meet, 256);
+    mbar_init(&bar.q_free, 1);
+    mbar_init(&bar.meet, 256);
     fence_mbar_init();
   }
 
@@ -288,11 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     }
     return n * heads;
   };
-  long long mine = 0, last_units = 0;
-  for (int i = 0; i < per; ++i) {
-    last_units = request_units(b0 + i, b0 + i < b1);
-    mine += last_units;
-  }
+  long long mine = 0;
+  for (int i = 0; i < per; ++i) mine += request_units(b0 + i, b0 + i < b1);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -300,152 +359,99 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     if (lane >= d) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
   long long total = 0, before = incl - mine;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
   const long long span = max(static_cast<long long>(kSetup + 4), quotient(total + gridDim.x - 1, gridDim.x));
-  if (span * blockIdx.x >= total) return;
   const int snap = static_cast<int>(min(span / kSnap, static_cast<long long>(1 << 20)));
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     const long long at = span * (blockIdx.x + i);
     const bool here = at >= before && at < before + mine;
-    if (per > 1 && __any_sync(0xffffffffu, here)) {
-      long long rem = at - before;
-      int b = b0;
-      for (int k = 0; k < per - 1; ++k) {  // (the run's last takes what is left)
-        const bool go = here && b == b0 + k && b < b1 - 1;
-        const long long n = request_units(b0 + k, go);
-        if (go && rem >= n) {
-          rem -= n;
-          ++b;
-        }
+    if (!__any_sync(0xffffffffu, here)) continue;
+    long long rem = at - before;
+    int b = b0;
+    for (int k = 0; k < per - 1; ++k) {  // (the run's last takes what is left)
+      const bool go = here && b == b0 + k && b < b1 - 1;
+      const long long n = request_units(b0 + k, go);
+      if (go && rem >= n) {
+        rem -= n;
+        ++b;
       }
-      if (here) cut_b[i] = b, cut_rem[i] = rem;
-    } else if (here) {
-      cut_b[i] = b0, cut_rem[i] = at - before;
     }
-  }
-  if (warp == 12) tmem_alloc(&tmem_holder, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_holder;
-  if (warp < 2) {  // warp 0: where the range starts; warp 1: where it ends
-    const long long at = span * (blockIdx.x + warp);
-    if (at < total) {
-      Cursor cut;
-      cut.start(a, cut_b[warp], cut_rem[warp], at, blockIdx.x + warp == 0 ? 0 : snap, lane);
-      if (lane == 0) cuts[warp] = cut;
-    } else if (lane == 0) {
-      cuts[warp].unit = total;
-    }
+    if (here) cut_b[i] = b, cut_rem[i] = rem;
   }
   __syncthreads();
-  // S: two tiles of each half, 64 columns each, whose first 32 become P; O behind them
-  const uint32_t tS = tmem, tO = tmem + 256;
-
-  Walk walk;
-  walk.at = cuts[0];
-  walk.end = cuts[1].unit;
+  const uint32_t tS = tmem, tP = tmem + 192, tO = tmem + 256;
   bool ok = true;  // no wait of this role has run out
-  bool some = walk.first(a);
 
   // (one instruction a warpgroup)
   if (warp < 8) setmaxnreg_inc<168>();
   else if (warp < 12) setmaxnreg_dec<112>();
   else setmaxnreg_dec<64>();
 
+  // The next segment, as this warp's seg-th; its place is given back.
+  uint32_t seg = 0;
+  const auto next_segment = [&](Segment& s) {
+    if (!ok) return false;
+    const uint32_t at = seg % kSegments;
+    ok = mbar_wait(&bar.seg_full[at], seg / kSegments & 1, a.err);
+    ok = __all_sync(0xffffffffu, ok);
+    s = segments[at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.seg_empty[at]);
+    ++seg;
+    return ok && s.count > 0;
+  };
+
   if (warp < 8) {
     // ---------------- softmax ----------------
     const int half = warp >> 2, row = tid & 127;  // this thread's row of the half
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tS + lanes + half * 128, o_at = tO + lanes + half * D;
-    uint8_t* const q_sm = sm + half * L::kQHalf;
+    const uint32_t p_at = tP + lanes + half * 32, o_at = tO + lanes + half * D;
     uint8_t* const scratch = sm + L::kScratch + warp * 2048;  // 32 rows of 64 bytes
-    float unit = 0.f;  // this row's row_unit
-    int lim = 0;       // the last position it sees
-    // The queries of the warp's 32 rows, a row's 16-byte pieces on consecutive lanes: scaled so that
-    // the row's largest element is in [2^9, 2^10), as fp16, in the order (0,4),(1,5),(2,6),(3,7)
-    // of each eight dimensions, which is the one K's decoding gives.
-    auto load_q = [&]() {
-      constexpr int LR = D / 8, RI = 32 / LR;  // lanes a row, rows a step
-      const Request& r = walk.at.r;
-      const int c0 = walk.at.part * kRows + half * 128;
-      const int w = lane % LR, sub = lane / LR;
-      uint4 v[32 / RI];
-#pragma unroll
-      for (int i = 0; i < 32 / RI; ++i) {
-        const int c = c0 + (warp & 3) * 32 + i * RI + sub, token = a.token_of(c);
-        v[i] = c < r.rows
-                   ? __ldg(reinterpret_cast<const uint4*>(
-                               static_cast<const __nv_bfloat16*>(a.q) +
-                               static_cast<size_t>(r.row0 + token) * a.ldq +
-                               (walk.at.head * G + c - token * G) * D) + w)
-                   : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < 32 / RI; ++i) {
-        const int at = (warp & 3) * 32 + i * RI + sub;
-        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
-#pragma unroll
-        for (int d = LR / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int e = top > 0.f && top < INFINITY
-                          ? min(120, 9 + 127 - static_cast<int>(__float_as_uint(top) >> 23))
-                          : 0;
-        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e + 127) << 23), a.scale_log2);
-        // (never 0, so that a masked score stays -inf)
-        if (w == 0)
-          row_unit[half * 128 + at] = fmaxf(
-              kKvUnit * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
-        *reinterpret_cast<uint4*>(q_sm + (w >> 3) * (128 * 128) + at * 128 + (((w & 7) ^ (at & 7)) << 4)) =
-            make_uint4(pack_f16x2(bf16_lo(x[0]) * up, bf16_lo(x[2]) * up),
-                       pack_f16x2(bf16_hi(x[0]) * up, bf16_hi(x[2]) * up),
-                       pack_f16x2(bf16_lo(x[1]) * up, bf16_lo(x[3]) * up),
-                       pack_f16x2(bf16_hi(x[1]) * up, bf16_hi(x[3]) * up));
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&q_full[half]);
-      __syncwarp();
-      unit = row_unit[half * 128 + row];
-      const int c = c0 + row;  // (a row past the last is written nowhere)
-      lim = c < r.rows ? r.kv - r.q_len + a.token_of(c) : r.kv - 1;
-    };
+    const float unit = fmaxf(fabsf(a.scale_log2), 1e-30f);  // to scores in units of log2(e); never 0,
+                                                            // so that a masked score stays -inf
     // the softmax warps wait for one another, bounded like every wait
     uint32_t meetings = 0;
     auto meet_all = [&]() {
-      mbar_arrive(&meet);
-      ok = mbar_wait(&meet, meetings++ & 1, a.err);
+      mbar_arrive(&bar.meet);
+      ok = mbar_wait(&bar.meet, meetings++ & 1, a.err);
       ok = __all_sync(0xffffffffu, ok);
     };
-    uint32_t n = 0;  // tiles of this half
-    bool active = some && (half == 0 || walk.second_half());
-    if (active) load_q();
-    while (some && ok) {
-      const Walk now = walk;
-      const int first_pos = now.at.tile * kTile;
+    uint32_t step = 0, n = 0;  // S tiles of both halves, tiles of this half
+    Segment g = {};
+    while (next_segment(g)) {
+      const int halves = g.rows > 128 ? 2 : 1;
+      const bool active = half < halves;
       float m = kNone, l = 0.f;
-      const float my_unit = unit;
-      const int my_lim = lim;
       if (active) {
-        for (int j = 0; j < now.count; ++j, ++n) {
-          ok = mbar_wait(&s_full[half][n & 1], n >> 1 & 1, a.err);
+        // the last position this row sees, from the segment's first tile on (a row past the
+        // last is written nowhere)
+        const int lim = g.see + a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) - g.tile * kTile;
+        uint32_t at = (step + half) % 3;  // S's place
+        for (int j = 0; j < g.count; ++j, ++n) {
+          const uint32_t pv_there = n > 0 ? mbar_peek(&bar.pv_done[half], (n - 1) & 1) : 1;
+          ok = mbar_wait(&bar.s_full[half][n % 3], n / 3 & 1, a.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = s_at + (n & 1) * 64;
           uint32_t s[2][32];
-          tmem_ld_32x32b_x32(at, s[0]);
-          tmem_ld_32x32b_x32(at + 32, s[1]);
+          tmem_ld_32x32b_x32(tS + lanes + at * 64, s[0]);
+          tmem_ld_32x32b_x32(tS + lanes + at * 64 + 32, s[1]);
           tmem_ld_wait();
-          const int left = my_lim - (first_pos + j * kTile);  // the tile's positions 0..left are seen
+          tc_fence_before();
+          mbar_arrive(&bar.s_read[at]);
+          at += halves;
+          if (at >= 3) at -= 3;
+          const int left = lim - j * kTile;  // the tile's positions 0..left are seen
           if (__any_sync(0xffffffffu, left < kTile - 1)) {
 #pragma unroll
             for (int i = 0; i < kTile; ++i)
@@ -455,28 +461,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
 #pragma unroll
           for (int i = 0; i < kTile; ++i)
             top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i >> 5][i & 31]));
-          const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * my_unit;
-          if (__any_sync(0xffffffffu, peak > m + (kRef + kSlack))) {
-            const float moved = fmaxf(m, peak - kRef), f = ex2(m - moved);
+          const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+          const bool move = __any_sync(0xffffffffu, peak > m + (kRef + kSlack));
+          float f = 1.f;
+          if (move) {
+            const float moved = fmaxf(m, peak - kRef);
+            f = ex2(m - moved);
             m = moved;
             l *= f;
-            if (j > 0) {  // O of the tiles before, once their products are done
-              ok = mbar_wait(&pv_done[half][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_at + d, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_32x32b_x32(o_at + d, o);
-              }
-            }
           }
-          const float2 by = make_float2(my_unit, my_unit), minus = make_float2(-m, -m);
+          const float2 by = make_float2(unit, unit), minus = make_float2(-m, -m);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t p[32];
 #pragma unroll
@@ -488,78 +482,92 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
             sum[i & 1] = add2(sum[i & 1], e);
             p[i] = pack_f16x2(e.x, e.y);
           }
-          tmem_st_32x32b_x32(at, p);
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          // the product before is done: P's place is free, and O may be rescaled
+          if (!pv_there) {
+            ok = mbar_wait(&bar.pv_done[half], (n - 1) & 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          tmem_st_32x32b_x32(p_at, p);
+          if (move && j > 0) {
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_at + d, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x32(o_at + d, o);
+            }
+          }
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&p_full[half][n & 1]);
+          mbar_arrive(&bar.p_full[half]);
         }
       }
       if (!ok) break;
-      // the next segment's queries, while this one's last products run
-      some = walk.next(a);
-      const bool next_active = some && (half == 0 || walk.second_half());
-      if (next_active) load_q();
+      step += g.count * halves;
 
       if (active) {
-        ok = mbar_wait(&pv_done[half][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
+        ok = mbar_wait(&bar.pv_done[half], (n - 1) & 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
       }
-      const Request& r = now.at.r;
-      const int c0 = now.at.part * kRows;
-      const long long group = now.at.unit - now.at.tile;
-      const bool whole = now.at.tile == 0 && now.count == now.at.tiles;
+      const bool whole = g.tile == 0 && g.count == g.tiles;
       // this CTA's piece of a group it shares: 0 began before it, 1 goes on after it
       float* const piece = a.prompt_pieces +
-                           static_cast<size_t>(blockIdx.x * 2 + (now.at.tile > 0 ? 0 : 1)) * piece_floats<D>();
+                           static_cast<size_t>(blockIdx.x * 2 + (g.tile > 0 ? 0 : 1)) * piece_floats<D>();
       if (active) {
         // 64 bytes of every row at a time, from one row a lane to 4 lanes a row
         const float f = whole ? (l == 0.f ? 0.f : kKvUnit * a.v_scale / l) : 1.f;
-        const int step = whole ? 32 : 16;  // dimensions
         const auto at = [&](int x, int k) {  // 16-byte piece k of row x
           return reinterpret_cast<uint4*>(scratch + x * 64 + ((k ^ (x >> 1 & 3)) << 4));
         };
         uint8_t* dst[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int x = (warp & 3) * 32 + i * 8 + (lane >> 2), c = c0 + half * 128 + x, token = a.token_of(c);
+          const int x = half * 128 + (warp & 3) * 32 + i * 8 + (lane >> 2);
+          const int c = g.first_row + x, token = a.token_of(c);
           dst[i] = nullptr;
-          if (c < r.rows)
+          if (x < g.rows)
             dst[i] = (whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                         static_cast<size_t>(r.row0 + token) * a.ldo +
-                                                         (now.at.head * G + c - token * G) * D)
-                            : reinterpret_cast<uint8_t*>(piece + 2 * kRows + (half * 128 + x) * D)) +
+                                                         static_cast<size_t>(g.row0 + token) * a.ldo +
+                                                         (g.head * G + c - token * G) * D)
+                            : reinterpret_cast<uint8_t*>(piece + 2 * kRows + x * D)) +
                      (lane & 3) * 16;
         }
-#pragma unroll 1
-        for (int d = 0; d < D; d += step) {
-          uint32_t o[32];
-          if (whole) {
-            tmem_ld_32x32b_x32(o_at + d, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-          } else {
-            uint32_t part[16];
-            tmem_ld_32x32b_x16(o_at + d, part);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = part[i];
-          }
+        const auto put = [&](const uint32_t* o, int off) {  // 16 words of this lane's row
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *at(lane, k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (dst[i]) {
-              *reinterpret_cast<uint4*>(dst[i]) = *at(i * 8 + (lane >> 2), lane & 3);
-              dst[i] += 64;
-            }
+            if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + off) = *at(i * 8 + (lane >> 2), lane & 3);
           __syncwarp();
+        };
+#pragma unroll 1
+        for (int d = 0; d < D; d += 64) {
+          uint32_t o[2][32];
+          tmem_ld_32x32b_x32(o_at + d, o[0]);
+          tmem_ld_32x32b_x32(o_at + d + 32, o[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (whole) {
+              uint32_t x[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                x[i] = pack_bf16x2(__uint_as_float(o[k][2 * i]) * f, __uint_as_float(o[k][2 * i + 1]) * f);
+              put(x, (d + k * 32) * 2);
+            } else {
+              put(o[k], (d + k * 32) * 4);
+              put(o[k] + 16, (d + k * 32 + 16) * 4);
+            }
+          }
         }
         tc_fence_before();
         if (!whole) {
@@ -570,14 +578,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (!whole) {
         // The cuts within the group, as their CTAs see them, and the pieces between them: the
         // first cut's CTA before it (piece 1), then pieces 0.
-        const int first_cut = static_cast<int>(quotient(group + snap, span)) + 1;
-        const int last_cut = static_cast<int>(quotient(group + now.at.tiles - snap + span - 1, span)) - 1;
-        const int n = last_cut - first_cut + 2;
+        const int first_cut = static_cast<int>(quotient(g.unit + snap, span)) + 1;
+        const int last_cut = static_cast<int>(quotient(g.unit + g.tiles - snap + span - 1, span)) - 1;
+        const int pieces = last_cut - first_cut + 2;
         __threadfence();
         meet_all();
         if (!ok) break;
         if (tid == 0) {
-          last_cta = atomicAdd(a.prompt_arrivals + first_cut, 1) == n - 1;
+          last_cta = atomicAdd(a.prompt_arrivals + first_cut, 1) == pieces - 1;
           if (last_cta) a.prompt_arrivals[first_cut] = 0;
           __threadfence();
         }
@@ -588,22 +596,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
             return a.prompt_pieces +
                    static_cast<size_t>(i == 0 ? (first_cut - 1) * 2 + 1 : (first_cut + i - 1) * 2) * piece_floats<D>();
           };
-          const int rows = min(kRows, r.rows - now.at.part * kRows);
-          for (int x = warp; x < rows; x += 8) {
+          for (int x = warp; x < g.rows; x += 8) {
             float top = kNone;
-            for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(piece_of(i) + x));
+            for (int i = lane; i < pieces; i += 32) top = fmaxf(top, __ldcg(piece_of(i) + x));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             float sum = 0.f, o[D / 32] = {};
-            for (int i0 = 0; i0 < n; i0 += 32) {
+            for (int i0 = 0; i0 < pieces; i0 += 32) {
               float f = 0.f;
-              if (i0 + lane < n) {
+              if (i0 + lane < pieces) {
                 f = ex2(__ldcg(piece_of(i0 + lane) + x) - top);
                 sum += f * __ldcg(piece_of(i0 + lane) + kRows + x);
               }
-              const int some_pieces = min(32, n - i0);
+              const int here = min(32, pieces - i0);
 #pragma unroll 4
-              for (int k = 0; k < some_pieces; ++k) {
+              for (int k = 0; k < here; ++k) {
                 const float w = __shfl_sync(0xffffffffu, f, k);
                 const float* p = piece_of(i0 + k) + 2 * kRows + x * D + lane * (D / 32);
 #pragma unroll
@@ -617,17 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             const float f = sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum;
-            const int at = now.at.part * kRows + x, token = a.token_of(at);
+            const int c = g.first_row + x, token = a.token_of(c);
             uint32_t* out = reinterpret_cast<uint32_t*>(
-                static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(r.row0 + token) * a.ldo +
-                (now.at.head * G + at - token * G) * D + lane * (D / 32));
+                static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(g.row0 + token) * a.ldo +
+                (g.head * G + c - token * G) * D + lane * (D / 32));
 #pragma unroll
             for (int d = 0; d < D / 32; d += 2) out[d / 2] = pack_bf16x2(o[d] * f, o[d + 1] * f);
           }
         }
         meet_all();  // last_cta is read
+        if (!ok) break;
       }
-      active = next_active;
     }
   } else if (warp < 12) {
     // ---------------- decoding ----------------
@@ -644,17 +651,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const int vo = (lane & 3) | (w & 1) << 2;
     const int vd = (lane >> 2) | (D == 128 ? ((w >> 1) ^ (lane >> 1 & 1)) << 3 : 0);
     const bool v_mine = D == 128 || w < 2;
-    const int v_half = vo & 1;              // token of the octet's block half
+    const int v_half = vo & 1;              // the octet's half of its block
     const uint32_t sel_lo = vo & 1 ? 0x1054u : 0x5410u, sel_hi = vo & 1 ? 0x3276u : 0x7632u;
     const uint32_t sel[2] = {vd & 1 ? sel_hi : sel_lo, vd & 1 ? sel_lo : sel_hi};
     const bool swap = D == 128 && kc >= 2;  // these lanes decode their last 16 dimensions first
+    // 2^120, with the sign of the softmax's scale (whose size the scores are multiplied by)
+    const uint32_t k_unit = a.scale_log2 < 0.f ? 0xFB80FB80u : 0x7B807B80u;
     uint32_t n = 0;  // tiles decoded
-    while (some && ok) {
-      for (int j = 0; j < walk.count; ++j, ++n) {
+    Segment g = {};
+    // A segment's queries, a row's 16-byte pieces on consecutive lanes, in the order (0,4),(1,5),
+    // (2,6),(3,7) of each eight dimensions, which is the one K's decoding gives.
+    const auto load_q = [&]() {
+      constexpr int LR = D / 8, RI = 128 / LR, kBatch = 8;  // lanes a row, rows a step, steps at once
+      const int x0 = t / LR, p = t % LR;
+      if (seg > 1) ok = mbar_wait(&bar.q_free, seg & 1, a.err);  // of the segment before
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) +
+                                     static_cast<size_t>(g.row0) * a.ldq + g.head * G * D + p * 8;
+#pragma unroll 1
+      for (int h = 0; h < (g.rows > 128 ? 2 : 1); ++h) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < 128 / RI; i0 += kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int x = h * 128 + (i0 + i) * RI + x0, c = g.first_row + x, token = a.token_of(c);
+            v[i] = x < g.rows ? __ldg(reinterpret_cast<const uint4*>(
+                                    q + static_cast<size_t>(token) * a.ldq + (c - token * G) * D))
+                              : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int x = (i0 + i) * RI + x0;
+            *reinterpret_cast<uint4*>(sm + h * L::kQHalf + (p >> 3) * (128 * 128) + x * 128 +
+                                      (((p & 7) ^ (x & 7)) << 4)) =
+                make_uint4(prmt(v[i].x, v[i].z, 0x5410), prmt(v[i].x, v[i].z, 0x7632),
+                           prmt(v[i].y, v[i].w, 0x5410), prmt(v[i].y, v[i].w, 0x7632));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar.q_full[h]);
+      }
+    };
+    while (next_segment(g)) {
+      // The queries: the first segment's at once, later ones behind two tiles, when the products
+      // with those before are about done.
+      const int q_before = seg == 1 ? 0 : min(2, g.count);
+      for (int j = 0; j <= g.count && ok; ++j) {
+        if (j == q_before) load_q();
+        if (j == g.count || !ok) break;
         const int stage = n % kStages, parity = (n / kStages) & 1, slot = n % kRaw;
-        ok = mbar_wait(&raw_full[slot], (n / kRaw) & 1, a.err);
+        const uint32_t raw_there = mbar_peek(&bar.raw_full[slot], (n / kRaw) & 1),
+                       k_free = mbar_peek(&bar.k_empty[stage], parity ^ 1),
+                       v_free = mbar_peek(&bar.v_empty[stage], parity ^ 1);
+        if (!raw_there) ok = mbar_wait(&bar.raw_full[slot], (n / kRaw) & 1, a.err);
         const uint8_t* const tile = sm + L::kRaws + slot * L::kRawTile;
-        uint32_t kw[KT][4], ks[KT];  // ks: the two groups' scales as fp16
+        uint32_t kw[KT][4], ks[KT];  // ks: the two groups' scales in bytes 0 and 1
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
           const int token = kt + i * (128 / KC), in = token & 15, fr = kv_token_frag(in);
@@ -663,14 +716,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           kw[i][0] = swap ? x.z : x.x, kw[i][1] = swap ? x.w : x.y;
           kw[i][2] = swap ? x.x : x.z, kw[i][3] = swap ? x.y : x.w;
           if constexpr (D == 128) {
-            const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(
-                blk + kv_k_scales(D) + (fr & 7) * 16 + kc * 4 + (fr >> 3) * 2));
-            ks[i] = swap ? prmt(two, two, 0x1032) : two;
+            const uint32_t two = *reinterpret_cast<const uint16_t*>(
+                blk + kv_k_scales(D) + (fr & 7) * 16 + kc * 4 + (fr >> 3) * 2);
+            ks[i] = swap ? prmt(two, 0u, 0x4401) : two;
           } else {
-            const uint32_t x4 =
-                *reinterpret_cast<const uint32_t*>(blk + kv_k_scales(D) + (fr & 7) * 8 + kc * 4) >>
-                (8 * (fr >> 3));
-            ks[i] = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(x4, 0u, 0x4420)));
+            ks[i] = prmt(*reinterpret_cast<const uint32_t*>(blk + kv_k_scales(D) + (fr & 7) * 8 + kc * 4),
+                         0u, fr >> 3 ? 0x4431 : 0x4420);
           }
         }
         uint32_t vw[8], vs[4];
@@ -683,8 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           const int sh = 16 * v_half;  // then bytes 0, 1: tokens with bit 2 clear and set
           vs[0] = x.x >> sh, vs[1] = x.y >> sh, vs[2] = x.z >> sh, vs[3] = x.w >> sh;
         }
-        mbar_arrive(&raw_empty[slot]);
-        ok = ok && mbar_wait(&k_empty[stage], parity ^ 1, a.err);
+        mbar_arrive(&bar.raw_empty[slot]);
+        if (!k_free) ok = ok && mbar_wait(&bar.k_empty[stage], parity ^ 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // K: rows of tokens
@@ -693,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
         for (int i = 0; i < KT; ++i) {
           const int token = kt + i * (128 / KC);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const Decode dec = decode_scales(g ? both_hi(ks[i]) : both_lo(ks[i]));
+          for (int half = 0; half < 2; ++half) {
+            const DecodeBf16 dec = decode_scale_bf16(ks[i], half, k_unit);
 #pragma unroll
-            for (int x = 2 * g; x < 2 * g + 2; ++x) {
+            for (int x = 2 * half; x < 2 * half + 2; ++x) {
               uint32_t o[4];
               decode4(kw[i][x], dec, o);
               const int chunk = kc * 4 + (swap ? x ^ 2 : x);  // of 8 dimensions
@@ -707,9 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&k_full[stage]);
+        mbar_arrive(&bar.k_full[stage]);
         // V: rows of dimensions, 8 tokens a chunk
-        ok = mbar_wait(&v_empty[stage], parity ^ 1, a.err);
+        if (!v_free) ok = mbar_wait(&bar.v_empty[stage], parity ^ 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (v_mine) {
@@ -735,35 +786,142 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&v_full[stage]);
+        mbar_arrive(&bar.v_full[stage]);
+        ++n;
       }
-      if (!ok) break;
-      some = walk.next(a);
     }
+  } else if (warp < 14) {
+    // ---------------- PV products ----------------
+    // Descriptors advance by constants, 32 bytes (2 units) a 16-wide step.
+    constexpr uint32_t kDesc = idesc_f16_f32(128, D);
+    const uint32_t leader = elect_leader();
+    const int half = warp - 12;
+    const uint32_t p_at = tP + half * 32, o_at = tO + half * D;
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sm) + L::kV);
+    uint32_t stage = 0, turn = 0, n = 0;  // of the next tile; tiles of this half
+    Segment g = {};
+    while (next_segment(g)) {
+      const bool active = half == 0 || g.rows > 128;
+      for (int j = 0; j < g.count; ++j) {
+        const uint32_t v_there = mbar_peek(&bar.v_full[stage], turn);
+        if (active) ok = mbar_wait(&bar.p_full[half], n & 1, a.err);
+        if (!v_there) ok = ok && mbar_wait(&bar.v_full[stage], turn, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (active) {
+          tc_fence_after();
+          const uint64_t vd = v_desc + stage * (L::kKv >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_ts(o_at, p_at + ks * 8, vd + ks * 2, kDesc, ks > 0 ? 1 : j, leader);
+          commit(&bar.pv_done[half], leader);
+          commit(&bar.v_empty[stage], leader);
+          ++n;
+        } else if (leader) {
+          mbar_arrive(&bar.v_empty[stage]);  // no rows: the stages pass by
+        }
+        if (++stage == kStages) stage = 0, turn ^= 1;
+      }
+    }
+    // every product issued is done before the CTA's memory goes
+    commit(&bar.idle[half], leader);
+    mbar_wait(&bar.idle[half], 0, a.err);
   } else if (warp == 14) {
-    // ---------------- fetching ----------------
+    // ---------------- QK products ----------------
+    constexpr uint32_t kDesc = idesc_bf16_f32(128, kTile);
+    const uint32_t leader = elect_leader();
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sm)), k_desc = smem_desc_sw128(smem_u32(sm) + L::kK);
+    uint32_t stage = 0, turn = 0;           // of the next tile of K
+    uint32_t at = 0, phase = 0;             // of the next S's place
+    uint32_t n[2] = {0, 0}, groups1 = 0;    // the halves' next s_full; groups of half 1
+    bool used = false;                      // S's places have been used
+    Segment g = {};
+    while (next_segment(g)) {
+      const int halves = g.rows > 128 ? 2 : 1;
+      ok = mbar_wait(&bar.q_full[0], (seg - 1) & 1, a.err);
+      if (halves == 2) ok = ok && mbar_wait(&bar.q_full[1], groups1++ & 1, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      uint32_t k_there = 0, free = 0;  // what was seen ahead
+      for (int j = 0; j < g.count && ok; ++j) {
+        if (!k_there) ok = mbar_wait(&bar.k_full[stage], turn, a.err);
+        const uint32_t k_stage = stage;
+        if (++stage == kStages) stage = 0, turn ^= 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves) break;
+          if (used && !free) ok = ok && mbar_wait(&bar.s_read[at], phase ^ 1, a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s_at = tS + at * 64;
+          if (++at == 3) at = 0, phase ^= 1, used = true;
+          free = used ? mbar_peek(&bar.s_read[at], phase ^ 1) : 1;
+          if (h == halves - 1) k_there = mbar_peek(&bar.k_full[stage], turn);
+          uint64_t qd = q_desc + h * (L::kQHalf >> 4), kd = k_desc + k_stage * (L::kKv >> 4);
+#pragma unroll
+          for (int slab = 0; slab < D / 64; ++slab) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma_ss(s_at, qd + ks * 2, kd + ks * 2, kDesc, slab > 0 || ks > 0, leader);
+            qd += 128 * 128 >> 4;
+            kd += kTile * 128 >> 4;
+          }
+          commit(&bar.s_full[h][n[h]], leader);
+          if (++n[h] == 3) n[h] = 0;
+        }
+        commit(&bar.k_empty[k_stage], leader);
+      }
+      commit(&bar.q_free, leader);
+    }
+    commit(&bar.idle[2], leader);
+    mbar_wait(&bar.idle[2], 0, a.err);
+  } else {
+    // ---------------- the walk and the packed tiles ----------------
     const int shift = a.pages.page_shift;
     const int step = min(kTile, 1 << shift);          // positions of a copy
-    const bool mine = lane * kKvBlock < kTile && lane * kKvBlock % step == 0;
+    const bool copies = lane * kKvBlock < kTile && lane * kKvBlock % step == 0;
     const uint32_t bytes = step / kKvBlock * kv_block_bytes(D);
+    Walk walk;
+    bool some = false;
+    if (span * blockIdx.x < total) {
+      walk.end = total;
+      if (span * (blockIdx.x + 1) < total) {
+        walk.at.start(a, cut_b[1], cut_rem[1], span * (blockIdx.x + 1), snap, lane);
+        walk.end = walk.at.unit;
+      }
+      walk.at.start(a, cut_b[0], cut_rem[0], span * blockIdx.x, blockIdx.x == 0 ? 0 : snap, lane);
+      some = walk.first(a);
+    }
     uint32_t n = 0;
-    const auto prefetch_q = [&](const Cursor& at) {  // a group's queries to L2
-      const int first = a.token_of(at.part * kRows), last = a.token_of(min((at.part + 1) * kRows, at.r.rows) - 1);
-      for (int token = first + lane; token <= last; token += 32)
-        bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + static_cast<size_t>(at.r.row0 + token) * a.ldq +
-                             at.head * G * D,
-                         G * D * 2);
-    };
-    while (some && ok) {
-      Walk ahead = walk;
-      if (ahead.next(a)) prefetch_q(ahead.at);
-      const Request& r = walk.at.r;
-      const int32_t* row = a.table + static_cast<size_t>(walk.at.b) * a.max_blocks;
-      const int last = max(0, (r.kv - 1) >> shift);  // the request's last page
-      // the page of position pos (of the last page past the end: masked, and within the cache)
-      auto page_of = [&](int j) {
-        const int pos = (walk.at.tile + j) * kTile + lane * kKvBlock;
-        return mine && r.kv > 0 ? __ldg(row + min(pos >> shift, last)) : 0;
+    while (ok) {
+      // announce the segment, or the end
+      const uint32_t place = seg % kSegments;
+      ok = mbar_wait(&bar.seg_empty[place], (seg / kSegments & 1) ^ 1, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const Cursor& c = walk.at;
+      const int rows = some ? min(kRows, c.r.rows - c.part * kRows) : 0;
+      if (lane == 0) {
+        segments[place] = some ? Segment{walk.count, c.tile, c.tiles, rows, c.part * kRows, c.r.row0,
+                                         c.r.kv - c.r.q_len, c.head, c.unit - c.tile}
+                               : Segment{};
+        mbar_arrive(&bar.seg_full[place]);
+      }
+      __syncwarp();
+      ++seg;
+      if (!some) break;
+      if (seg > 1) {  // its queries to L2: they are read behind the segment before
+        const int last = a.token_of(c.part * kRows + rows - 1);
+        for (int token = a.token_of(c.part * kRows) + lane; token <= last; token += 32)
+          bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) +
+                               static_cast<size_t>(c.r.row0 + token) * a.ldq + c.head * G * D,
+                           G * D * 2);
+      }
+      const int32_t* const pages = a.table + static_cast<size_t>(c.b) * a.max_blocks;
+      const int last = max(0, (c.r.kv - 1) >> shift);  // the request's last page
+      // the page of a tile's position (of the last page past the end: masked, and within the cache)
+      const auto page_of = [&](int j) {
+        const int pos = (c.tile + j) * kTile + lane * kKvBlock;
+        return copies && c.r.kv > 0 ? __ldg(pages + min(pos >> shift, last)) : 0;
       };
       int id = page_of(0);
       for (int j = 0; j < walk.count; ++j, ++n) {
@@ -773,95 +931,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           atomicOr(a.err, LORA_ERRF_BAD_ID);
           id = 0;
         }
-        ok = mbar_wait(&raw_empty[slot], ((n / kRaw) & 1) ^ 1, a.err);
+        ok = mbar_wait(&bar.raw_empty[slot], ((n / kRaw) & 1) ^ 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], L::kRawTile);
+        if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], L::kRawTile);
         __syncwarp();
-        if (mine) {
-          const int pos = (walk.at.tile + j) * kTile + lane * kKvBlock;
+        if (copies) {
+          const int pos = (c.tile + j) * kTile + lane * kKvBlock;
           bulk_load_g2s(sm + L::kRaws + slot * L::kRawTile + lane * kv_block_bytes(D),
-                        a.pages.base + a.pages.block(id, walk.at.head, (pos & ((1 << shift) - 1)) / kKvBlock),
-                        bytes, &raw_full[slot]);
+                        a.pages.base + a.pages.block(id, c.head, (pos & ((1 << shift) - 1)) / kKvBlock),
+                        bytes, &bar.raw_full[slot]);
         }
         id = next_id;
       }
-      if (!ok) break;
-      some = walk.next(a);
+      if (ok) some = walk.next(a);
     }
     // copies in flight write this CTA's memory: every one issued has landed when its slot's
     // barrier has turned
     for (uint32_t i = n > kRaw ? n - kRaw : 0; i < n; ++i)
-      mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, a.err);
-  } else if (warp < 14 && lane == 0) {
-    // ---------------- products ----------------
-    // One thread a half, so that one half's waits and commits pass while the other's products
-    // run; descriptors advance by constants, 32 bytes (2 units) a 16-wide step.
-    constexpr uint32_t kQkDesc = idesc_f16_f32(128, kTile), kPvDesc = idesc_f16_f32(128, D);
-    const int half = warp - 12;
-    const uint32_t s_at = tS + half * 128, o_at = tO + half * D;
-    const uint32_t base = smem_u32(sm);
-    const uint64_t q_desc = smem_desc_sw128(base + half * L::kQHalf),
-                   k_desc = smem_desc_sw128(base + L::kK), v_desc = smem_desc_sw128(base + L::kV);
-    uint32_t k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;  // of the next tiles
-    uint32_t groups_done = 0, n = 0;                            // groups and PV products of this half
-    const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait(bar, parity & 1, a.err);
-      tc_fence_after();
-      return ok;
-    };
-    const auto qk = [&](uint32_t tile) {  // S of the half's tile, whose K is the next stage
-      if (!wait(&k_full[k_stage], k_turn)) return;
-      uint64_t qd = q_desc, kd = k_desc + k_stage * (L::kKv >> 4);
-#pragma unroll
-      for (int slab = 0; slab < D / 64; ++slab) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc_mma_bf16(s_at + (tile & 1) * 64, qd + ks * 2, kd + ks * 2, kQkDesc, slab > 0 || ks > 0);
-        qd += 128 * 128 >> 4;
-        kd += kTile * 128 >> 4;
-      }
-      tc_commit(&s_full[half][tile & 1]);
-      tc_commit(&k_empty[k_stage]);
-      if (++k_stage == kStages) k_stage = 0, ++k_turn;
-    };
-    while (some && ok) {
-      const int count = walk.count;
-      if (half == 1 && !walk.second_half()) {
-        // no rows: the stages pass by
-        for (int j = 0; j < count; ++j) {
-          if (!wait(&k_full[k_stage], k_turn) || !wait(&v_full[v_stage], v_turn)) break;
-          mbar_arrive(&k_empty[k_stage]);
-          mbar_arrive(&v_empty[v_stage]);
-          if (++k_stage == kStages) k_stage = 0, ++k_turn;
-          if (++v_stage == kStages) v_stage = 0, ++v_turn;
-        }
-      } else {
-        // S of two tiles ahead.  S of tile i takes the place of P of tile i - 2, so its product
-        // waits until that one's is done.
-        if (!wait(&q_full[half], groups_done++)) break;
-        if (n > 0 && !wait(&pv_done[half][(n - 1) & 1], (n - 1) >> 1)) break;
-        qk(n);
-        if (count > 1 && ok) qk(n + 1);
-        for (int j = 0; j < count && ok; ++j, ++n) {
-          if (!wait(&v_full[v_stage], v_turn) || !wait(&p_full[half][n & 1], n >> 1)) break;
-          const uint64_t vd = v_desc + v_stage * (L::kKv >> 4);
-          const uint32_t p_at = s_at + (n & 1) * 64;
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_f16_ts(o_at, p_at + ks * 8, vd + ks * 2, kPvDesc, j > 0 || ks > 0);
-          tc_commit(&pv_done[half][n & 1]);
-          tc_commit(&v_empty[v_stage]);
-          if (++v_stage == kStages) v_stage = 0, ++v_turn;
-          if (j + 2 < count && wait(&pv_done[half][n & 1], n >> 1)) qk(n + 2);
-        }
-      }
-      if (!ok) break;
-      some = walk.next(a);
-    }
-    // every product issued is done before the CTA's memory goes
-    tc_commit(&idle[half]);
-    mbar_wait(&idle[half], 0, a.err);
+      mbar_wait(&bar.raw_full[i % kRaw], (i / kRaw) & 1, a.err);
   }
   __syncwarp();
   tc_fence_before();
