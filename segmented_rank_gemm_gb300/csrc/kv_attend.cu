@@ -358,11 +358,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-          // words x, y hold dimensions 0..3 of the eight, z, w 4..7: pairs (i, i + 4)
-          qf[2 * w][nt][0] = pack_f16x2(bf16_lo(x[0]) * up, bf16_lo(x[2]) * up);
-          qf[2 * w][nt][1] = pack_f16x2(bf16_hi(x[0]) * up, bf16_hi(x[2]) * up);
-          qf[2 * w + 1][nt][0] = pack_f16x2(bf16_lo(x[1]) * up, bf16_lo(x[3]) * up);
-          qf[2 * w + 1][nt][1] = pack_f16x2(bf16_hi(x[1]) * up, bf16_hi(x[3]) * up);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            qf[2 * w + (i >> 1)][nt][i & 1] = pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
         }
         // (never 0, so that a masked score stays -inf)
         const float down =

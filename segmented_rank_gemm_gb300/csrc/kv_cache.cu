@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = 0; j < 16; ++j) {
     float q = s > 0.f ? rintf(__fdiv_rn(x[j], s)) : 0.f;
     q = q != q ? 0.f : fminf(fmaxf(q, -7.f), 7.f);
-    code[j >> 3] |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * (j & 7));
+    code[j >> 3] |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * kv_nibble(is_v, j & 7));
   }
   const int per_head = pg.D / kKvGroup;
   const int head = hg / per_head, group = hg % per_head;
@@ -103,8 +103,9 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t word = j < 4 ? c.x : c.y;
-      const float a = static_cast<float>(static_cast<int>(word >> (8 * (j & 3)) & 15) - 8);
-      const float b = static_cast<float>(static_cast<int>(word >> (8 * (j & 3) + 4) & 15) - 8);
+      const int i = 2 * (j & 3);
+      const float a = static_cast<float>(static_cast<int>(word >> (4 * kv_nibble(is_v, i)) & 15) - 8);
+      const float b = static_cast<float>(static_cast<int>(word >> (4 * kv_nibble(is_v, i + 1)) & 15) - 8);
       out[j] = pack_bf16x2(a * s * g, b * s * g);
     }
   } else if (slot != -1 && hg == 0) {

@@ -5,9 +5,11 @@
 //     page -> head -> block of 16 positions -> { K codes | K scales | V codes | V scales }
 // so a page's positions of one head are one contiguous run that a single bulk copy fetches.
 // Within a block, with D = head_dim (D/2 bytes of codes and D/16 scales a token):
-//   K codes  [16][D/2]: token rows, dimension 2i in byte i's low nibble.
-//   V codes  [16][D/2]: the same, but D = 128 swaps the two 32-byte halves of tokens with bit 1
-//            set, so that the lanes of a warp reading one 8-byte piece of 4 tokens hit all banks.
+//   K codes  [16][D/2]: token rows, 8 dimensions a 32-bit word, whose nibbles 0..3 hold the even
+//            dimensions and 4..7 the odd ones: what decodes to a pair is then a pair of the query.
+//   V codes  [16][D/2]: 8 dimensions a word in order; D = 128 swaps the two 32-byte halves of tokens
+//            with bit 1 set, so that the lanes of a warp reading one 8-byte piece of 4 tokens hit
+//            all banks.
 //   K scales and V scales in the order the lanes of the attention's matrix fragments read
 //            them (k_scale_at, v_scale_at).
 // The rows of a 16 x 16 fragment are the block's tokens in the order frag_token: lane group
@@ -33,6 +35,11 @@ __host__ __device__ constexpr int kv_k_scales(int D) { return kv_codes_bytes(D);
 __host__ __device__ constexpr int kv_v_codes(int D) { return kv_codes_bytes(D) + kv_scales_bytes(D); }
 __host__ __device__ constexpr int kv_v_scales(int D) {
   return 2 * kv_codes_bytes(D) + kv_scales_bytes(D);
+}
+
+// Nibble of a word's dimension i in 0..7.
+__host__ __device__ constexpr int kv_nibble(bool is_v, int i) {
+  return is_v ? i : (i >> 1) + 4 * (i & 1);
 }
 
 // Token of the block at fragment index r in 0..15.

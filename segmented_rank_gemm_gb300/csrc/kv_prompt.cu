@@ -27,8 +27,8 @@
 // read its own, and with P beside S rather than in its place no QK waits for a PV.
 //
 // Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs; a cut
-// within kSnap of a group's edge (in parts of a range) moves there.  A group that is still cut
-// leaves pieces (m, l, O), joined in order by the last CTA to arrive.
+// near a group's edge moves there.  A group that is still cut leaves pieces (m, l, O), joined in
+// order by the last CTA to arrive.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,9 +46,13 @@ constexpr int kThreads = 16 * 32;  // four warpgroups, which split the registers
 constexpr int kRows = 256;      // rows of a group, two halves
 constexpr int kTile = 64;       // positions of a tile
 constexpr int kStages = 3;      // decoded tiles of K, and of V
-constexpr int kRaw = 4;         // packed tiles
-constexpr int kSetup = 2;       // units a group counts before its tiles
-constexpr int kSnap = 12;       // a cut within 1 / kSnap of a range from a group's edge moves there
+constexpr int kRaw = 3;         // packed tiles
+constexpr int kSetup = 6;       // units a group counts before its tiles: what its change costs
+// A cut this near to a group's edge moves there: a group cut in two costs its CTAs about as much as
+// this many tiles, as long as that is little of a range.
+__device__ __forceinline__ int snap_of(long long span) {
+  return static_cast<int>(min(max(span / 12, 8ll), min(span / 4, 1ll << 20)));
+}
 constexpr float kRef = 6.f;     // P is 2^kRef at the reference
 constexpr float kSlack = 8.f;   // how far (in powers of two) a score may exceed the reference
 constexpr float kNone = -1.7e38f;
@@ -267,6 +271,7 @@ constexpr int piece_floats() {
   return kRows * (D + 2);
 }
 
+constexpr int kScratchWarp = 4096;  // a softmax warp's 32 rows of 128 bytes, on their way out
 template <int D>
 struct Smem {
   static constexpr int kQHalf = 128 * D * 2;     // one half's queries
@@ -275,7 +280,7 @@ struct Smem {
   static constexpr int kRawTile = kTile / kKvBlock * kv_block_bytes(D);
   static constexpr int kRaws = kV + kStages * kKv;
   static constexpr int kScratch = kRaws + kRaw * kRawTile;
-  static constexpr int kBytes = kScratch + 8 * 2048 + 1024;  // + alignment
+  static constexpr int kBytes = kScratch + 8 * kScratchWarp + 1024;  // + alignment
 };
 constexpr int kSegments = 4;       // announced ahead
 constexpr int kSegmentReaders = 15;  // warps
@@ -305,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   __shared__ long long scan[kThreads / 32], cut_rem[2];
   __shared__ int cut_b[2];
   __shared__ int last_cta;
+  __shared__ float2 row_join[kRows];  // of a shared group's rows: max m, factor of O
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.pages.heads, G = a.group;
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     total += scan[w];
   }
   const long long span = max(static_cast<long long>(kSetup + 4), quotient(total + gridDim.x - 1, gridDim.x));
-  const int snap = static_cast<int>(min(span / kSnap, static_cast<long long>(1 << 20)));
+  const int snap = snap_of(span);
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     const long long at = span * (blockIdx.x + i);
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const int half = warp >> 2, row = tid & 127;  // this thread's row of the half
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t p_at = tP + lanes + half * 32, o_at = tO + lanes + half * D;
-    uint8_t* const scratch = sm + L::kScratch + warp * 2048;  // 32 rows of 64 bytes
+    uint8_t* const scratch = sm + L::kScratch + warp * kScratchWarp;
     const float unit = fmaxf(fabsf(a.scale_log2), 1e-30f);  // to scores in units of log2(e); never 0,
                                                             // so that a masked score stays -inf
     // the softmax warps wait for one another, bounded like every wait
@@ -521,32 +527,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       float* const piece = a.prompt_pieces +
                            static_cast<size_t>(blockIdx.x * 2 + (g.tile > 0 ? 0 : 1)) * piece_floats<D>();
       if (active) {
-        // 64 bytes of every row at a time, from one row a lane to 4 lanes a row
+        // 128 bytes of every row at a time, from one row a lane to 8 lanes a row
         const float f = whole ? (l == 0.f ? 0.f : kKvUnit * a.v_scale / l) : 1.f;
+        const float2 by = make_float2(f, f), none = make_float2(0.f, 0.f);
         const auto at = [&](int x, int k) {  // 16-byte piece k of row x
-          return reinterpret_cast<uint4*>(scratch + x * 64 + ((k ^ (x >> 1 & 3)) << 4));
+          return reinterpret_cast<uint4*>(scratch + x * 128 + ((k ^ (x & 7)) << 4));
         };
-        uint8_t* dst[4];
+        // where they go: from the group's first token (or row of the piece) on, in bytes
+        const int first_token = a.token_of(g.first_row);
+        uint8_t* const base =
+            whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                               static_cast<size_t>(g.row0 + first_token) * a.ldo + g.head * G * D)
+                  : reinterpret_cast<uint8_t*>(piece + 2 * kRows);
+        const int x0 = half * 128 + (warp & 3) * 32;
+        const bool all = x0 + 32 <= g.rows;
+        uint8_t* dst[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = half * 128 + (warp & 3) * 32 + i * 8 + (lane >> 2);
-          const int c = g.first_row + x, token = a.token_of(c);
-          dst[i] = nullptr;
-          if (x < g.rows)
-            dst[i] = (whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                         static_cast<size_t>(g.row0 + token) * a.ldo +
-                                                         (g.head * G + c - token * G) * D)
-                            : reinterpret_cast<uint8_t*>(piece + 2 * kRows + x * D)) +
-                     (lane & 3) * 16;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t x = x0 + i * 4 + (lane >> 3), c = g.first_row + x, token = a.token_of(c);
+          const uint32_t row_bytes = whole ? static_cast<uint32_t>(a.ldo) * 2 : 0;
+          const uint32_t in_row = whole ? (c - token * G) * (D * 2) : x * (D * 4);
+          dst[i] = base + static_cast<uint64_t>(token - first_token) * row_bytes + in_row + (lane & 7) * 16;
         }
-        const auto put = [&](const uint32_t* o, int off) {  // 16 words of this lane's row
+        const auto put = [&](const uint32_t (&o)[32], int off) {  // 32 words of this lane's row
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
             *at(lane, k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           __syncwarp();
+          uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + off) = *at(i * 8 + (lane >> 2), lane & 3);
+          for (int i = 0; i < 8; ++i) v[i] = *at(i * 4 + (lane >> 3), lane & 7);
+          if (all) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst[i] + off) = v[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (x0 + i * 4 + (lane >> 3) < g.rows) *reinterpret_cast<uint4*>(dst[i] + off) = v[i];
+          }
           __syncwarp();
         };
 #pragma unroll 1
@@ -555,18 +573,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           tmem_ld_32x32b_x32(o_at + d, o[0]);
           tmem_ld_32x32b_x32(o_at + d + 32, o[1]);
           tmem_ld_wait();
+          if (whole) {
+            uint32_t x[32];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (whole) {
-              uint32_t x[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                x[i] = pack_bf16x2(__uint_as_float(o[k][2 * i]) * f, __uint_as_float(o[k][2 * i + 1]) * f);
-              put(x, (d + k * 32) * 2);
-            } else {
-              put(o[k], (d + k * 32) * 4);
-              put(o[k] + 16, (d + k * 32 + 16) * 4);
+            for (int i = 0; i < 32; ++i) {
+              const float2 y = fma2(make_float2(__uint_as_float(o[i >> 4][2 * i & 31]),
+                                                __uint_as_float(o[i >> 4][(2 * i & 31) + 1])),
+                                    by, none);
+              x[i] = pack_bf16x2(y.x, y.y);
             }
+            put(x, d * 2);
+          } else {
+            put(o[0], d * 4);
+            put(o[1], d * 4 + 128);
           }
         }
         tc_fence_before();
@@ -596,40 +615,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
             return a.prompt_pieces +
                    static_cast<size_t>(i == 0 ? (first_cut - 1) * 2 + 1 : (first_cut + i - 1) * 2) * piece_floats<D>();
           };
-          for (int x = warp; x < g.rows; x += 8) {
-            float top = kNone;
-            for (int i = lane; i < pieces; i += 32) top = fmaxf(top, __ldcg(piece_of(i) + x));
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            float sum = 0.f, o[D / 32] = {};
-            for (int i0 = 0; i0 < pieces; i0 += 32) {
-              float f = 0.f;
-              if (i0 + lane < pieces) {
-                f = ex2(__ldcg(piece_of(i0 + lane) + x) - top);
-                sum += f * __ldcg(piece_of(i0 + lane) + kRows + x);
-              }
-              const int here = min(32, pieces - i0);
+          // a row's maximum and the factor of its sum first, one row a thread
+          if (tid < g.rows) {
+            float top = kNone, sum = 0.f;
 #pragma unroll 4
-              for (int k = 0; k < here; ++k) {
-                const float w = __shfl_sync(0xffffffffu, f, k);
-                const float* p = piece_of(i0 + k) + 2 * kRows + x * D + lane * (D / 32);
+            for (int i = 0; i < pieces; ++i) top = fmaxf(top, __ldcg(piece_of(i) + tid));
+#pragma unroll 4
+            for (int i = 0; i < pieces; ++i)
+              sum += ex2(__ldcg(piece_of(i) + tid) - top) * __ldcg(piece_of(i) + kRows + tid);
+            row_join[tid] = make_float2(top, sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum);
+          }
+          meet_all();
+          if (!ok) break;
+          // then a row a warp, four at a time
+#pragma unroll 1
+          for (int x0 = warp; x0 < g.rows; x0 += 32) {
+            float o[4][D / 32] = {};
+            for (int i = 0; i < pieces; ++i) {
+              const float* const piece_i = piece_of(i);
+              float w[4];
+              float2 y[4][D / 64];
 #pragma unroll
-                for (int d = 0; d < D / 32; d += 2) {
-                  const float2 y = __ldcg(reinterpret_cast<const float2*>(p + d));
-                  o[d] += w * y.x;
-                  o[d + 1] += w * y.y;
+              for (int k = 0; k < 4; ++k) {
+                const int x = min(x0 + k * 8, g.rows - 1);
+                w[k] = __ldcg(piece_i + x);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d)
+                  y[k][d] = __ldcg(reinterpret_cast<const float2*>(piece_i + 2 * kRows + x * D) + d * 32 + lane);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float f = ex2(w[k] - row_join[min(x0 + k * 8, g.rows - 1)].x);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d) {
+                  o[k][2 * d] += f * y[k][d].x;
+                  o[k][2 * d + 1] += f * y[k][d].y;
                 }
               }
             }
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float f = sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum;
-            const int c = g.first_row + x, token = a.token_of(c);
-            uint32_t* out = reinterpret_cast<uint32_t*>(
-                static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(g.row0 + token) * a.ldo +
-                (g.head * G + c - token * G) * D + lane * (D / 32));
+            for (int k = 0; k < 4; ++k) {
+              const int x = x0 + k * 8;
+              if (x >= g.rows) break;
+              const float f = row_join[x].y;
+              const int c = g.first_row + x, token = a.token_of(c);
+              uint32_t* out = reinterpret_cast<uint32_t*>(
+                  static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(g.row0 + token) * a.ldo +
+                  (g.head * G + c - token * G) * D);
 #pragma unroll
-            for (int d = 0; d < D / 32; d += 2) out[d / 2] = pack_bf16x2(o[d] * f, o[d + 1] * f);
+              for (int d = 0; d < D / 64; ++d)
+                out[d * 32 + lane] = pack_bf16x2(o[k][2 * d] * f, o[k][2 * d + 1] * f);
+            }
           }
         }
         meet_all();  // last_cta is read
@@ -659,48 +695,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const uint32_t k_unit = a.scale_log2 < 0.f ? 0xFB80FB80u : 0x7B807B80u;
     uint32_t n = 0;  // tiles decoded
     Segment g = {};
-    // A segment's queries, a row's 16-byte pieces on consecutive lanes, in the order (0,4),(1,5),
-    // (2,6),(3,7) of each eight dimensions, which is the one K's decoding gives.
-    const auto load_q = [&]() {
-      constexpr int LR = D / 8, RI = 128 / LR, kBatch = 8;  // lanes a row, rows a step, steps at once
+    // A segment's queries, copied a row's 16-byte pieces on consecutive lanes (rows past the last are
+    // zero), in two steps: asked for, and handed over.
+    const auto ask_q = [&]() {
+      constexpr int LR = D / 8, RI = 128 / LR;  // lanes a row, rows a step
       const int x0 = t / LR, p = t % LR;
       if (seg > 1) ok = mbar_wait(&bar.q_free, seg & 1, a.err);  // of the segment before
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) +
                                      static_cast<size_t>(g.row0) * a.ldq + g.head * G * D + p * 8;
-#pragma unroll 1
-      for (int h = 0; h < (g.rows > 128 ? 2 : 1); ++h) {
-#pragma unroll 1
-        for (int i0 = 0; i0 < 128 / RI; i0 += kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int x = h * 128 + (i0 + i) * RI + x0, c = g.first_row + x, token = a.token_of(c);
-            v[i] = x < g.rows ? __ldg(reinterpret_cast<const uint4*>(
-                                    q + static_cast<size_t>(token) * a.ldq + (c - token * G) * D))
-                              : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int x = (i0 + i) * RI + x0;
-            *reinterpret_cast<uint4*>(sm + h * L::kQHalf + (p >> 3) * (128 * 128) + x * 128 +
-                                      (((p & 7) ^ (x & 7)) << 4)) =
-                make_uint4(prmt(v[i].x, v[i].z, 0x5410), prmt(v[i].x, v[i].z, 0x7632),
-                           prmt(v[i].y, v[i].w, 0x5410), prmt(v[i].y, v[i].w, 0x7632));
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bar.q_full[h]);
+      uint8_t* const dst = sm + (p >> 3) * (128 * 128) + x0 * 128 + (((p & 7) ^ (x0 & 7)) << 4);
+      const int rows = g.rows > 128 ? 256 : 128;
+#pragma unroll 4
+      for (int i = 0; i < rows / RI; ++i) {
+        const int x = i * RI + x0, c = min(g.first_row + x, g.first_row + g.rows - 1), token = a.token_of(c);
+        cp_async_16_zfill(dst + (x >> 7) * L::kQHalf + (i * RI & 127) * 128,
+                          q + static_cast<size_t>(token) * a.ldq + (c - token * G) * D, x < g.rows ? 16 : 0);
       }
     };
+    const auto hand_q = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.q_full[0]);
+      if (g.rows > 128) mbar_arrive(&bar.q_full[1]);
+    };
     while (next_segment(g)) {
-      // The queries: the first segment's at once, later ones behind two tiles, when the products
-      // with those before are about done.
+      // The queries: the first segment's asked for at once, later ones behind two tiles, when the
+      // products with those before are about done; handed over a tile later (which needs no
+      // product with them: three tiles fit the stages).
       const int q_before = seg == 1 ? 0 : min(2, g.count);
-      for (int j = 0; j <= g.count && ok; ++j) {
-        if (j == q_before) load_q();
-        if (j == g.count || !ok) break;
+      for (int j = 0; j <= g.count; ++j) {
+        if (j == q_before) ask_q();
+        if (!ok) break;
+        if (j == q_before + 1 || (j == g.count && j == q_before)) hand_q();
+        if (j == g.count) break;
         const int stage = n % kStages, parity = (n / kStages) & 1, slot = n % kRaw;
         const uint32_t raw_there = mbar_peek(&bar.raw_full[slot], (n / kRaw) & 1),
                        k_free = mbar_peek(&bar.k_empty[stage], parity ^ 1),
