@@ -24,11 +24,11 @@
 // Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs
 // and those into equal ranges for their warps, so that one long request fills the GPU and many
 // short ones balance.  A group counts kSetup units besides its tiles, about what its queries'
-// load and its output cost.  Each warp is independent: it runs its own ring of bulk copies (a tile of
+// load and its output cost, and a cut near a group's edge moves there.  Each warp is independent: it runs its own ring of bulk copies (a tile of
 // one head is one contiguous 4.6 KB, two of them for 16-position pages) and keeps its group's
-// state in registers.  A group cut by a range's end leaves (m, l, O) pieces, joined by the CTA
-// and, between CTAs, by the last one to arrive, in the order of the pieces: results do not
-// depend on timing.
+// state in registers.  A group cut by a range's end leaves (m, l, O) pieces (a warp's last one in
+// its ring, which is free by then), joined by the CTA and, between CTAs, by the last one to arrive,
+// in the order of the pieces: results do not depend on timing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -109,15 +109,17 @@ struct Cursor {
   Request r;
   int b, head, col, tile;
   long long unit;
-  // The first tile at or after unit `at`, the rem-th of request b_.
-  __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at) {
+  // The first tile at or after unit `at`, the rem-th of request b_; a cut within snap of a group's
+  // edge moves there (to its end by tile = tiles, one past the last).
+  __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at,
+                                        int snap) {
     b = b_;
     r = load_request<NT>(a, b, false);
     const int per = r.tiles + kSetup;
     const long long group = quotient(rem, per);
     const int off = static_cast<int>(rem - group * per);
-    tile = max(0, off - kSetup);
-    unit = at + max(0, kSetup - off);
+    tile = off <= kSetup + snap ? 0 : per - off <= snap ? r.tiles : off - kSetup;
+    unit = at - off + kSetup + tile;
     head = static_cast<int>(quotient(group, r.col_tiles));
     col = static_cast<int>(group - static_cast<long long>(head) * r.col_tiles);
   }
@@ -148,6 +150,7 @@ struct PieceInfo {
   int tiles;        // of the group
   int cols;         // its columns
   int row0, head, first_col;
+  const float* at;
 };
 
 template <int D, int NT>
@@ -178,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ long long scan[kWarps];
-  __shared__ long long start_rem[kWarps];
-  __shared__ int start_b[kWarps];
+  __shared__ long long start_rem[kWarps + 1], cut_unit[kWarps + 1];  // of the warps' cuts
+  __shared__ int start_b[kWarps + 1];
   __shared__ PieceInfo info[kWarps * 2];
   __shared__ int last_cta[2];
 
@@ -224,17 +227,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     total += scan[w];
   }
   const long long span = max(static_cast<long long>(kMinSpan), quotient(total + gridDim.x - 1, gridDim.x));
-  const long long cta_lo = span * blockIdx.x, cta_hi = min(total, cta_lo + span);
-  if (cta_lo >= total) return;
-  const long long wspan = (cta_hi - cta_lo + kWarps - 1) / kWarps;
+  if (span * blockIdx.x >= total) return;
+  const long long raw_lo = span * blockIdx.x, raw_hi = min(total, raw_lo + span);
+  const int wspan = static_cast<int>((span + kWarps - 1) / kWarps), snap = wspan / 6;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const long long at = cta_lo + w * wspan;
-    if (at < cta_hi && at >= before && at < before + mine) {
+  for (int w = 0; w <= kWarps; ++w) {
+    const long long at = min(raw_hi, raw_lo + static_cast<long long>(w) * wspan);
+    if (at >= before && at < before + mine) {
       long long rem = at - before;
       int b = b0;
-      for (;; ++b) {
-        if (b == b1 - 1) break;  // the run's last: what is left is its own
+      for (; b < b1 - 1; ++b) {  // (the run's last takes what is left)
         const long long n = request_units(load_request<NT>(a, b, false), heads);
         if (rem < n) break;
         rem -= n;
@@ -244,18 +246,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     }
   }
   __syncthreads();
-
-  const long long w_lo = cta_lo + warp * wspan, w_hi = min(cta_hi, w_lo + wspan);
+  Cursor<NT> in;
+#pragma unroll 1
+  for (int w = kWarps + warp; w >= 0; w -= kWarps) {  // this warp's first tile; warp 0: the CTA's end too
+    if (w > kWarps) continue;
+    const long long at = min(raw_hi, raw_lo + static_cast<long long>(w) * wspan);
+    in.unit = total;
+    if (at < total) in.start(a, start_b[w], start_rem[w], at, at == 0 ? 0 : snap);
+    if (lane == 0) cut_unit[w] = in.unit;
+  }
+  __syncthreads();
+  const long long w_lo = cut_unit[warp], w_hi = cut_unit[warp + 1];
+  const long long cta_lo = cut_unit[0], cta_hi = cut_unit[kWarps];
   float* const warp_pieces =
       a.pieces + static_cast<size_t>(gridDim.x) * 2 * piece_floats<D, NT>() +
       static_cast<size_t>(blockIdx.x * kWarps + warp) * 2 * piece_floats<D, NT>();
+  if (w_lo < w_hi && in.tile == in.r.tiles) {  // the cut moved to its group's end
+    if (w_lo + kSetup < w_hi) in.next_group(a);
+    else in.unit = w_hi;
+  }
 
-  if (w_lo < w_hi) {
+  if (w_lo < w_hi && in.unit < w_hi) {
     uint8_t* const my_ring = ring + warp * kStages * kTileBytes;
     uint64_t* const bar = full[warp];
-    Cursor<NT> in, at;
-    in.start(a, start_b[warp], start_rem[warp], w_lo);
-    at = in;
+    Cursor<NT> at = in;
     const int shift = a.pages.page_shift;
     const uint32_t page_bytes = static_cast<uint32_t>(kBlock) << (shift - 4);  // of one head
     const size_t page_stride = static_cast<size_t>(page_bytes) * heads;
@@ -330,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     const int tv = (t & 1) | (t >> 1) << 1;
     const int G = a.group;
     int stage = 0, phase = 0;
+    uint32_t there = 0;  // the stage's tile has been seen to be there
 
     while (at.unit < w_hi) {
       // the group's queries, the last position each column sees, and an empty state
@@ -388,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
 
       const int count = static_cast<int>(min(static_cast<long long>(at.r.tiles - at.tile), w_hi - at.unit));
       for (int i = 0; i < count; ++i) {
-        if (!dead && !mbar_wait(bar + stage, phase, a.err)) dead = true;
+        if (!there && !dead && !mbar_wait(bar + stage, phase, a.err)) dead = true;
+        there = mbar_peek(bar + (stage == kStages - 1 ? 0 : stage + 1), stage == kStages - 1 ? phase ^ 1 : phase);
         const int pos0 = (at.tile + i) * kTile;
         if (pos0 <= lim_hi) {
           const uint8_t* tile = my_ring + stage * kTileBytes;
@@ -584,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       } else {
         // a piece: slot 0 began before this warp's range, slot 1 goes on after it
         const int slot = group < w_lo ? 0 : 1;
-        float* piece = warp_pieces + slot * piece_floats<D, NT>();
+        const bool last = at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi;
+        float* piece = last ? reinterpret_cast<float*>(my_ring) : warp_pieces + slot * piece_floats<D, NT>();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         if (lane == 0)
           info[warp * 2 + slot] =
               PieceInfo{group, at.r.tiles, min(8 * NT, at.r.q_len * G - at.col * 8 * NT), at.r.row0,
-                        at.head, at.col * 8 * NT};
+                        at.head, at.col * 8 * NT, piece};
       }
       if (at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi) break;
       at.next_group(a);
@@ -618,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   // one warp, the weights 2^(m_i - max m) one piece a lane, then the weighted sum, whose loads
   // do not wait for one another.
   constexpr int NC = 8 * NT, kPiece = piece_floats<D, NT>(), VL = D / 32;
-  const auto join_column = [&](auto piece_of, int n, const PieceInfo& gi, int c, float* dst) {
+  const auto join_column = [&](auto piece_of, auto load, int n, const PieceInfo& gi, int c, float* dst) {
     float m = kNone;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(piece_of(i) + c));
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, load(piece_of(i) + c));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float l = 0.f, o[VL] = {};
@@ -628,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       float f = 0.f;
       if (i0 + lane < n) {
         const float* p = piece_of(i0 + lane);
-        f = ex2(__ldcg(p + c) - m);
-        l += f * __ldcg(p + NC + c);
+        f = ex2(load(p + c) - m);
+        l += f * load(p + NC + c);
       }
       const int some = min(32, n - i0);
 #pragma unroll 8
@@ -637,10 +654,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         const float w = __shfl_sync(0xffffffffu, f, k);
         const float* p = piece_of(i0 + k) + 2 * NC + c * D + lane * VL;
         if constexpr (VL == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+          const float4 x = load(reinterpret_cast<const float4*>(p));
           o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
         } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+          const float2 x = load(reinterpret_cast<const float2*>(p));
           o[0] += w * x.x, o[1] += w * x.y;
         }
       }
@@ -667,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   };
   // The groups that several warps share, their columns dealt to the warps.  Those that other
   // CTAs share too become pieces of this CTA: 0 began before it, 1 goes on after it.
-  float* const cta_warp_pieces = a.pieces + static_cast<size_t>(gridDim.x) * 2 * kPiece +
-                                 static_cast<size_t>(blockIdx.x) * kWarps * 2 * kPiece;
+  const auto load_own = [](const auto* p) { return *p; };           // of this CTA's pieces
+  const auto load_other = [](const auto* p) { return __ldcg(p); };  // of other CTAs'
   int shared_group[2] = {-1, -1}, item = 0;
   for (int i = 0; i < kWarps * 2;) {
     if (info[i].group < 0) {
@@ -689,17 +706,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     }
     for (int c = 0; c < gi.cols; ++c, ++item)
       if (item % kWarps == warp)
-        join_column([&](int k) { return cta_warp_pieces + (k == 0 ? piece0 : (piece0 & ~1) + 2 * k) * kPiece; },
-                    n, gi, c, dst);
+        join_column([&](int k) { return info[k == 0 ? piece0 : (piece0 & ~1) + 2 * k].at; }, load_own, n, gi,
+                    c, dst);
   }
   if (shared_group[0] < 0 && shared_group[1] < 0) return;
-  // The last CTA to arrive joins the CTAs' pieces: the first CTA's piece 1, then pieces 0.
+  // The last CTA to arrive joins the CTAs' pieces: piece 1 of the CTA before the first of the CTAs'
+  // cuts within the group, then pieces 0 of those behind them.
+  const auto first_cut = [&](const PieceInfo& gi) {
+    return static_cast<int>(quotient(gi.group + snap, span)) + 1;
+  };
+  const auto last_cut = [&](const PieceInfo& gi) {
+    return static_cast<int>(quotient(gi.group + gi.tiles - snap + span - 1, span)) - 1;
+  };
   __threadfence();
   __syncthreads();
   if (tid < 2 && shared_group[tid] >= 0) {
     const PieceInfo gi = info[shared_group[tid]];
-    const int first = static_cast<int>(quotient(gi.group, span));
-    const int others = static_cast<int>(quotient(gi.group + gi.tiles - 1, span)) - first;
+    const int first = first_cut(gi), others = last_cut(gi) - first + 1;
     last_cta[tid] = atomicAdd(a.arrivals + first, 1) == others;
     if (last_cta[tid]) a.arrivals[first] = 0;
     __threadfence();
@@ -709,12 +732,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   for (int k = 0; k < 2; ++k) {
     if (shared_group[k] < 0 || !last_cta[k]) continue;
     const PieceInfo gi = info[shared_group[k]];
-    const int first = static_cast<int>(quotient(gi.group, span));
-    const int n = static_cast<int>(quotient(gi.group + gi.tiles - 1, span)) - first + 1;
+    const int first = first_cut(gi), n = last_cut(gi) - first + 2;
     for (int c = 0; c < gi.cols; ++c, ++item)
       if (item % kWarps == warp)
-        join_column([&](int x) { return a.pieces + static_cast<size_t>(x == 0 ? first * 2 + 1 : (first + x) * 2) * kPiece; },
-                    n, gi, c, nullptr);
+        join_column([&](int x) { return a.pieces + static_cast<size_t>((first + x) * 2 - (x == 0 ? 1 : 2)) * kPiece; },
+                    load_other, n, gi, c, nullptr);
   }
 }
 

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "lora_common.cuh"
+
 namespace lora {
 
 constexpr float kKvUnit = 32.f;  // decoded values times this are the cache's (before its scale)
@@ -122,6 +124,21 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Whether a barrier's phase is complete, without waiting.  A wait, even for a phase long complete,
+// takes about 160 cycles from its instruction to the branch on its result; asked for ahead of
+// other work, the answer costs nothing.
+__device__ __forceinline__ uint32_t mbar_peek(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+
 // a / b of non-negative values, in 32 bits where they fit (a 64-bit division takes longer than a
 // load from L2).
 __device__ __forceinline__ long long quotient(long long a, long long b) {

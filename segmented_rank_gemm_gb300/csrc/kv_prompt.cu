@@ -116,21 +116,6 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Whether a barrier's phase is complete, without waiting.  A wait, even for a phase long complete,
-// takes about 160 cycles from its instruction to the branch on its result; asked for ahead of
-// other work, the answer costs nothing.
-__device__ __forceinline__ uint32_t mbar_peek(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done;
-}
-
 // ---- requests, groups and the sequence of tiles ----
 struct Request {
   int row0, q_len, kv, rows, parts;  // rows of one head, groups of a head
