@@ -212,6 +212,20 @@ int set_batch_segments(lora_layer_t* layer, const int32_t* token_slot_dev, int T
 int lora_forward(lora_layer_t* layer, const void* x_dev, void* y_dev, int T, void* stream);
 
 /*
+ * lora_forward for a layer with an e4m3 base whose rows already come in e4m3, as
+ * lora_rms_norm (lora_norm.h) writes them: the base product uses these rows, and the layer
+ * does not quantise x (one launch and one read of x less).
+ *   x_dev   [T,K] bf16, what the low-rank product reads.
+ *   xq_dev  [T,K] e4m3 bytes, 16-byte aligned; sx_dev [T] fp32: row t is xq[t] * sx[t].
+ * xq and sx must not overlap y; they and x come from earlier work on `stream`.  With the rows
+ * that the layer's own quantiser gives for x, y is lora_forward's.
+ * Errors: as lora_forward; LORA_EINVAL for a layer without an e4m3 base, a null or misaligned
+ * xq or sx, or overlap with y.
+ */
+int lora_forward_e4m3(lora_layer_t* layer, const void* x_dev, const void* xq_dev,
+                      const float* sx_dev, void* y_dev, int T, void* stream);
+
+/*
  * The whole layer for callers holding host buffers: copies x_host [T,K] and
  * token_slot_host [T] to layer-owned device staging, runs set_batch_segments and
  * lora_forward, and copies y back to y_host [T,N].  All on `stream`, asynchronously:

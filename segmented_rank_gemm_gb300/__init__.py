@@ -8,14 +8,15 @@ has not been built: there is no CPU fallback.
 
 ``segmented_rank_gemm_gb300.kv`` (a paged 4-bit key/value cache, the attention over it, block
 tables and slot maps; ``include/lora_kv.h``) and ``segmented_rank_gemm_gb300.norm`` (the
-residual norm; ``include/lora_norm.h``) are the steps between a decoder block's projections.
+residual norm; ``include/lora_norm.h``) are the steps between a decoder block's projections;
+``segmented_rank_gemm_gb300.block`` runs them together.
 
 ``segmented_rank_gemm_gb300.workloads`` (seeded synthetic inputs) imports without the
 library.
 """
 import importlib
 
-__all__ = ["lora", "kv", "norm", "workloads", "build"]
+__all__ = ["lora", "kv", "norm", "block", "workloads", "build"]
 
 
 def __getattr__(name):

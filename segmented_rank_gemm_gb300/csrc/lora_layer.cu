@@ -562,21 +562,36 @@ static int run_builder(lora_layer_t* L, cudaStream_t stream) {
   return LORA_OK;
 }
 
-int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* stream_) {
-  if (!L) return LORA_EINVAL;
-  if (L->T_batch < 0) return fail(L, LORA_ESTATE, "lora_forward before set_batch_segments");
+// One forward of the current batch.  xq and sx: the caller's e4m3 rows of x with their scales
+// (lora_forward_e4m3), or null: the layer quantises x itself where its base is e4m3.
+static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, const float* sx,
+                         void* y_dev, int T, void* stream_, const char* name) {
+  if (L->T_batch < 0) return fail(L, LORA_ESTATE, "%s before set_batch_segments", name);
   if (T != L->T_batch)
     return fail(L, LORA_ESTATE, "T=%d differs from the batch's T=%d", T, L->T_batch);
   if (T == 0) return LORA_OK;
   if (!x_dev || !y_dev) return fail(L, LORA_EINVAL, "null x or y");
   const size_t es = L->esize;
-  const char* xb = static_cast<const char*>(x_dev);
   const char* yb = static_cast<const char*>(y_dev);
-  if (xb < yb + (size_t)T * L->N * es && yb < xb + (size_t)T * L->K * es)
-    return fail(L, LORA_EINVAL, "x and y overlap");
+  auto overlaps_y = [&](const void* p, size_t bytes) {
+    const char* b = static_cast<const char*>(p);
+    return b < yb + (size_t)T * L->N * es && yb < b + bytes;
+  };
+  if (overlaps_y(x_dev, (size_t)T * L->K * es)) return fail(L, LORA_EINVAL, "x and y overlap");
   if (L->dtype == LORA_BF16 &&
       (reinterpret_cast<uintptr_t>(x_dev) % 16 != 0 || reinterpret_cast<uintptr_t>(y_dev) % 16 != 0))
     return fail(L, LORA_EINVAL, "bf16 x and y must be 16-byte aligned");
+  // the caller's rows are read where they are, through a tensor map of their own (it travels
+  // in the launch's parameters, so nothing of it outlives this call)
+  CUtensorMap tmap_rows;
+  if (xq) {
+    if (overlaps_y(xq, (size_t)T * L->K) || overlaps_y(sx, (size_t)T * sizeof(float)))
+      return fail(L, LORA_EINVAL, "xq or sx and y overlap");
+    if (reinterpret_cast<uintptr_t>(xq) % 16 != 0 || reinterpret_cast<uintptr_t>(sx) % 4 != 0)
+      return fail(L, LORA_EINVAL, "xq must be 16-byte aligned, sx 4-byte");
+    LORA_CUDA(L, encode_tmap_u8(&tmap_rows, xq, T, L->K, kTcTileRows));
+  }
+  const bool quantise = L->fp8 && !xq;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   LORA_CUDA(L, wait_pending_loads(L, stream));
 
@@ -610,7 +625,7 @@ int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* s
     ba.err = L->err;
     ba.num_sms = L->num_sms;
     ba.per_column = L->percol_slots > 0;
-    if (L->fp8) {
+    if (quantise) {
       // e4m3 base: the row quantiser, launched ahead of the BGMV kernel, counts x's rows on
       // q_ready, which the GEMM's loads wait for and its last CTA resets.  A forward that
       // stopped between those launches left the count set: clear it first.
@@ -622,7 +637,7 @@ int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* s
     }
     LORA_CUDA(L, launch_bgmv_delta(ba, stream, &L->launches));
   } else if (bf16) {
-    if (L->fp8) {
+    if (quantise) {
       // e4m3 base: the rows quantised first (a programmatic launch; the shrink below waits
       // for it, and the GEMM's loads of xq wait for its row count)
       if (L->q_dirty) LORA_CUDA(L, cudaMemsetAsync(L->q_ready, 0, 2 * sizeof(int32_t), stream));
@@ -716,10 +731,12 @@ int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* s
   ga.force_cs = L->gemm_plan.ksplit;
   ga.force_pair = L->gemm_plan.pair;
   ga.fp8 = L->fp8;
-  ga.tmap_xq = L->fp8 ? &L->tmap_xq : nullptr;
-  ga.sx = L->sx;
+  ga.tmap_xq = xq ? &tmap_rows : L->fp8 ? &L->tmap_xq : nullptr;
+  ga.sx = xq ? sx : L->sx;
   ga.sw = L->sw;
-  ga.q_ready = L->fp8 ? L->q_ready : nullptr;
+  // the caller's rows were written before this call's first kernel starts, so nothing counts
+  // them: the GEMM's loads start as those of a bf16 x do
+  ga.q_ready = quantise ? L->q_ready : nullptr;
   ga.tmap_delta = L->delta ? &L->tmap_delta : nullptr;
   LORA_CUDA(L, trace_mark(L, 4, stream));
   if (bf16) {
@@ -729,7 +746,7 @@ int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* s
     LORA_CUDA(L, launch_gemm_simt_f32(ga, stream));
     ++L->launches;
   }
-  L->q_dirty = false;
+  if (quantise) L->q_dirty = false;
   LORA_CUDA(L, trace_mark(L, 5, stream));
 
   if (!is_capturing(stream)) {
@@ -737,6 +754,19 @@ int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* s
     L->have_forward = true;
   }
   return LORA_OK;
+}
+
+int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* stream) {
+  if (!L) return LORA_EINVAL;
+  return forward_batch(L, x_dev, nullptr, nullptr, y_dev, T, stream, "lora_forward");
+}
+
+int lora_forward_e4m3(lora_layer_t* L, const void* x_dev, const void* xq_dev, const float* sx_dev,
+                      void* y_dev, int T, void* stream) {
+  if (!L) return LORA_EINVAL;
+  if (!L->fp8) return fail(L, LORA_EINVAL, "lora_forward_e4m3 needs a layer with an e4m3 base");
+  if (T > 0 && (!xq_dev || !sx_dev)) return fail(L, LORA_EINVAL, "null xq or sx");
+  return forward_batch(L, x_dev, xq_dev, sx_dev, y_dev, T, stream, "lora_forward_e4m3");
 }
 
 int lora_forward_host(lora_layer_t* L, const void* x_host, const int32_t* token_slot_host,

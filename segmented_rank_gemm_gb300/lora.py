@@ -34,9 +34,10 @@ LAYER_FUNCTIONS = ("lora_layer_create", "lora_layer_create_pooled", "lora_layer_
                    "lora_get_pool_usage",
                    "load_adapter_slot", "load_adapter_slot_composed",
                    "unload_adapter_slot",
-                   "set_batch_segments", "lora_forward", "lora_forward_host", "lora_get_status",
-                   "lora_get_segments", "lora_set_trace_events", "lora_set_gemm_plan",
-                   "lora_last_error", "lora_layer_destroy", "lora_build_segments_static",
+                   "set_batch_segments", "lora_forward", "lora_forward_e4m3",
+                   "lora_forward_host", "lora_get_status", "lora_get_segments",
+                   "lora_set_trace_events", "lora_set_gemm_plan", "lora_last_error",
+                   "lora_layer_destroy", "lora_build_segments_static",
                    "lora_wait_selftest", "lora_get_launch_count")
 # every entry point declared in include/lora_kv.h
 KV_FUNCTIONS = ("lora_kv_maps", "lora_kv_release", "lora_kv_cache_create", "lora_kv_append",
@@ -87,6 +88,7 @@ def _load() -> ctypes.CDLL:
     L.unload_adapter_slot.argtypes = [vp, i32, vp]
     L.set_batch_segments.argtypes = [vp, vp, i32, vp]
     L.lora_forward.argtypes = [vp, vp, vp, i32, vp]
+    L.lora_forward_e4m3.argtypes = [vp, vp, vp, vp, vp, i32, vp]
     L.lora_forward_host.argtypes = [vp, vp, vp, vp, i32, vp]
     L.lora_get_status.argtypes = [vp, vp]
     L.lora_get_segments.argtypes = [vp, vp, vp, vp, vp, vp, vp]
@@ -260,6 +262,11 @@ def lora_forward(layer, x, y, T, stream=None) -> None:
     _check(layer, _lib.lora_forward(layer, _ptr(x), _ptr(y), T, _stream(stream)))
 
 
+def lora_forward_e4m3(layer, x, xq, sx, y, T, stream=None) -> None:
+    _check(layer, _lib.lora_forward_e4m3(layer, _ptr(x), _ptr(xq), _ptr(sx), _ptr(y), T,
+                                         _stream(stream)))
+
+
 def lora_forward_host(layer, x_host, token_slot_host, y_host, T, stream=None) -> None:
     _check(layer, _lib.lora_forward_host(layer, _ptr(x_host), _ptr(token_slot_host),
                                          _ptr(y_host), T, _stream(stream)))
@@ -364,7 +371,7 @@ class LoraLayer:
             raise ValueError("W must be a CUDA tensor")
         self.K, self.N = int(W.shape[0]), int(W.shape[1])
         self.num_slots, self.max_rank, self.max_tokens = num_slots, max_rank, max_tokens
-        self.dtype = W.dtype
+        self.dtype, self.fp8_base = W.dtype, fp8_base
         if fp8_base:
             if pool_rows or W.dtype != torch.bfloat16:
                 raise ValueError("an e4m3 base layer takes a bf16 W and no row pool")
@@ -417,6 +424,22 @@ class LoraLayer:
         if y is None:
             y = torch.empty(T, self.N, dtype=self.dtype, device=x.device)
         lora_forward(self.handle, x, y, T, stream)
+        return y
+
+    def forward_e4m3(self, x: torch.Tensor, xq: torch.Tensor, sx: torch.Tensor,
+                     y: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """forward with the base's e4m3 rows given: ``xq`` [T, K] bytes and ``sx`` [T], as
+        ``norm.rms_norm`` writes them; ``x`` feeds the low-rank product."""
+        T = int(x.shape[0])
+        for name, t, shape, ok in (("x", x, (T, self.K), (self.dtype,)),
+                                   ("xq", xq, (T, self.K), (torch.uint8, torch.float8_e4m3fn)),
+                                   ("sx", sx, (T,), (torch.float32,))):
+            if not t.is_cuda or t.dtype not in ok or tuple(t.shape) != shape \
+                    or not t.is_contiguous():
+                raise ValueError(f"{name} must be a dense CUDA tensor {shape} of {ok[0]}")
+        if y is None:
+            y = torch.empty(T, self.N, dtype=self.dtype, device=x.device)
+        lora_forward_e4m3(self.handle, x, xq, sx, y, T, stream)
         return y
 
     def __call__(self, x, token_slot, y=None, stream=None):
