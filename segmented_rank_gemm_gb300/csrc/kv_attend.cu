@@ -190,19 +190,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   const int g = lane >> 2, t = lane & 3;
   const int heads = a.pages.heads;
 
-  // rows of no request
-  {
-    const int lo = max(0, min(__ldg(a.q_offsets), a.T)), hi = max(0, min(__ldg(a.q_offsets + a.B), a.T));
-    const int words = a.q_heads * D / 8;  // 16-byte words of a row
-    const long long n = static_cast<long long>(lo + a.T - hi) * words;
-    for (long long i = blockIdx.x * kThreads + tid; i < n; i += gridDim.x * kThreads) {
-      int row = static_cast<int>(i / words);
-      if (row >= lo) row += hi - lo;
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(row) * a.ldo)[
-          i % words] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-
   // the sequence's length and this CTA's range; where each warp starts
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -227,6 +214,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     total += scan[w];
   }
   const long long span = max(static_cast<long long>(kMinSpan), quotient(total + gridDim.x - 1, gridDim.x));
+  // What came before wrote the lengths, but not as the kernel just ahead of this one if that one
+  // let this one start early (append does, the maps do not); q, the cache and `out` it may still
+  // be using.  The kernel for many rows needs nothing of this one's: it may start now, and waits
+  // for this one at its end.
+  griddep_wait();
+  if (a.many_follow) griddep_launch_dependents();
+
+  // rows of no request
+  {
+    const int lo = max(0, min(__ldg(a.q_offsets), a.T)), hi = max(0, min(__ldg(a.q_offsets + a.B), a.T));
+    const int words = a.q_heads * D / 8;  // 16-byte words of a row
+    const long long n = static_cast<long long>(lo + a.T - hi) * words;
+    for (long long i = blockIdx.x * kThreads + tid; i < n; i += gridDim.x * kThreads) {
+      int row = static_cast<int>(i / words);
+      if (row >= lo) row += hi - lo;
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(row) * a.ldo)[
+          i % words] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
   if (span * blockIdx.x >= total) return;
   const long long raw_lo = span * blockIdx.x, raw_hi = min(total, raw_lo + span);
   const int wspan = static_cast<int>((span + kWarps - 1) / kWarps), snap = wspan / 6;
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         float top = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          v[w] = off >= 0 ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+          v[w] = off >= 0 ? load_in_order(src + w) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
@@ -747,8 +754,7 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   cudaError_t e = ensure_smem_limit(kv_attend_kernel<D, NT>, smem, limit);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(kKvMaxCtas, a.num_sms * kCtasPerSm);
-  kv_attend_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kv_attend_kernel<D, NT>, dim3(ctas), kThreads, smem, stream, a);
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // kv_cache.cu -- the 4-bit key/value cache object, its write and its read-back, and the
 // argument checks of the attention over it (include/lora_kv.h).
+#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -12,6 +13,7 @@
 #include "lora_common.cuh"
 #include "lora_kernels.h"
 #include "lora_kv.h"
+#include "kv_decode.cuh"
 #include "kv_kernels.h"
 
 namespace lora {
@@ -23,98 +25,198 @@ __device__ __forceinline__ float e4m3_value(uint8_t b) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
-// One group of 16 dimensions of one token and head a thread: 32 bytes in, 8 bytes of codes
-// and one scale out.  Bound: bytes, and for small batches the launch.
-__global__ void __launch_bounds__(kThreads)
-    kv_append_kernel(KvPages pg, const __nv_bfloat16* __restrict__ k, int ldk,
-                     const __nv_bfloat16* __restrict__ v, int ldv,
-                     const int32_t* __restrict__ slots, int T, float k_scale, float v_scale,
-                     int32_t* err) {
-  const int groups = pg.heads * pg.D / kKvGroup;  // of a token, K or V
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long n = static_cast<long long>(T) * groups;
-  if (i >= 2 * n) return;
-  const bool is_v = i >= n;
-  const long long e = is_v ? i - n : i;
-  const int t = static_cast<int>(e / groups), hg = static_cast<int>(e % groups);
-  const int slot = slots[t];
-  if (static_cast<unsigned>(slot) >=
-      static_cast<unsigned>(pg.num_pages) << pg.page_shift) {
-    if (slot != -1 && hg == 0) atomicOr(err, LORA_ERRF_BAD_ID);
-    return;
-  }
-  const uint4* src = reinterpret_cast<const uint4*>(
-      (is_v ? v + static_cast<size_t>(t) * ldv : k + static_cast<size_t>(t) * ldk) + hg * kKvGroup);
-  const uint4 lo = __ldg(src), hi = __ldg(src + 1);
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  float x[16], top = 0.f;
+// A group of 16 dimensions of one token and head, of K and of V, a thread: twice 32 bytes of
+// values, 8 of codes and one scale.  Threads run along the token's row, so both directions move
+// whole lines.
+struct Group {
+  unsigned t;    // token
+  int hg;        // group of the token's row
+  int slot;
+  bool there;    // the slot is one of the cache's
+  uint8_t *k, *v, *k_scale, *v_scale;  // codes and scales
+};
+__device__ __forceinline__ Group locate(const KvPages& pg, const int32_t* slots, unsigned i,
+                                        unsigned groups) {
+  Group x;
+  x.t = i / groups;
+  x.hg = static_cast<int>(i - x.t * groups);
+  x.slot = load_in_order(slots + x.t);
+  x.there = static_cast<unsigned>(x.slot) < static_cast<unsigned>(pg.num_pages) << pg.page_shift;
+  const int per_log2 = pg.D == 128 ? 3 : 2;  // groups of a head
+  const int head = x.hg >> per_log2, group = x.hg & ((1 << per_log2) - 1);
+  const int pos = x.slot & ((1 << pg.page_shift) - 1), token = pos & (kKvBlock - 1);
+  uint8_t* blk = pg.base + pg.block(x.slot >> pg.page_shift, head, pos / kKvBlock);
+  x.k = blk + kv_k_code_at(pg.D, token, group * 8);
+  x.v = blk + kv_v_code_at(pg.D, token, group * 8);
+  x.k_scale = blk + kv_k_scale_at(pg.D, token, group);
+  x.v_scale = blk + kv_v_scale_at(pg.D, token, group);
+  return x;
+}
+
+// Codes of 16 values whose quotients by s round to -7 .. 7, y = 1 / s correctly rounded.  The
+// quotient is Markstein's: q = x y is corrected twice by its remainder, x - q s, exact in one
+// fused multiply-add once q is within one unit in the last place, which makes the last result the
+// correctly rounded x / s -- as a division, with one reciprocal for the group.  Adding
+// 1.5 2^23 rounds to an integer, ties to even, and leaves it in the low bits; a shifted add
+// puts it in its nibble, and what the sums carry besides is one constant.
+template <bool IS_V>
+__device__ __forceinline__ uint2 codes_of(const uint32_t (&w)[8], float s, float y) {
+  const float2 y2 = make_float2(y, y), minus_s = make_float2(-s, -s);
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  uint32_t code[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[2 * j] = bf16_lo(w[j]);
-    x[2 * j + 1] = bf16_hi(w[j]);
-    top = fmaxf(top, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));  // ignores NaN
+  for (int h = 0; h < 2; ++h) {
+    code[h] = 0x11111111u * (8u - 0x4B400000u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = make_float2(bf16_lo(w[4 * h + j]), bf16_hi(w[4 * h + j]));
+      float2 q = mul2(x, y2);
+      q = fma2(fma2(q, minus_s, x), y2, q);
+      q = fma2(fma2(q, minus_s, x), y2, q);
+      q = add2(q, magic);
+      code[h] += __float_as_uint(q.x) << (4 * kv_nibble(IS_V, 2 * j));
+      code[h] += __float_as_uint(q.y) << (4 * kv_nibble(IS_V, 2 * j + 1));
+    }
   }
-  const float g = is_v ? v_scale : k_scale;
+  return make_uint2(code[0], code[1]);
+}
+
+// Writes the group at src, of a cache of scale g.
+template <bool IS_V>
+__device__ __forceinline__ void write_group(const uint4 lo, const uint4 hi, float g, uint8_t* codes,
+                                            uint8_t* scale) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  // the largest magnitude; a NaN if there is one
+  __nv_bfloat162 top2 = __habs2(reinterpret_cast<const __nv_bfloat162&>(w[0]));
+#pragma unroll
+  for (int j = 1; j < 8; ++j)
+    top2 = __hmax2_nan(top2, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[j])));
+  float top = __bfloat162float(__hmax_nan(top2.x, top2.y));
+  const bool nan = top != top;
+  if (nan) {
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+  }
   const uint8_t sb = static_cast<uint8_t>(
       __nv_cvt_float_to_fp8(__fdiv_rn(top, 7.f * g), __NV_SATFINITE, __NV_E4M3));
   const float s = e4m3_value(sb) * g;
-  uint32_t code[2] = {0u, 0u};
+  const float y = __frcp_rn(s);
+  uint2 code;
+  // (the range keeps every product and remainder of a quotient from a half up a normal number)
+  if (!nan && s > 0x1p-60f && s < 0x1p60f && top * y < 7.49f) {
+    code = codes_of<IS_V>(w, s, y);
+  } else {  // zeros, saturated scales, the smallest scales, NaN: division and clamp by element
+    code = make_uint2(0u, 0u);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float q = s > 0.f ? rintf(__fdiv_rn(x[j], s)) : 0.f;
-    q = q != q ? 0.f : fminf(fmaxf(q, -7.f), 7.f);
-    code[j >> 3] |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * kv_nibble(is_v, j & 7));
+    for (int j = 0; j < 16; ++j) {
+      const float x = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+      float q = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+      q = q != q ? 0.f : fminf(fmaxf(q, -7.f), 7.f);
+      (j < 8 ? code.x : code.y) |= static_cast<uint32_t>(static_cast<int>(q) + 8)
+                                   << (4 * kv_nibble(IS_V, j & 7));
+    }
   }
-  const int per_head = pg.D / kKvGroup;
-  const int head = hg / per_head, group = hg % per_head;
-  const int page = slot >> pg.page_shift, pos = slot & ((1 << pg.page_shift) - 1);
-  const int token = pos & (kKvBlock - 1);
-  uint8_t* blk = pg.base + pg.block(page, head, pos / kKvBlock);
-  const int at = is_v ? kv_v_code_at(pg.D, token, group * 8) : kv_k_code_at(pg.D, token, group * 8);
-  *reinterpret_cast<uint2*>(blk + at) = make_uint2(code[0], code[1]);
-  blk[is_v ? kv_v_scale_at(pg.D, token, group) : kv_k_scale_at(pg.D, token, group)] = sb;
+  *reinterpret_cast<uint2*>(codes) = code;
+  *scale = sb;
+}
+
+// Bound: bytes, and for small batches the launch.
+__global__ void __launch_bounds__(kThreads)
+    kv_append_kernel(KvPages pg, const __nv_bfloat16* k, int ldk, const __nv_bfloat16* v, int ldv,
+                     const int32_t* slots, int T, float k_scale, float v_scale, int32_t* err) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const unsigned groups = pg.heads * pg.D / kKvGroup;  // of a token's row
+  const unsigned i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= T * groups) return;
+  const Group at = locate(pg, slots, i, groups);
+  const uint4* ks =
+      reinterpret_cast<const uint4*>(k + static_cast<size_t>(at.t) * ldk + at.hg * kKvGroup);
+  const uint4* vs =
+      reinterpret_cast<const uint4*>(v + static_cast<size_t>(at.t) * ldv + at.hg * kKvGroup);
+  const uint4 k0 = load_in_order(ks), k1 = load_in_order(ks + 1);
+  const uint4 v0 = load_in_order(vs), v1 = load_in_order(vs + 1);
+  if (!at.there) {
+    if (at.slot != -1 && at.hg == 0) atomicOr(err, LORA_ERRF_BAD_ID);
+    return;
+  }
+  write_group<false>(k0, k1, k_scale, at.k, at.k_scale);
+  write_group<true>(v0, v1, v_scale, at.v, at.v_scale);
+}
+
+// Values n s g of a group: n s is exact in bf16 (kv_decode.cuh), so a cache of scale 1 gives it
+// as it is.
+template <bool IS_V>
+__device__ __forceinline__ void values_of(uint2 c, uint32_t sb, float g, uint32_t (&out)[8]) {
+  const DecodeBf16 dec = decode_scale_bf16(sb, 0, 0x7B807B80u);  // 2^120
+  uint32_t lo[4], hi[4];  // pairs of nibbles i and i + 4
+  decode4(c.x, dec, lo);
+  decode4(c.y, dec, hi);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (IS_V) {  // dimensions i and i + 4
+      out[j] = prmt(lo[2 * (j & 1)], lo[2 * (j & 1) + 1], j < 2 ? 0x5410 : 0x7632);
+      out[4 + j] = prmt(hi[2 * (j & 1)], hi[2 * (j & 1) + 1], j < 2 ? 0x5410 : 0x7632);
+    } else {  // dimensions 2 i and 2 i + 1
+      out[j] = lo[j];
+      out[4 + j] = hi[j];
+    }
+  }
+  if (g != 1.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = pack_bf16x2(bf16_lo(out[j]) * g, bf16_hi(out[j]) * g);
+  }
+}
+
+// Stores the 32 bytes of group i and, by the neighbour lane, of group i ^ 1, so that a store
+// covers whole sectors: the lanes of a pair exchange halves, and write first the even lane's
+// group, then the odd one's.
+__device__ __forceinline__ void store_pair(uint4* rows, unsigned i, unsigned n,
+                                           const uint32_t (&x)[8]) {
+  const bool odd = i & 1;
+  uint32_t give[4], first[4], second[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) give[j] = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[4 + j], 1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    first[j] = odd ? give[j] : x[j];
+    second[j] = odd ? x[4 + j] : give[j];
+  }
+  const unsigned even = i & ~1u;
+  uint4* dst = rows + static_cast<size_t>(even) * 2 + odd;
+  if (even < n) dst[0] = make_uint4(first[0], first[1], first[2], first[3]);
+  if (even + 1 < n) dst[2] = make_uint4(second[0], second[1], second[2], second[3]);
 }
 
 __global__ void __launch_bounds__(kThreads)
-    kv_read_kernel(KvPages pg, const int32_t* __restrict__ slots, int T, float k_scale,
-                   float v_scale, __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v,
-                   int32_t* err) {
-  const int groups = pg.heads * pg.D / kKvGroup;
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long n = static_cast<long long>(T) * groups;
-  if (i >= 2 * n) return;
-  const bool is_v = i >= n;
-  const long long e = is_v ? i - n : i;
-  const int t = static_cast<int>(e / groups), hg = static_cast<int>(e % groups);
-  const int slot = slots[t];
-  uint32_t out[8] = {};
-  if (static_cast<unsigned>(slot) < static_cast<unsigned>(pg.num_pages) << pg.page_shift) {
-    const int per_head = pg.D / kKvGroup;
-    const int head = hg / per_head, group = hg % per_head;
-    const int page = slot >> pg.page_shift, pos = slot & ((1 << pg.page_shift) - 1);
-    const int token = pos & (kKvBlock - 1);
-    const uint8_t* blk = pg.base + pg.block(page, head, pos / kKvBlock);
-    const int at =
-        is_v ? kv_v_code_at(pg.D, token, group * 8) : kv_k_code_at(pg.D, token, group * 8);
-    const uint2 c = *reinterpret_cast<const uint2*>(blk + at);
-    const uint8_t sb =
-        blk[is_v ? kv_v_scale_at(pg.D, token, group) : kv_k_scale_at(pg.D, token, group)];
-    const float s = e4m3_value(sb), g = is_v ? v_scale : k_scale;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t word = j < 4 ? c.x : c.y;
-      const int i = 2 * (j & 3);
-      const float a = static_cast<float>(static_cast<int>(word >> (4 * kv_nibble(is_v, i)) & 15) - 8);
-      const float b = static_cast<float>(static_cast<int>(word >> (4 * kv_nibble(is_v, i + 1)) & 15) - 8);
-      out[j] = pack_bf16x2(a * s * g, b * s * g);
+    kv_read_kernel(KvPages pg, const int32_t* slots, int T, float k_scale, float v_scale,
+                   __nv_bfloat16* k, __nv_bfloat16* v, int32_t* err) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const unsigned groups = pg.heads * pg.D / kKvGroup;
+  const unsigned i = blockIdx.x * kThreads + threadIdx.x, n = T * groups;
+  uint32_t kv[8] = {}, vv[8] = {};
+  if (i < n) {
+    const Group at = locate(pg, slots, i, groups);
+    if (at.there) {
+      const uint2 kc = load_in_order(reinterpret_cast<const uint2*>(at.k));
+      const uint2 vc = load_in_order(reinterpret_cast<const uint2*>(at.v));
+      const uint32_t ks = load_in_order(at.k_scale), vs = load_in_order(at.v_scale);
+      values_of<false>(kc, ks, k_scale, kv);
+      values_of<true>(vc, vs, v_scale, vv);
+    } else if (at.slot != -1 && at.hg == 0) {
+      atomicOr(err, LORA_ERRF_BAD_ID);
     }
-  } else if (slot != -1 && hg == 0) {
-    atomicOr(err, LORA_ERRF_BAD_ID);
   }
-  uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + static_cast<size_t>(t) * groups * kKvGroup +
-                                        hg * kKvGroup);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  store_pair(reinterpret_cast<uint4*>(k), i, n, kv);
+  store_pair(reinterpret_cast<uint4*>(v), i, n, vv);
+}
+
+// Blocks over the groups of T rows.
+dim3 rows_grid(const KvPages& pg, int T) {
+  const long long n = static_cast<long long>(T) * (pg.heads * pg.D / kKvGroup);
+  return dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads));
 }
 
 }  // namespace
@@ -230,12 +332,11 @@ int lora_kv_append(lora_kv_cache_t* c, const void* k, int ldk, const void* v, in
   if (T == 0) return LORA_OK;
   if (!k || !v || !slots || !aligned16(k) || !aligned16(v))
     return fail(c, LORA_EINVAL, "k, v and kv_slot must be given, k and v 16-byte aligned");
-  const long long n = 2LL * T * (width / kKvGroup);
-  kv_append_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0,
-                     static_cast<cudaStream_t>(stream)>>>(
-      c->pages, static_cast<const __nv_bfloat16*>(k), ldk, static_cast<const __nv_bfloat16*>(v), ldv,
-      slots, T, c->k_scale, c->v_scale, c->err);
-  KV_CUDA(c, cudaGetLastError());
+  KV_CUDA(c, launch_dependent(kv_append_kernel, rows_grid(c->pages, T), kThreads, 0,
+                              static_cast<cudaStream_t>(stream), c->pages,
+                              static_cast<const __nv_bfloat16*>(k), ldk,
+                              static_cast<const __nv_bfloat16*>(v), ldv, slots, T, c->k_scale,
+                              c->v_scale, c->err));
   return LORA_OK;
 }
 
@@ -246,12 +347,10 @@ int lora_kv_read(lora_kv_cache_t* c, const int32_t* slots, int T, void* k_out, v
   if (T == 0) return LORA_OK;
   if (!slots || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
     return fail(c, LORA_EINVAL, "kv_slot and outputs must be given, outputs 16-byte aligned");
-  const long long n = 2LL * T * (c->pages.heads * c->pages.D / kKvGroup);
-  kv_read_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0,
-                   static_cast<cudaStream_t>(stream)>>>(
-      c->pages, slots, T, c->k_scale, c->v_scale, static_cast<__nv_bfloat16*>(k_out),
-      static_cast<__nv_bfloat16*>(v_out), c->err);
-  KV_CUDA(c, cudaGetLastError());
+  KV_CUDA(c, launch_dependent(kv_read_kernel, rows_grid(c->pages, T), kThreads, 0,
+                              static_cast<cudaStream_t>(stream), c->pages, slots, T, c->k_scale,
+                              c->v_scale, static_cast<__nv_bfloat16*>(k_out),
+                              static_cast<__nv_bfloat16*>(v_out), c->err));
   return LORA_OK;
 }
 
@@ -304,8 +403,9 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.prompt_arrivals = c->arrivals + kKvMaxCtas;
   a.err = c->err;
   a.num_sms = c->num_sms;
+  a.many_follow = static_cast<long long>(max_q) * a.group > kFewRows;
   KV_CUDA(c, launch_kv_attend(a, static_cast<cudaStream_t>(stream)));
-  if (static_cast<long long>(max_q) * (q_heads / heads) > kFewRows)
+  if (a.many_follow)
     KV_CUDA(c, launch_kv_prompt(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;
 }

@@ -970,6 +970,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   __syncthreads();
   tc_fence_after();
   if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+  // the kernel for few rows, ahead of this one, may still be at work: what follows in the stream
+  // waits for this one alone
+  griddep_wait();
 }
 
 template <int D>
@@ -977,8 +980,8 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   static int limit[kAttrDevices] = {};
   cudaError_t e = ensure_smem_limit(kv_prompt_kernel<D>, Smem<D>::kBytes, limit);
   if (e != cudaSuccess) return e;
-  kv_prompt_kernel<D><<<std::min(kKvMaxCtas, a.num_sms), kThreads, Smem<D>::kBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kv_prompt_kernel<D>, dim3(std::min(kKvMaxCtas, a.num_sms)), kThreads,
+                          Smem<D>::kBytes, stream, a);
 }
 
 }  // namespace

@@ -118,6 +118,34 @@ def test_cached_values_are_exact(D, page, hkv, g):
     cache.close()
 
 
+@pytest.mark.parametrize("g", [1.0, 0.013, 1 / 3, 1.9, 3e-30, 5e30, 2e-38])
+def test_quotients_at_every_tie(g):
+    # values on and beside the half codes of scales of every size: n + 1/2 times the scale in bf16,
+    # one bf16 step to both sides of it, and random ones
+    from segmented_rank_gemm_gb300.kv import KvCache
+    rng = np.random.default_rng(17)
+    D, hkv, T = 128, 1, 2048
+    top = (7.0 * g * np.exp2(rng.uniform(-8, 8, (T, D // 16, 1)))).astype(np.float32)
+    scale = ref.to_e4m3(top / (np.float32(7) * np.float32(g))) * g
+    x = scale * (rng.integers(-7, 7, (T, D // 16, 16)) + 0.5)
+    x = torch.from_numpy(x.astype(np.float32)).bfloat16()
+    x = (x.view(torch.int16) + torch.from_numpy(rng.integers(-1, 2, x.shape).astype(np.int16))).view(
+        torch.bfloat16)
+    some = torch.from_numpy(rng.random(x.shape) < 0.2)
+    x = torch.where(some, torch.from_numpy((top * rng.uniform(-1, 1, x.shape)).astype(np.float32)).bfloat16(), x)
+    x[:, :, 3] = torch.from_numpy(top[:, :, 0]).bfloat16()
+    x = x.reshape(T, hkv, D)
+    cache = KvCache(T // 16, 16, hkv, D, 1, g, g)
+    slots = _ints(rng.permutation(T))
+    cache.append(x.to(DEV), x.flip(-1).contiguous().to(DEV), slots)
+    gk, gv = cache.read(slots)
+    assert cache.status() == 0
+    for got, y in ((gk, x), (gv, x.flip(-1))):
+        want = torch.from_numpy(ref.held(_np(y), g).astype(np.float32)).bfloat16()
+        assert torch.equal(got.cpu(), want)
+    cache.close()
+
+
 GROUPS = 16
 
 
