@@ -303,12 +303,12 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
       cudaMalloc(&c->pieces, floats * sizeof(float)) != cudaSuccess ||
       cudaMalloc(&c->prompt_pieces, kv_prompt_workspace_floats(c->num_sms, head_dim) *
                                         sizeof(float)) != cudaSuccess ||
-      cudaMalloc(&c->arrivals, 2 * kKvMaxCtas * sizeof(int32_t)) != cudaSuccess ||
+      cudaMalloc(&c->arrivals, (2 * kKvMaxCtas + 2) * sizeof(int32_t)) != cudaSuccess ||
       cudaMalloc(&c->err, sizeof(int32_t)) != cudaSuccess) {
     cudaGetLastError();
     rc = LORA_ENOMEM;
   } else if (cudaMemsetAsync(c->pages.base, 0, c->bytes, stream) != cudaSuccess ||
-             cudaMemsetAsync(c->arrivals, 0, 2 * kKvMaxCtas * sizeof(int32_t), stream) != cudaSuccess ||
+             cudaMemsetAsync(c->arrivals, 0, (2 * kKvMaxCtas + 2) * sizeof(int32_t), stream) != cudaSuccess ||
              cudaMemsetAsync(c->err, 0, sizeof(int32_t), stream) != cudaSuccess ||
              cudaStreamSynchronize(stream) != cudaSuccess) {
     rc = LORA_ECUDA;
@@ -401,6 +401,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.few_rows = kFewRows;
   a.prompt_pieces = c->prompt_pieces;
   a.prompt_arrivals = c->arrivals + kKvMaxCtas;
+  a.prompt_claim = c->arrivals + 2 * kKvMaxCtas;
   a.err = c->err;
   a.num_sms = c->num_sms;
   a.many_follow = static_cast<long long>(max_q) * a.group > kFewRows;

@@ -106,6 +106,7 @@ struct KvAttendArgs {
   int many_follow;  // that kernel is launched next
   float* prompt_pieces;      // that kernel's workspaces
   int32_t* prompt_arrivals;  // [kKvMaxCtas] (zeroed)
+  int32_t* prompt_claim;     // groups claimed, CTAs done claiming (zeroed)
   int32_t* err;
   int num_sms;
 };

@@ -26,8 +26,11 @@
 // product takes 256 (PV) or 384 (QK).  With three S, the next one is under way when a softmax has
 // read its own, and with P beside S rather than in its place no QK waits for a PV.
 //
-// Work split: the tiles of all groups form one sequence, cut into equal ranges for the CTAs; a cut
-// near a group's edge moves there.  A group that is still cut leaves pieces (m, l, O), joined in
+// Work split: a CTA claims a group at a time, larger ones first, which leaves the CTAs within about
+// a small group of one another whatever the lengths are, and every group to one CTA: results do not
+// depend on the order.  Where the largest group alone would outlast that (few groups, long
+// contexts), the tiles of all groups form one sequence instead, cut into equal ranges for the CTAs; a
+// cut near a group's edge moves there.  A group that is still cut leaves pieces (m, l, O), joined in
 // order by the last CTA to arrive.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,6 +51,7 @@ constexpr int kTile = 64;       // positions of a tile
 constexpr int kStages = 3;      // decoded tiles of K, and of V
 constexpr int kRaw = 3;         // packed tiles
 constexpr int kSetup = 6;       // units a group counts before its tiles: what its change costs
+constexpr int kPieces = 15;     // units that the pieces of a group cut in two cost
 // A cut this near to a group's edge moves there: a group cut in two costs its CTAs about as much as
 // this many tiles, as long as that is little of a range.
 __device__ __forceinline__ int snap_of(long long span) {
@@ -154,6 +158,28 @@ __device__ __forceinline__ long long head_units(const KvAttendArgs& a, const Req
   long long n = 0;
   for (int part = lane; part < r.parts; part += 32) n += part_units(a, r, part);
   return warp_sum(n);
+}
+
+// The first of a request's groups (their tiles grow with the part) of at least `tiles` tiles;
+// r.parts if there is none.
+__device__ __forceinline__ int first_part(const KvAttendArgs& a, const Request& r, int tiles) {
+  if (tiles <= 1) return 0;
+  // its last row's token sees position kTile (tiles - 1)
+  const long long token = static_cast<long long>(kTile) * (tiles - 1) - (r.kv - r.q_len);
+  if (token <= 0) return 0;
+  if (token >= r.q_len) return r.parts;
+  return static_cast<int>(token) * a.group / kRows;
+}
+// Groups are dealt whole in kBuckets classes of size, the largest first: the least tiles of class i
+// when the largest group has `most`.
+constexpr int kBuckets = 4;
+__device__ __forceinline__ int bucket_least(int most, int i) {
+  return i == kBuckets - 1 ? 1 : (most * (kBuckets - 1 - i) + kBuckets - 1) / kBuckets;
+}
+// Parts [lo, hi) of a request are in class i.
+__device__ __forceinline__ int2 bucket_parts(const KvAttendArgs& a, const Request& r, int most, int i) {
+  return make_int2(first_part(a, r, bucket_least(most, i)),
+                   i == 0 ? r.parts : first_part(a, r, bucket_least(most, i - 1)));
 }
 
 // A position in the sequence of tiles, and the tile's unit.
@@ -294,12 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   __shared__ uint32_t tmem_holder;
   __shared__ long long scan[kThreads / 32], cut_rem[2];
   __shared__ int cut_b[2];
+  __shared__ int warp_most[kThreads / 32], bucket_count[kBuckets][kThreads / 32];
   __shared__ int last_cta;
   __shared__ float2 row_join[kRows];  // of a shared group's rows: max m, factor of O
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.pages.heads, G = a.group;
 
+  int job = 0;  // the first group to claim, asked for early
+  if (warp == 15 && lane == 0) job = atomicAdd(a.prompt_claim, 1);
   if (warp == 12) tmem_alloc(&tmem_holder, kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < kSegments; ++i) mbar_init(&bar.seg_full[i], 1), mbar_init(&bar.seg_empty[i], kSegmentReaders);
@@ -323,9 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   // with many groups are summed by its warp.
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  int most = 0;  // tiles of the largest group
   const auto request_units = [&](int b, bool mine) {  // of request b (mine), by all lanes
     Request r = {};
     if (mine) r = load_request(a, b);
+    if (r.parts) most = max(most, group_tiles(a, r, r.parts - 1));
     long long n = 0;
     if (r.parts <= 4)
       for (int part = 0; part < r.parts; ++part) n += part_units(a, r, part);
@@ -350,6 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     if (lane >= d) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) warp_most[warp] = most;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -359,11 +392,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
+    most = max(most, warp_most[w]);
   }
   const long long span = max(static_cast<long long>(kSetup + 4), quotient(total + gridDim.x - 1, gridDim.x));
   const int snap = snap_of(span);
+  // Whole groups, claimed one by one, unless the largest would outlast the rest by more than its
+  // cutting costs.
+  const bool whole = most + kSetup <= span + kPieces;
+  if (whole) {
 #pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBuckets; ++i) {
+      int n = 0;
+      for (int b = b0; b < b1; ++b) {
+        const int2 parts = bucket_parts(a, load_request(a, b), most, i);
+        n += (parts.y - parts.x) * heads;
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) bucket_count[i][warp] = n;
+    }
+  }
+#pragma unroll 1
+  for (int i = 0; i < (whole ? 0 : 2); ++i) {
     const long long at = span * (blockIdx.x + i);
     const bool here = at >= before && at < before + mine;
     if (!__any_sync(0xffffffffu, here)) continue;
@@ -896,7 +945,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const uint32_t bytes = step / kKvBlock * kv_block_bytes(D);
     Walk walk;
     bool some = false;
-    if (span * blockIdx.x < total) {
+    // Whole groups: a lane's two counts of a warp's requests in a class, classes first, and the
+    // groups up to them.
+    static_assert(kBuckets * (kThreads / 32) == 64, "two counts a lane");
+    const int* const counts = &bucket_count[0][0];
+    const int count0 = whole ? counts[2 * lane] : 0, count1 = whole ? counts[2 * lane + 1] : 0;
+    const auto scan_lanes = [&](int v) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += x;
+      }
+      return v;
+    };
+    const int upto = scan_lanes(count0 + count1);
+    // The job-th group, for every lane.
+    const auto take = [&]() {
+      job = __shfl_sync(0xffffffffu, job, 0);
+      unsigned beyond = __ballot_sync(0xffffffffu, job < upto);
+      if (!beyond) return false;
+      int k = __ffs(beyond) - 1;
+      int rem = job - __shfl_sync(0xffffffffu, upto - count0 - count1, k);
+      const int c0 = __shfl_sync(0xffffffffu, count0, k);
+      int entry = 2 * k;
+      if (rem >= c0) rem -= c0, ++entry;
+      const int bucket = entry / (kThreads / 32), first = entry % (kThreads / 32) * 32;
+      // the thread of that warp whose requests have it, then the request
+      const int x0 = min((first + lane) * per, a.B), x1 = min(x0 + per, a.B);
+      int n = 0;
+      for (int b = x0; b < x1; ++b) {
+        const int2 parts = bucket_parts(a, load_request(a, b), most, bucket);
+        n += (parts.y - parts.x) * heads;
+      }
+      const int incl = scan_lanes(n);
+      k = __ffs(__ballot_sync(0xffffffffu, rem < incl)) - 1;
+      rem -= __shfl_sync(0xffffffffu, incl - n, k);
+      Cursor& c = walk.at;
+      int2 parts;
+      for (c.b = (first + k) * per;; ++c.b) {
+        c.r = load_request(a, c.b);
+        parts = bucket_parts(a, c.r, most, bucket);
+        n = (parts.y - parts.x) * heads;
+        if (rem < n) break;
+        rem -= n;
+      }
+      c.head = rem / (parts.y - parts.x);
+      c.part = parts.y - 1 - (rem - c.head * (parts.y - parts.x));
+      c.tile = 0;
+      c.unit = 0;
+      c.tiles = walk.count = group_tiles(a, c.r, c.part);
+      return true;
+    };
+    if (whole) {
+      some = take();
+    } else if (span * blockIdx.x < total) {
       walk.end = total;
       if (span * (blockIdx.x + 1) < total) {
         walk.at.start(a, cut_b[1], cut_rem[1], span * (blockIdx.x + 1), snap, lane);
@@ -958,7 +1060,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
         }
         id = next_id;
       }
-      if (ok) some = walk.next(a);
+      if (!ok) break;
+      if (whole) {
+        if (lane == 0) job = atomicAdd(a.prompt_claim, 1);
+        some = take();
+      } else {
+        some = walk.next(a);
+      }
+    }
+    // the last CTA to have claimed sets the counts back
+    if (lane == 0) {
+      __threadfence();
+      if (atomicAdd(a.prompt_claim + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+        a.prompt_claim[0] = 0;
+        a.prompt_claim[1] = 0;
+      }
     }
     // copies in flight write this CTA's memory: every one issued has landed when its slot's
     // barrier has turned

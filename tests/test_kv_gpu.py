@@ -218,6 +218,34 @@ def test_prompt_of_some_length():
     _close(out, s.expected(q, new, 128 ** -0.5), np.abs(s.hv).max())
 
 
+@pytest.mark.parametrize("D,G,kv,new", [
+    (128, 4, [6000], [70]), (128, 8, [300, 9000, 5, 2600], [300, 33, 5, 40]),
+    (64, 4, [20000, 64], [9, 64]), (128, 1, [4000, 3000, 3500], [300, 17, 260])])
+def test_long_prompts_are_cut_and_joined(D, G, kv, new):
+    # few groups over long contexts: a group's tiles are shared by several CTAs
+    s = Setup(kv, D, 1, 64, seed=21)
+    q = s.queries(new, G)
+    out = s.attend(q.to(DEV), new)
+    assert s.cache.status() == 0
+    _close(out, s.expected(q, new, D ** -0.5), np.abs(s.hv).max())
+    assert torch.equal(out, s.attend(q.to(DEV), new))
+
+
+@pytest.mark.parametrize("B,hi,top", [(12, 400, 1500), (700, 12, 120), (2100, 8, 40)])
+def test_prompts_of_many_lengths(B, hi, top):
+    # groups of very different sizes, requests of few rows and none between them, more requests
+    # than a CTA has threads
+    rng = np.random.default_rng(B)
+    new = [int(n) for n in rng.integers(0, hi + 1, B)]
+    kv = [n + int(rng.integers(0, top)) for n in new]
+    s = Setup(kv, 64, 2, 32, seed=22)
+    q = s.queries(new, 4)
+    out = s.attend(q.to(DEV), new)
+    assert s.cache.status() == 0
+    _close(out, s.expected(q, new, 0.125), np.abs(s.hv).max())
+    assert torch.equal(out, s.attend(q.to(DEV), new))
+
+
 @pytest.mark.parametrize("kv", [[60000], [1, 50000, 3, 17000]])
 def test_long_contexts_are_split_and_joined(kv):
     s = Setup(kv, 128, 1, 64, seed=5, spread=1.5)
