@@ -755,15 +755,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (g.rows > 128) mbar_arrive(&bar.q_full[1]);
     };
     while (next_segment(g)) {
-      // The queries: the first segment's asked for at once, later ones behind two tiles, when the
-      // products with those before are about done; handed over a tile later (which needs no
-      // product with them: three tiles fit the stages).
-      const int q_before = seg == 1 ? 0 : min(2, g.count);
+      // The queries: asked for as soon as the products with those before are seen to be done, and
+      // behind two tiles at the latest (which need no product with them: three tiles fit the
+      // stages); handed over a tile later.
+      const int q_last = seg == 1 ? 0 : min(2, g.count);
+      bool asked = false, handed = false;
+      const auto hand_once = [&]() {
+        if (asked && !handed) hand_q();
+        handed = asked;
+      };
       for (int j = 0; j <= g.count; ++j) {
-        if (j == q_before) ask_q();
+        hand_once();
+        if (!asked && (j == q_last || __any_sync(0xffffffffu, mbar_peek(&bar.q_free, seg & 1)))) {
+          ask_q();
+          asked = true;
+        }
         if (!ok) break;
-        if (j == q_before + 1 || (j == g.count && j == q_before)) hand_q();
-        if (j == g.count) break;
+        if (j == g.count) {
+          hand_once();
+          break;
+        }
         const int stage = n % kStages, parity = (n / kStages) & 1, slot = n % kRaw;
         const uint32_t raw_there = mbar_peek(&bar.raw_full[slot], (n / kRaw) & 1),
                        k_free = mbar_peek(&bar.k_empty[stage], parity ^ 1),
