@@ -48,7 +48,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;    // positions of a tile
 constexpr int kStages = 3;   // tiles of a warp's ring
 constexpr int kSetup = 2;    // units a group counts before its tiles
-constexpr int kMinSpan = 8;  // units of a CTA's range, at least
+constexpr int kMinSpan = 4;  // units of a CTA's range, at least
 constexpr int kCtasPerSm = 2;
 constexpr float kRef = 6.f;    // p is 2^kRef at the reference
 constexpr float kSlack = 8.f;  // how far (in powers of two) a score may exceed the reference

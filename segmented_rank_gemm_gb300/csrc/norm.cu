@@ -8,8 +8,9 @@
 // between its load and its stores.
 //
 // Bound: DRAM bytes (x, r, w in; h, y, xq, sx out).  A row is shared by TPR threads with VEC
-// 16-byte vectors each, all loaded before the reduction; rows of up to 8 vectors a warp lane
-// stay within a warp and need no barrier.
+// 16-byte vectors each, all loaded before the reduction; rows of up to 4 vectors a warp lane
+// stay within a warp and need no barrier.  Measured: 8192 rows of 4096 in bf16 with everything
+// written 47.6 us, 6.3 TB/s; 512 rows 4.5 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -69,6 +70,17 @@ struct Chunk<float, 4> {
   }
 };
 template <>
+struct Chunk<__nv_bfloat16, 2> {
+  static __device__ __forceinline__ void load(const void* p, size_t i, float (&f)[2]) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + i);
+    f[0] = bf16_lo(v);
+    f[1] = bf16_hi(v);
+  }
+  static __device__ __forceinline__ void store(void* p, size_t i, const float (&f)[2]) {
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p) + i) = pack_bf16x2(f[0], f[1]);
+  }
+};
+template <>
 struct Chunk<__nv_bfloat16, 1> {
   static __device__ __forceinline__ void load(const void* p, size_t i, float (&f)[1]) {
     f[0] = __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -92,6 +104,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[VW], flo
                                            bool fast) {
   if constexpr (VW == 1) {
     *p = static_cast<uint8_t>(to_e4m3x2(f[0], 0.f, s, r, fast) & 0xff);
+  } else if constexpr (VW == 2) {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(to_e4m3x2(f[0], f[1], s, r, fast));
   } else {
     uint32_t q[VW / 4];
 #pragma unroll
@@ -115,7 +129,7 @@ __global__ void __launch_bounds__(NT) rms_norm_kernel(NormArgs a) {
   const size_t x0 = static_cast<size_t>(row) * a.ldx, r0 = static_cast<size_t>(row) * a.ldr;
   const size_t h0 = static_cast<size_t>(row) * a.ldh, y0 = static_cast<size_t>(row) * a.K;
 
-  float h[VEC][VW], w[VEC][VW];
+  float h[VEC][VW];  // then h w
   float sum = 0.f, top = 0.f;
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
@@ -143,13 +157,14 @@ __global__ void __launch_bounds__(NT) rms_norm_kernel(NormArgs a) {
   for (int c = 0; c < VEC; ++c) {
     const int e = lane + c * TPR;
     if (e < n) {
-      C::load(a.w, static_cast<size_t>(e) * VW, w[c]);
+      float w[VW];
+      C::load(a.w, static_cast<size_t>(e) * VW, w);
       if (a.h) C::store(a.h, h0 + static_cast<size_t>(e) * VW, h[c]);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         sum += h[c][j] * h[c][j];
-        w[c][j] *= h[c][j];  // h w
-        top = fmaxf(top, fabsf(w[c][j]));
+        h[c][j] *= w[j];
+        top = fmaxf(top, fabsf(h[c][j]));
       }
     }
   }
@@ -181,10 +196,10 @@ __global__ void __launch_bounds__(NT) rms_norm_kernel(NormArgs a) {
     const int e = lane + c * TPR;
     if (e < n) {
 #pragma unroll
-      for (int j = 0; j < VW; ++j) w[c][j] *= rstd;  // y
+      for (int j = 0; j < VW; ++j) h[c][j] *= rstd;  // y
       const size_t at = y0 + static_cast<size_t>(e) * VW;
-      if (a.y) C::store(a.y, at, w[c]);
-      if (a.xq) store_e4m3<VW>(a.xq + at, w[c], s, rcp, fast);
+      if (a.y) C::store(a.y, at, h[c]);
+      if (a.xq) store_e4m3<VW>(a.xq + at, h[c], s, rcp, fast);
     }
   }
 }
@@ -196,21 +211,33 @@ cudaError_t launch(const NormArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Threads and chunks a row, by its chunks.  Measured with a residual, h and y written (us, 8192
+// rows of bf16 unless said): 1024 wide 7.6 with a warp a row, 9.5 with 128 threads of one chunk; 4096
+// wide 42.1 with 128 threads of four chunks, 45.2 with 256 of two, 52.0 with 512 of one; 8192
+// wide 80.6 with 256 of four, 97.8 with 512 of two; 32768 wide (2048 rows) 100 with 1024 of four,
+// 154 with 512 of eight; 4-byte floats, 14336 wide (4096 rows) 157 and 168 with the same.  Rows that no 16-byte vector fits (odd widths or distances) go by 4-byte pairs or by
+// elements: 1001 wide 13.4 us, 4090 wide 46.8, 4095 wide 68.6, where 256 threads of eight and 512 of 16 elements
+// took 22.7, 104 and 104.
 template <typename T, int VW>
 cudaError_t launch_width(const NormArgs& a, cudaStream_t stream) {
   const int n = a.K / VW;  // chunks of a row
-  if constexpr (VW > 1) {
+  if constexpr (VW > 2) {
+    if (n <= 64) return launch<T, VW, 32, 2, 128>(a, stream);
     if (n <= 128) return launch<T, VW, 32, 4, 128>(a, stream);
     if (n <= 256) return launch<T, VW, 128, 2, 128>(a, stream);
-    if (n <= 512) return launch<T, VW, 256, 2, 256>(a, stream);
-    if (n <= 1024) return launch<T, VW, 512, 2, 512>(a, stream);
+    if (n <= 512) return launch<T, VW, 128, 4, 128>(a, stream);
+    if (n <= 1024) return launch<T, VW, 256, 4, 256>(a, stream);
     if (n <= 2048) return launch<T, VW, 512, 4, 512>(a, stream);
-    if (n <= 4096) return launch<T, VW, 512, 8, 512>(a, stream);
+    if (n <= 4096) return launch<T, VW, 1024, 4, 1024>(a, stream);
     return launch<T, VW, 1024, 8, 1024>(a, stream);
   } else {
     if (n <= 128) return launch<T, VW, 32, 4, 128>(a, stream);
+    if (n <= 512) return launch<T, VW, 32, 16, 128>(a, stream);
+    if (n <= 1024) return launch<T, VW, 128, 8, 128>(a, stream);
     if (n <= 2048) return launch<T, VW, 256, 8, 256>(a, stream);
+    if (n <= 4096) return launch<T, VW, 512, 8, 512>(a, stream);
     if (n <= 8192) return launch<T, VW, 512, 16, 512>(a, stream);
+    if (n <= 16384) return launch<T, VW, 1024, 16, 1024>(a, stream);
     return launch<T, VW, 1024, 32, 1024>(a, stream);
   }
 }
@@ -267,9 +294,13 @@ extern "C" int lora_rms_norm(const void* x, int ldx, const void* res, int ldr, c
   const bool vec = K % vw == 0 && ldx % vw == 0 && (!res || ldr % vw == 0) && (!h || ldh % vw == 0) &&
                    aligned(x, 16) && aligned(res, 16) && aligned(w, 16) && aligned(h, 16) &&
                    aligned(y, 16) && aligned(xq, vw);
+  const bool pairs = K % 2 == 0 && ldx % 2 == 0 && (!res || ldr % 2 == 0) && (!h || ldh % 2 == 0) &&
+                     aligned(x, 4) && aligned(res, 4) && aligned(w, 4) && aligned(h, 4) &&
+                     aligned(y, 4) && aligned(xq, 2);
   cudaError_t e;
   if (dtype == LORA_BF16)
-    e = vec ? launch_width<__nv_bfloat16, 8>(a, stream) : launch_width<__nv_bfloat16, 1>(a, stream);
+    e = vec ? launch_width<__nv_bfloat16, 8>(a, stream)
+        : pairs ? launch_width<__nv_bfloat16, 2>(a, stream) : launch_width<__nv_bfloat16, 1>(a, stream);
   else
     e = vec ? launch_width<float, 4>(a, stream) : launch_width<float, 1>(a, stream);
   return e == cudaSuccess ? LORA_OK : LORA_ECUDA;
