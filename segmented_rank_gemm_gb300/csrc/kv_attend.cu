@@ -171,6 +171,29 @@ __device__ __forceinline__ long long column_offset(const KvAttendArgs& a, const 
          static_cast<long long>(head * G + (col - token * G)) * a.pages.D;
 }
 
+// A bulk copy, or two one behind the other, counted on `bar` and asked for by the one lane with `mine`.
+__device__ __forceinline__ void fetch_one(uint32_t mine, uint32_t dst, const uint8_t* src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %3;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], %3, [%4];\n\t}" ::"r"(mine),
+      "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fetch_two(uint32_t mine, uint32_t dst, const uint8_t* src0,
+                                          const uint8_t* src1, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], %4, [%5];\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%7], [%3], %4, [%5];\n\t}" ::"r"(mine),
+      "r"(dst), "l"(src0), "l"(src1), "r"(bytes), "r"(bar), "r"(2 * bytes), "r"(dst + bytes)
+      : "memory");
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(KvAttendArgs a) {
   constexpr int kBlock = kv_block_bytes(D), kTileBytes = 2 * kBlock;
@@ -280,68 +303,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     const int shift = a.pages.page_shift;
     const uint32_t page_bytes = static_cast<uint32_t>(kBlock) << (shift - 4);  // of one head
     const size_t page_stride = static_cast<size_t>(page_bytes) * heads;
-    const int in_page = (1 << shift) / kTile - 1;  // mask of a tile's place in its page
+    const int in_page = max(0, (1 << shift) / kTile - 1);  // mask of a tile's place in its page
 
-    // page ids of 32 consecutive tiles of the request being fetched, one tile a lane (two
-    // pages a tile where a page is half of one)
-    int ids_b = -1, ids_tile = 0, id0 = 0, id1 = 0;
-    bool dead = false;
-    auto fetch_ids = [&]() {
-      ids_b = in.b;
-      ids_tile = in.tile & ~31;
-      const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
-      const int32_t* row = a.table + static_cast<size_t>(in.b) * a.max_blocks;
-      const int pos = (ids_tile + lane) * kTile;
-      const bool some = in.r.kv > 0;
-      id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
-      id1 = some ? __ldg(row + min((pos + kKvBlock) >> shift, last)) : 0;
-      const unsigned pages = a.pages.num_pages;
-      if (static_cast<unsigned>(id0) >= pages || static_cast<unsigned>(id1) >= pages) {
-        atomicOr(a.err, LORA_ERRF_BAD_ID);
-        if (static_cast<unsigned>(id0) >= pages) id0 = 0;
-        if (static_cast<unsigned>(id1) >= pages) id1 = 0;
-      }
-    };
-    const uint8_t* in_base = nullptr;  // the head's part of page 0
-    int in_stage = 0;
-    auto begin_run = [&]() {
-      if (in.b != ids_b || (in.tile & ~31) != ids_tile) fetch_ids();
-      in_base = a.pages.base + static_cast<size_t>(in.head) * page_bytes;
-    };
-    auto issue = [&]() {  // fetch tile `in` into its stage
-      const int p0 = __shfl_sync(0xffffffffu, id0, in.tile & 31);
-      const int p1 = shift == 4 ? __shfl_sync(0xffffffffu, id1, in.tile & 31) : 0;
-      if (lane == 0) {
-        uint8_t* dst = my_ring + in_stage * kTileBytes;
-        mbar_arrive_expect_tx(bar + in_stage, kTileBytes);
-        const uint8_t* src = in_base + p0 * page_stride;
-        if (shift > 4) {
-          bulk_load_g2s(dst, src + (in.tile & in_page) * kTileBytes, kTileBytes, bar + in_stage);
-        } else {
-          bulk_load_g2s(dst, src, kBlock, bar + in_stage);
-          bulk_load_g2s(dst + kBlock, in_base + p1 * page_stride, kBlock, bar + in_stage);
-        }
-      }
-      in_stage = in_stage == kStages - 1 ? 0 : in_stage + 1;
-    };
-    bool more = in.unit < w_hi;  // `in` is a tile to fetch
-    auto fetch = [&]() {         // fetch it and move on
-      if (!more) return;
-      issue();
-      if (in.tile + 1 < in.r.tiles) {
-        ++in.tile;
-        more = ++in.unit < w_hi;
-        if (more && (in.tile & 31) == 0) begin_run();
+    // Where 32 consecutive tiles of the request and head being fetched are, one tile a lane, which
+    // asks for it (two pages a tile where a page is half of one).
+    int src_b = -1, src_tile = 0, src_head = 0;
+    const uint8_t *src0 = nullptr, *src1 = nullptr;
+    auto aim = [&]() {
+      if (in.b == src_b && (in.tile & ~31) == src_tile) {  // another head's
+        const ptrdiff_t by = static_cast<ptrdiff_t>(in.head - src_head) * page_bytes;
+        src0 += by;
+        src1 += by;
       } else {
-        more = in.unit + 1 + kSetup < w_hi;
-        if (more) {
+        src_b = in.b;
+        src_tile = in.tile & ~31;
+        const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
+        const int32_t* row = a.table + static_cast<size_t>(in.b) * a.max_blocks;
+        const int pos = (src_tile + lane) * kTile;
+        const bool some = in.r.kv > 0;
+        int id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
+        int id1 = some ? __ldg(row + min((pos + kKvBlock) >> shift, last)) : 0;
+        const unsigned pages = a.pages.num_pages;
+        if (static_cast<unsigned>(id0) >= pages || static_cast<unsigned>(id1) >= pages) {
+          atomicOr(a.err, LORA_ERRF_BAD_ID);
+          if (static_cast<unsigned>(id0) >= pages) id0 = 0;
+          if (static_cast<unsigned>(id1) >= pages) id1 = 0;
+        }
+        const uint8_t* base = a.pages.base + static_cast<size_t>(in.head) * page_bytes;
+        src0 = base + id0 * page_stride + ((src_tile + lane) & in_page) * kTileBytes;
+        src1 = base + id1 * page_stride;
+      }
+      src_head = in.head;
+    };
+    bool dead = false;
+    // Fetch tile `in` into a stage, if there is one left, and move on; in.unit is its group's first
+    // tile's.
+    int in_left = static_cast<int>(min(static_cast<long long>(in.r.tiles - in.tile), w_hi - in.unit));
+    in.unit -= in.tile;
+    const uint32_t ring_at = smem_u32(my_ring), bar_at = smem_u32(bar);
+    auto fetch = [&](int stage) {
+      if (in_left == 0) return;
+      const uint32_t mine = lane == (in.tile & 31);
+      if (shift > 4)
+        fetch_one(mine, ring_at + stage * kTileBytes, src0, kTileBytes, bar_at + stage * 8);
+      else
+        fetch_two(mine, ring_at + stage * kTileBytes, src0, src1, kBlock, bar_at + stage * 8);
+      ++in.tile;
+      if (--in_left > 0) {
+        if ((in.tile & 31) == 0) aim();
+      } else if (in.tile == in.r.tiles) {
+        in.unit += in.tile;
+        if (in.unit + kSetup < w_hi) {
           in.next_group(a);
-          begin_run();
+          aim();
+          in_left = static_cast<int>(min(static_cast<long long>(in.r.tiles), w_hi - in.unit));
         }
       }
     };
-    if (more) begin_run();
-    for (int i = 0; i < kStages; ++i) fetch();
+    aim();
+    for (int i = 0; i < kStages; ++i) fetch(i);
 
     uint32_t qf[KT][NT][2];
     int lim[NT][2];
@@ -350,8 +370,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     const int ta = kv_frag_token(g);  // tokens of fragment rows g and g + 8: ta, ta + 8
     const int tv = (t & 1) | (t >> 1) << 1;
     const int G = a.group;
-    int stage = 0, phase = 0;
-    uint32_t there = 0;  // the stage's tile has been seen to be there
+    int stage = 0;
+    uint32_t phase = 0;
+    bool there = false;  // the stage's tile has been seen to be there
 
     while (at.unit < w_hi) {
       // the group's queries, the last position each column sees, and an empty state
@@ -410,8 +431,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
 
       const int count = static_cast<int>(min(static_cast<long long>(at.r.tiles - at.tile), w_hi - at.unit));
       for (int i = 0; i < count; ++i) {
-        if (!there && !dead && !mbar_wait(bar + stage, phase, a.err)) dead = true;
-        there = mbar_peek(bar + (stage == kStages - 1 ? 0 : stage + 1), stage == kStages - 1 ? phase ^ 1 : phase);
+        if (!there && !dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar + stage, phase, a.err));
+        const int next_stage = stage == kStages - 1 ? 0 : stage + 1;
+        const uint32_t next_phase = next_stage ? phase : phase ^ 1;
+        there = __all_sync(0xffffffffu, mbar_peek(bar + next_stage, next_phase));
         const int pos0 = (at.tile + i) * kTile;
         if (pos0 <= lim_hi) {
           const uint8_t* tile = my_ring + stage * kTileBytes;
@@ -565,14 +588,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
 
         // the stage is free: every lane has read it
         __syncwarp();
-        if (stage == kStages - 1) {
-          stage = 0;
-          phase ^= 1;
-        } else {
-          ++stage;
-        }
-        dead = __any_sync(0xffffffffu, dead);
-        if (!dead) fetch();
+        if (!dead) fetch(stage);
+        stage = next_stage;
+        phase = next_phase;
       }
       const bool whole = at.tile + count == at.r.tiles && group >= w_lo;
 
