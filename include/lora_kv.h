@@ -126,11 +126,12 @@ int lora_kv_read(lora_kv_cache_t* cache, const int32_t* kv_slot_dev, int T, void
  *                   multiple of kv_heads: query head i reads cache head i / (q_heads / kv_heads).
  *   q_offsets [B+1], kv_len [B], block_table [B, max_blocks]: as from lora_kv_maps.
  *   max_q           an upper bound of a request's new tokens (q_offsets[b+1] - q_offsets[b]);
- *                   a request above it is flagged and its rows are zero.
+ *                   a request above it is flagged and its rows are unspecified.
  * With q rows and n cached tokens, row i of a request sees positions 0 .. n - q + i.  A row
  * that sees nothing is zero, and so are rows outside every request.  Scores, the softmax's
  * maximum and sum and the output's accumulation are fp32; the products run on the tensor
- * cores from bf16 q and the cache's exact values, and probabilities as fp16.
+ * cores from q as it is (bf16, or scaled by a power of two into fp16), the cache's exact
+ * values, and probabilities as fp16.
  * Offsets that are not ascending within [0, T], lengths outside [0, max_blocks * page_size]
  * and page ids outside the cache are flagged (lora_kv_get_status) and read nothing outside
  * the cache; the results of such requests are unspecified.

@@ -32,6 +32,13 @@
 // contexts), the tiles of all groups form one sequence instead, cut into equal ranges for the CTAs; a
 // cut near a group's edge moves there.  A group that is still cut leaves pieces (m, l, O), joined in
 // order by the last CTA to arrive.
+//
+// Measured (32 query heads over 8 of 128): 8 prompts of 1024 tokens at up to 2048 positions 130 us,
+// 110 GFLOP at 0.85 PFLOP/s, the tensor pipe at work in 40% of the cycles; cut into equal ranges
+// instead of whole groups 153 us, with natural instead of falling sizes 12% more by the model.  A
+// tile takes 1780 cycles, of which its products are 1365 (QK and PV of both halves from three
+// warps, measured alone); a quarter of the time goes to the changes of groups, where the
+// output of one, the queries of the next and its first products follow one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -50,8 +57,10 @@ constexpr int kRows = 256;      // rows of a group, two halves
 constexpr int kTile = 64;       // positions of a tile
 constexpr int kStages = 3;      // decoded tiles of K, and of V
 constexpr int kRaw = 3;         // packed tiles
-constexpr int kSetup = 6;       // units a group counts before its tiles: what its change costs
-constexpr int kPieces = 15;     // units that the pieces of a group cut in two cost
+// Units (a tile's time, 1780 cycles) a group counts before its tiles, what its change costs (9500
+// cycles measured), and units that the pieces of a group cut in two cost (13000 each).
+constexpr int kSetup = 6;
+constexpr int kPieces = 15;
 // A cut this near to a group's edge moves there: a group cut in two costs its CTAs about as much as
 // this many tiles, as long as that is little of a range.
 __device__ __forceinline__ int snap_of(long long span) {
