@@ -76,7 +76,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
+// The first of a sum.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // ---- requests, groups and the sequence of tiles ----
 struct Request {
@@ -166,7 +173,7 @@ struct PieceInfo {
 template <int D, int NT>
 struct State {
   float o[D / 16][NT][4];  // [dimension pair][column tile][fragment]
-  float2 m[NT], l[NT];     // of the fragment's two columns
+  float2 minus[NT], l[NT];  // -m and l of the fragment's two columns
 };
 
 // Columns' rows in q and out: the element offset of column c, or -1.
@@ -408,12 +415,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                           ? min(120, 9 + 127 - static_cast<int>(__float_as_uint(top) >> 23))
                           : 0;
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e + 127) << 23), a.scale_log2);
+        const float up16 = up * 0x1p-4f;  // of the dimensions whose keys come sixteen times as large
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            qf[2 * w + (i >> 1)][nt][i & 1] = pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+            qf[2 * w + (i >> 1)][nt][i & 1] =
+                i & 1 ? pack_f16x2(bf16_lo(x[i]) * up16, bf16_hi(x[i]) * up16)
+                      : pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
         }
         // (never 0, so that a masked score stays -inf)
         const float down =
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
           const int c = at.col * 8 * NT + nt * 8 + 2 * t + j;
           lim[nt][j] = at.r.kv - at.r.q_len + min(a.token_of(c), at.r.q_len - 1);
         }
-        st.m[nt] = make_float2(kNone, kNone);
+        st.minus[nt] = make_float2(-kNone, -kNone);
         st.l[nt] = make_float2(0.f, 0.f);
       }
       const int lim_lo = at.r.kv - at.r.q_len + a.token_of(at.col * 8 * NT);
@@ -471,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
               sc[0] = both_lo(both);
               sc[1] = both_hi(both);
             }
-            float acc[NT][4] = {};
+            float acc[NT][4];
 #pragma unroll
             for (int p = 0; p < KW / 2; ++p) {  // the lane's scale groups
-              Decode dec[2];
+              Decode16 dec[2];
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                dec[r] = decode_scales(D == 128 ? (p ? both_hi(sc[r]) : both_lo(sc[r])) : sc[r]);
+                dec[r] = decode_scales16(D == 128 ? (p ? both_hi(sc[r]) : both_lo(sc[r])) : sc[r]);
 #pragma unroll
               for (int w = 2 * p; w < 2 * p + 2; ++w) {
                 uint32_t v[2][4];
@@ -485,8 +495,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                 decode4(kw[1][w], dec[1], v[1]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  mma_f16(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][nt][0],
-                          qf[2 * w][nt][1]);
+                  if (w == 0)
+                    mma_f16_first(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[0][nt][0], qf[0][nt][1]);
+                  else
+                    mma_f16(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][nt][0],
+                            qf[2 * w][nt][1]);
                   mma_f16(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][nt][0],
                           qf[2 * w + 1][nt][1]);
                 }
@@ -517,9 +530,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
           for (int nt = 0; nt < NT; ++nt) {
             top[nt].x = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
             top[nt].y = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
-            top[nt].x *= unit[nt].x;
-            top[nt].y *= unit[nt].y;
-            over |= top[nt].x > st.m[nt].x + (kRef + kSlack) || top[nt].y > st.m[nt].y + (kRef + kSlack);
+            over |= fmaf(top[nt].x, unit[nt].x, st.minus[nt].x) > kRef + kSlack ||
+                    fmaf(top[nt].y, unit[nt].y, st.minus[nt].y) > kRef + kSlack;
           }
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -529,10 +541,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                 top[nt].x = fmaxf(top[nt].x, __shfl_xor_sync(0xffffffffu, top[nt].x, d));
                 top[nt].y = fmaxf(top[nt].y, __shfl_xor_sync(0xffffffffu, top[nt].y, d));
               }
-              const float2 m = make_float2(fmaxf(st.m[nt].x, top[nt].x - kRef),
-                                           fmaxf(st.m[nt].y, top[nt].y - kRef));
-              const float fx = ex2(st.m[nt].x - m.x), fy = ex2(st.m[nt].y - m.y);
-              st.m[nt] = m;
+              const float2 minus = make_float2(fminf(st.minus[nt].x, kRef - top[nt].x * unit[nt].x),
+                                               fminf(st.minus[nt].y, kRef - top[nt].y * unit[nt].y));
+              const float fx = ex2(minus.x - st.minus[nt].x), fy = ex2(minus.y - st.minus[nt].y);
+              st.minus[nt] = minus;
               st.l[nt].x *= fx;
               st.l[nt].y *= fy;
 #pragma unroll
@@ -551,10 +563,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
             uint32_t pf[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float2 minus = make_float2(-st.m[nt].x, -st.m[nt].y);
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float2 x = fma2(s[k][nt][r], unit[nt], minus);
+                const float2 x = fma2(s[k][nt][r], unit[nt], st.minus[nt]);
                 const float2 p = make_float2(ex2(x.x), ex2(x.y));
                 st.l[nt] = add2(st.l[nt], p);
                 pf[nt][r] = transpose_8x8(pack_f16x2(p.x, p.y));
@@ -575,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
             }
             vs = *reinterpret_cast<const uint32_t*>(blk + kv_v_scales(D) +
                                                     ((D == 128 ? g : g >> 1) * 4 + t) * 4);
-            const Decode dec[2] = {
-                decode_scales(e4m3x2_to_f16x2(static_cast<uint16_t>(vs))),
-                decode_scales(e4m3x2_to_f16x2(static_cast<uint16_t>(vs >> 16)))};
+            const Decode16 dec[2] = {
+                decode_scales16(e4m3x2_to_f16x2(static_cast<uint16_t>(vs))),
+                decode_scales16(e4m3x2_to_f16x2(static_cast<uint16_t>(vs >> 16)))};
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
@@ -621,14 +632,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                 column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + 2 * t + j, a.ldo);
             if (off < 0) continue;
             const float l = j ? st.l[nt].y : st.l[nt].x;
-            const float f = l == 0.f ? 0.f : back / l;
+            const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
 #pragma unroll
             for (int w = 0; w < LD / 8; ++w) {
               uint32_t x[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                x[i] = pack_bf16x2(st.o[4 * w + i][nt][j] * f, st.o[4 * w + i][nt][j + 2] * f);
+                x[i] = pack_bf16x2(st.o[4 * w + i][nt][j] * f, st.o[4 * w + i][nt][j + 2] * f16);
               dst[w] = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
@@ -643,15 +654,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
           for (int j = 0; j < 2; ++j) {
             const int c = nt * 8 + 2 * t + j;
             if (g == 0) {
-              piece[c] = j ? st.m[nt].y : st.m[nt].x;
+              piece[c] = -(j ? st.minus[nt].y : st.minus[nt].x);
               piece[8 * NT + c] = j ? st.l[nt].y : st.l[nt].x;
             }
             float* o = piece + 16 * NT + c * D + g * LD;
 #pragma unroll
             for (int m = 0; m < KT; m += 2)
               *reinterpret_cast<float4*>(o + 2 * m) =
-                  make_float4(st.o[m][nt][j], st.o[m][nt][j + 2], st.o[m + 1][nt][j],
-                              st.o[m + 1][nt][j + 2]);
+                  make_float4(st.o[m][nt][j], st.o[m][nt][j + 2] * 0x1p-4f, st.o[m + 1][nt][j],
+                              st.o[m + 1][nt][j + 2] * 0x1p-4f);
           }
         if (lane == 0)
           info[warp * 2 + slot] =
