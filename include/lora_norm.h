@@ -27,8 +27,8 @@ extern "C" {
  *                          nearest even, saturating, from the fp32 y; the row format of an e4m3 layer
  *                          (lora_forward_e4m3).
  *   dtype                  LORA_BF16 or LORA_F32: of x, the residual, w, h and y.
- * Rows need no alignment: 16-byte vectors are used where every pointer and row distance
- * allows them.
+ * Rows need no alignment but their elements' (2 or 4 bytes; LORA_EINVAL without it): 16-byte
+ * vectors are used where every pointer and row distance allows them.
  * Limits: 0 <= T <= 1 << 20, 1 <= K <= 32768, row distances >= K, eps >= 0; at least one of
  * y, xq, residual_out.  y, xq and sx overlap no input.  Errors: LORA_EINVAL, LORA_ECUDA.
  */

@@ -276,6 +276,9 @@ extern "C" int lora_rms_norm(const void* x, int ldx, const void* res, int ldr, c
   if (T == 0) return LORA_OK;
   if (!x || !w || !xq != !sx || (!y && !xq && !h)) return LORA_EINVAL;
   const size_t es = dtype == LORA_BF16 ? 2 : 4;
+  for (const void* p : {x, res, w, static_cast<const void*>(h), static_cast<const void*>(y)})
+    if (!aligned(p, static_cast<int>(es))) return LORA_EINVAL;
+  if (!aligned(sx, 4)) return LORA_EINVAL;
   const size_t t = T, n = K;
   const Rows in[] = {{x, t, n * es, ldx * es}, {res, t, n * es, ldr * es}, {w, 1, n * es, n * es}};
   const Rows out[] = {{y, t, n * es, n * es}, {xq, t, n, n}, {sx, t, 4, 4}, {h, t, n * es, ldh * es}};

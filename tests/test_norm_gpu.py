@@ -145,3 +145,34 @@ def test_refusals():
             lora_rms_norm(**{**ok, **change})
     lora_rms_norm(**ok)
     lora_rms_norm(x[:0], w, 1e-6, y=y[:0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,K", [(7, 2), (5, 127), (6, 130), (3, 511), (4, 512), (5, 514), (4, 1026), (3, 2047),
+                                 (2, 2050), (3, 4090), (2, 4095), (2, 8190), (2, 12000), (2, 16384), (2, 16386),
+                                 (1, 32766), (3, 24576)])
+def test_norm_at_every_split(T, K, dtype):
+    # widths on both sides of the splits of rows of vectors, pairs and elements
+    x, r, w = _inputs(T, K, dtype, seed=T * K)
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    xq = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=DEV)
+    sx = torch.empty(T, device=DEV)
+    from segmented_rank_gemm_gb300.norm import lora_rms_norm
+    lora_rms_norm(x, w, 1e-5, r, h, y, xq, sx)
+    _check(x, r, w, 1e-5, h, y, xq, sx)
+
+
+def test_norm_refuses_split_elements():
+    from segmented_rank_gemm_gb300 import lora
+    lib = lora.library()
+    x, r, w = _inputs(4, 64, torch.bfloat16)
+    y, sx = torch.empty_like(x), torch.empty(4, device=DEV)
+    xq = torch.empty(4, 64, dtype=torch.float8_e4m3fn, device=DEV)
+    good = [x.data_ptr(), 64, r.data_ptr(), 64, w.data_ptr(), 1e-6, 3, 63, lora.LORA_BF16, None, 0,
+            y.data_ptr(), xq.data_ptr(), sx.data_ptr(), 0]
+    for i in (0, 2, 4, 11, 13):
+        bad = list(good)
+        bad[i] += 1
+        assert lib.lora_rms_norm(*bad) == lora.LORA_EINVAL
+    assert lib.lora_rms_norm(*good) == 0
+    torch.cuda.synchronize()
