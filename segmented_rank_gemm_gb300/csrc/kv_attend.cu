@@ -31,9 +31,9 @@
 // between CTAs, by the last one to arrive, in the order of the pieces: results do not depend on
 // timing.
 //
-// Measured (32 query heads over 8 of 128): 3 contexts of 91 to 107 thousand positions 84.8 us, 350
-// MB at 4.1 TB/s; 512 single tokens over 1 to 2048 positions 65.3 us; one over 1000 12.8 us.  What
-// bounds it: a tile is 630 instructions, half of them the decoding, of which a scheduler's four warps issue
+// Measured (32 query heads over 8 of 128): 3 contexts of 91 to 107 thousand positions 81.4 us, 350
+// MB at 4.3 TB/s; 512 single tokens over 1 to 2048 positions 63.3 us; one over 1000 12.8 us.  What
+// bounds it: a tile is 617 instructions, half of them the decoding, of which a scheduler's four warps issue
 // three in four cycles in the main loop (the tiles stream at 5.7 TB/s there); before it lie 4.5 us of
 // launch, scan and first loads, and behind it the spread of the warps and the joins, 10 to 15 us.
 #include <cuda_bf16.h>
@@ -276,7 +276,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
 
   if (span * blockIdx.x >= total) return;
   const long long raw_lo = span * blockIdx.x, raw_hi = min(total, raw_lo + span);
-  const int wspan = static_cast<int>((span + kWarps - 1) / kWarps), snap = wspan / 6;
+  // A cut within snap of a group's edge moves there, which spares two pieces (512 tokens beside 8
+  // prompts: 84.8 us without, 83.1 with; 512 tokens alone 63.5 and 63.3, up to 65.5 for wspan / 4).
+  const int wspan = static_cast<int>((span + kWarps - 1) / kWarps), snap = min(wspan / 4, 2);
 #pragma unroll
   for (int w = 0; w <= kWarps; ++w) {
     const long long at = min(raw_hi, raw_lo + static_cast<long long>(w) * wspan);
