@@ -14,7 +14,7 @@
 // prefix sums (the lengths come from L2) and keeps them in shared memory; batches of at most
 // kRowsPerCta rows run in one CTA.  Larger ones split rows and pages over CTAs; the
 // last CTA to finish writes kv_len and the counts, which may overwrite inputs the others read.
-// Measured: 512 single tokens 4.4 us, 520 requests with 3247 rows 5.4, 2999 with 42455 7.7; with
+// Measured: 512 single tokens 4.4 us, 520 requests with 3247 rows 5.5, 2999 with 42455 7.7; with
 // four rows a thread the last two take 6.9 and 10.9, with half the threads idle (512 a CTA) the
 // first takes 5.4.
 #include <cuda_runtime.h>
