@@ -33,7 +33,7 @@
 // cut near a group's edge moves there.  A group that is still cut leaves pieces (m, l, O), joined in
 // order by the last CTA to arrive.
 //
-// Measured (32 query heads over 8 of 128): 8 prompts of 1024 tokens at up to 2048 positions 130 us,
+// Measured (32 query heads over 8 of 128): 8 prompts of 1024 tokens at up to 2048 positions 129 us,
 // 110 GFLOP at 0.85 PFLOP/s, the tensor pipe at work in 40% of the cycles; cut into equal ranges
 // instead of whole groups 153 us, with natural instead of falling sizes 12% more by the model.  A
 // tile takes 1780 cycles, of which its products are 1365 (QK and PV of both halves from three
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
         const int lim = g.see + a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) - g.tile * kTile;
         uint32_t at = (step + half) % 3;  // S's place
         for (int j = 0; j < g.count; ++j, ++n) {
-          const uint32_t pv_there = n > 0 ? mbar_peek(&bar.pv_done[half], (n - 1) & 1) : 1;
+          uint32_t pv_there = 1;  // the product before has been seen to be done
           ok = mbar_wait(&bar.s_full[half][n % 3], n / 3 & 1, a.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -530,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum[i & 1] = add2(sum[i & 1], e);
             p[i] = pack_f16x2(e.x, e.y);
+            // (as late as spares the wait: at the tile's start it is not done yet)
+            if (i == 23 && n > 0) pv_there = mbar_peek(&bar.pv_done[half], (n - 1) & 1);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           // the product before is done: P's place is free, and O may be rescaled
