@@ -14,7 +14,7 @@
 // prefix sums (the lengths come from L2) and keeps them in shared memory; batches of at most
 // kRowsPerCta rows run in one CTA.  Larger ones split rows and pages over CTAs; the
 // last CTA to finish writes kv_len and the counts, which may overwrite inputs the others read.
-// Measured: 512 single tokens 4.4 us, 520 requests with 3247 rows 5.5, 2999 with 42455 7.7; with
+// Measured: 512 single tokens 4.1 us, 520 requests with 3247 rows 5.5, 2999 with 42455 7.7; with
 // four rows a thread the last two take 6.9 and 10.9, with half the threads idle (512 a CTA) the
 // first takes 5.4.
 #include <cuda_runtime.h>
@@ -100,6 +100,7 @@ __device__ __forceinline__ bool page_ok(int page, int page_shift) {
 }
 
 __global__ void __launch_bounds__(kThreads) kv_maps_kernel(MapsArgs a) {
+  griddep_wait();
   extern __shared__ int32_t smem[];
   int32_t* off = smem;              // [B + 1]
   int32_t* first = smem + a.B + 1;  // [B + 1]
@@ -292,8 +293,10 @@ int lora_kv_maps(const int32_t* len_dev, const int32_t* new_dev, const int32_t* 
   if (smem > 40 * 1024 && ensure_smem_limit(kv_maps_kernel, smem, limit) != cudaSuccess)
     return LORA_ECUDA;
   const int ctas = std::min(kMaxCtas, std::max(1, (std::max(T, B) + kRowsPerCta - 1) / kRowsPerCta));
-  kv_maps_kernel<<<ctas, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? LORA_OK : LORA_ECUDA;
+  return launch_dependent(kv_maps_kernel, dim3(ctas), kThreads, smem, static_cast<cudaStream_t>(stream),
+                          a) == cudaSuccess
+             ? LORA_OK
+             : LORA_ECUDA;
 }
 
 int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_size,

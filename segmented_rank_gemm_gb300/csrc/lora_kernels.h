@@ -309,4 +309,22 @@ cudaError_t launch_slot_meta(float* scale, int R, int32_t* rank, int32_t* loaded
                              const SlotScales& cols, int r, int is_loaded, int32_t* row_base,
                              int rb, cudaStream_t stream);
 
+// Launches a kernel that may start before the one ahead of it in the stream has ended (once that
+// one's blocks have all left or said so) and waits for it itself (griddep_wait).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace lora
