@@ -32,7 +32,7 @@
 // timing.
 //
 // Measured (32 query heads over 8 of 128): 3 contexts of 91 to 107 thousand positions 81.4 us, 350
-// MB at 4.3 TB/s; 512 single tokens over 1 to 2048 positions 63.3 us; one over 1000 12.8 us.  What
+// MB at 4.3 TB/s; 512 single tokens over 1 to 2048 positions 62.9 us; one over 1000 12.8 us.  What
 // bounds it: a tile is 617 instructions, half of them the decoding, of which a scheduler's four warps issue
 // three in four cycles in the main loop (the tiles stream at 5.7 TB/s there); before it lie 4.5 us of
 // launch, scan and first loads, and behind it the spread of the warps and the joins, 10 to 15 us.
@@ -41,6 +41,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_decode.cuh"
 #include "kv_kernels.h"
@@ -682,13 +683,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   // Join column c of n pieces, in the order of the sequence, into dst (a piece) or the output:
   // one warp, the weights 2^(m_i - max m) one piece a lane, then the weighted sum, whose loads
   // do not wait for one another.
-  constexpr int NC = 8 * NT, kPiece = piece_floats<D, NT>(), VL = D / 32;
+  constexpr int NC = 8 * NT, kPiece = piece_floats<D, NT>(), VL = D / 32, kAhead = 4;
   const auto join_column = [&](auto piece_of, auto load, int n, const PieceInfo& gi, int c, float* dst) {
+    using Vec = std::conditional_t<VL == 4, float4, float2>;
+    float o[VL] = {};
+    const auto ask = [&](int k) {
+      return load(reinterpret_cast<const Vec*>(piece_of(k) + 2 * NC + c * D + lane * VL));
+    };
+    const auto add = [&](float w, const Vec& x) {
+      o[0] += w * x.x, o[1] += w * x.y;
+      if constexpr (VL == 4) o[2] += w * x.z, o[3] += w * x.w;
+    };
+    Vec ahead[kAhead];  // the first pieces', asked for with the maxima
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < n) ahead[k] = ask(k);
     float m = kNone;
     for (int i = lane; i < n; i += 32) m = fmaxf(m, load(piece_of(i) + c));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f, o[VL] = {};
+    float l = 0.f;
     for (int i0 = 0; i0 < n; i0 += 32) {
       float f = 0.f;
       if (i0 + lane < n) {
@@ -697,18 +711,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         l += f * load(p + NC + c);
       }
       const int some = min(32, n - i0);
-#pragma unroll 8
-      for (int k = 0; k < some; ++k) {
-        const float w = __shfl_sync(0xffffffffu, f, k);
-        const float* p = piece_of(i0 + k) + 2 * NC + c * D + lane * VL;
-        if constexpr (VL == 4) {
-          const float4 x = load(reinterpret_cast<const float4*>(p));
-          o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
-        } else {
-          const float2 x = load(reinterpret_cast<const float2*>(p));
-          o[0] += w * x.x, o[1] += w * x.y;
-        }
+      if (i0 == 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (k < n) add(__shfl_sync(0xffffffffu, f, k), ahead[k]);
       }
+#pragma unroll 8
+      for (int k = i0 == 0 ? kAhead : 0; k < some; ++k) add(__shfl_sync(0xffffffffu, f, k), ask(i0 + k));
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
