@@ -91,13 +91,14 @@ struct Request {
   int row0, q_len, kv, tiles, col_tiles;
 };
 
-// Request b, checked: one with bad offsets has q_len 0.
+// Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
+// one before stands ahead of them.)
 template <int NT>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bool report) {
   Request r;
-  r.row0 = __ldg(a.q_offsets + b);
-  const int end = __ldg(a.q_offsets + b + 1);
-  r.kv = __ldg(a.kv_len + b);
+  r.row0 = load_in_order(a.q_offsets + b);
+  const int end = load_in_order(a.q_offsets + b + 1);
+  r.kv = load_in_order(a.kv_len + b);
   r.q_len = end - r.row0;
   bool bad = false;
   if (r.row0 < 0 || end > a.T || r.q_len < 0 || r.q_len > a.max_q) {
@@ -231,6 +232,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   const int g = lane >> 2, t = lane & 3;
   const int heads = a.pages.heads;
 
+  if (tid < kWarps * 2) info[tid].group = -1;
+  if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
+  fence_mbar_init();
+  // The kernel ahead may have written anything that is read below, the lengths among it (the maps of
+  // the batch do).  The kernel for many rows needs nothing of this one's: it may start now, on what came
+  // before both, and waits for this one at its end.
+  griddep_wait();
+  if (a.many_follow) griddep_launch_dependents();
+
   // the sequence's length and this CTA's range; where each warp starts
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -244,9 +254,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     if (lane >= d) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
-  if (tid < kWarps * 2) info[tid].group = -1;
-  if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
-  fence_mbar_init();
   __syncthreads();
   long long total = 0, before = incl - mine;
 #pragma unroll
@@ -255,16 +262,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     total += scan[w];
   }
   const long long span = max(static_cast<long long>(kMinSpan), quotient(total + gridDim.x - 1, gridDim.x));
-  // What came before wrote the lengths, but not as the kernel just ahead of this one if that one
-  // let this one start early (append does, the maps do not); q, the cache and `out` it may still
-  // be using.  The kernel for many rows needs nothing of this one's: it may start now, and waits
-  // for this one at its end.
-  griddep_wait();
-  if (a.many_follow) griddep_launch_dependents();
 
   // rows of no request
   {
-    const int lo = max(0, min(__ldg(a.q_offsets), a.T)), hi = max(0, min(__ldg(a.q_offsets + a.B), a.T));
+    const int lo = max(0, min(load_in_order(a.q_offsets), a.T));
+    const int hi = max(0, min(load_in_order(a.q_offsets + a.B), a.T));
     const int words = a.q_heads * D / 8;  // 16-byte words of a row
     const long long n = static_cast<long long>(lo + a.T - hi) * words;
     for (long long i = blockIdx.x * kThreads + tid; i < n; i += gridDim.x * kThreads) {
