@@ -113,6 +113,7 @@ struct ShrinkTcArgs {
   int ks;              // K split (planes written), from sgmv_shrink_tc_split
   int pool_rows;       // P: rows of the A pool (debug-flavour bounds checks)
   int v_rows;          // rows of a plane of v (T_max)
+  bool gemm_waits;     // the GEMM waits for its rows itself (the quantiser's row count)
   int32_t* err;
   int num_sms;
 };
@@ -122,7 +123,7 @@ int sgmv_shrink_tc_groups(int Rt);
 // at most max_planes.
 int sgmv_shrink_tc_split(int T, int K, int S, int num_sms, int max_planes);
 // tmap_a: the A pool [P rows][K] bf16 with a (64 x Rt) box.  Writes planes 0 .. ks - 1 of
-// v.  Launched with programmatic stream serialization (it waits for the builder itself).
+// v.  Launched with programmatic stream serialization (it waits for the kernel ahead itself).
 cudaError_t launch_sgmv_shrink_tc(const ShrinkTcArgs& a, const CUtensorMap& tmap_a,
                                   cudaStream_t stream);
 

@@ -666,6 +666,7 @@ static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, con
     sa.ks = v_split;
     sa.pool_rows = L->P;
     sa.v_rows = L->T_max;
+    sa.gemm_waits = quantise;
     sa.err = L->err;
     sa.num_sms = L->num_sms;
     LORA_CUDA(L, launch_sgmv_shrink_tc(sa, L->tmap_a, stream));
@@ -734,8 +735,8 @@ static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, con
   ga.tmap_xq = xq ? &tmap_rows : L->fp8 ? &L->tmap_xq : nullptr;
   ga.sx = xq ? sx : L->sx;
   ga.sw = L->sw;
-  // the caller's rows were written before this call's first kernel starts, so nothing counts
-  // them: the GEMM's loads start as those of a bf16 x do
+  // the caller's rows were written before the low-rank kernel lets the GEMM start (it waits for
+  // the kernel ahead first), so nothing counts them: their loads start as those of a bf16 x do
   ga.q_ready = quantise ? L->q_ready : nullptr;
   ga.tmap_delta = L->delta ? &L->tmap_delta : nullptr;
   LORA_CUDA(L, trace_mark(L, 4, stream));

@@ -41,9 +41,11 @@
 //               i of a composition) and stores the row's R fp32 values at v[kp][perm row].
 // The x bytes dominate (every adapted row is read once per K range and unit of its
 // window); each A_s is read once per unit.
-// Launch: programmatic dependent launch after the segment builder; the kernel lets the base
-// GEMM launch at once (its main loop needs nothing from here) and waits for the builder's
-// results before it reads them.  Every mbarrier wait is bounded (lora_common.cuh).
+// Launch: programmatic dependent launch after the segment builder or whatever else is ahead: the
+// kernel waits for it, and only then lets the base GEMM launch, whose main loop needs nothing from
+// here but reads the caller's rows (x, or e4m3 rows given with it), which the kernel ahead may
+// have written.  Behind the row quantiser the GEMM launches at once: it reads no rows but the
+// quantiser's, and waits for those itself (a.gemm_waits).  Every mbarrier wait is bounded (lora_common.cuh).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -115,8 +117,9 @@ __global__ void __launch_bounds__(kShThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  griddep_launch_dependents();  // the base GEMM's main loop may start now
-  griddep_wait();               // the segment builder's units, perm and segments
+  if (a.gemm_waits) griddep_launch_dependents();
+  griddep_wait();  // the segment builder's units, perm and segments; the rows of x
+  if (!a.gemm_waits) griddep_launch_dependents();  // the base GEMM's main loop may start now
   const int n_items = a.meta[2] * ks;
   const int n_seg = a.meta[0], T_a = a.meta[1];
   const int nkb = (a.K + kShBK - 1) / kShBK;
