@@ -99,12 +99,9 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   r.row0 = load_in_order(a.q_offsets + b);
   const int end = load_in_order(a.q_offsets + b + 1);
   r.kv = load_in_order(a.kv_len + b);
-  r.q_len = end - r.row0;
-  bool bad = false;
-  if (r.row0 < 0 || end > a.T || r.q_len < 0 || r.q_len > a.max_q) {
-    bad = true;
-    r.q_len = 0;
-  }
+  // (in this order: the difference of any two offsets need not be an int)
+  bool bad = r.row0 < 0 || end < r.row0 || end > a.T || end - r.row0 > a.max_q;
+  r.q_len = bad ? 0 : end - r.row0;
   const int cap = a.max_blocks << a.pages.page_shift;
   if (r.kv < 0 || r.kv > cap) {
     bad = true;

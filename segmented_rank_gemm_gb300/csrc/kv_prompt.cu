@@ -140,10 +140,11 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b) {
   Request r;
   r.row0 = __ldg(a.q_offsets + b);
   const int end = __ldg(a.q_offsets + b + 1);
-  r.q_len = end - r.row0;
+  // (in this order: the difference of any two offsets need not be an int)
+  const bool bad = r.row0 < 0 || end < r.row0 || end > a.T || end - r.row0 > a.max_q;
+  r.q_len = bad ? 0 : end - r.row0;
   const int cap = a.max_blocks << a.pages.page_shift;
   r.kv = min(max(__ldg(a.kv_len + b), 0), cap);
-  if (r.row0 < 0 || end > a.T || r.q_len < 0 || r.q_len > a.max_q) r.q_len = 0;
   r.rows = r.q_len * a.group;
   if (r.rows <= a.few_rows) r.rows = 0;
   r.parts = (r.rows + kRows - 1) / kRows;

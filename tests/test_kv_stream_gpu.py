@@ -71,3 +71,25 @@ def test_attention_right_behind_the_maps(B, page, blocks, top, rounds):
         _close(behind[i, first[b]:first[b] + m], want, np.abs(hv).max(), "request %d" % b)
     assert not behind[i, first[-1]:].any()
     cache.close()
+
+
+@pytest.mark.parametrize("new", [[1, 2, 1], [9, 12, 10]])  # few rows a cache head, many
+def test_offsets_whose_difference_passes_32_bits(new):
+    # from 2^31 - 1 down to -2^31 is 1 in 32 bits: still offsets out of range
+    from segmented_rank_gemm_gb300.lora import LORA_EID
+    from test_kv_gpu import Setup
+    kv = [40, 70, 33]
+    s = Setup(kv, 64, 1, 16, seed=31)
+    q = s.queries(new, 4)
+    top, T = max(new), sum(new)
+    good = s.attend(q.to(DEV), new)
+    off = np.concatenate(([0], np.cumsum(new)))
+    for first, last in ((2 ** 31 - 1, -2 ** 31), (2 ** 31 - 1, -2 ** 31 + top - 1),
+                        (T + 1, T + 2), (2 ** 31 - 2, 2 ** 31 - 1), (-2 ** 31, -2 ** 31 + 1)):
+        bad = off.copy()
+        bad[1], bad[2] = first, last  # request 1 between them; 0 and 2 end and begin there
+        out = s.cache.attend(q.to(DEV), _ints(bad), _ints(kv), _ints(s.table), top)
+        assert out.shape == good.shape
+        assert s.cache.status() == LORA_EID
+    assert torch.equal(s.attend(q.to(DEV), new), good)
+    assert s.cache.status() == 0
