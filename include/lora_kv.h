@@ -148,9 +148,18 @@ int lora_kv_attend(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_hea
 /*
  * Synchronise `stream`, read and clear the cache's device error flags: LORA_OK, LORA_EID (a
  * slot, page id, length or offset out of range), LORA_ETIMEOUT (a wait inside a kernel gave
- * up; results invalid) or LORA_ECUDA.
+ * up; the results of calls since then are invalid) or LORA_ECUDA.  After LORA_ETIMEOUT the
+ * attention's workspace is as new: the calls that follow on `stream` are sound.
  */
 int lora_kv_get_status(lora_kv_cache_t* cache, void* stream);
+
+/*
+ * Self-test of a wait that gives up: enqueues a kernel whose wait nothing completes (it gives up
+ * after 2 s) and which leaves the cache as an attention call leaves it whose wait ran out.
+ * lora_kv_get_status then returns LORA_ETIMEOUT, the expected result, and the cache is usable again.
+ * Errors: LORA_EINVAL, LORA_ECUDA.
+ */
+int lora_kv_wait_selftest(lora_kv_cache_t* cache, void* stream);
 
 /* Bytes of the cache's pages (not of its workspace).  0 for NULL. */
 int64_t lora_kv_cache_bytes(const lora_kv_cache_t* cache);

@@ -218,6 +218,18 @@ __global__ void __launch_bounds__(kThreads)
   store_pair(reinterpret_cast<uint4*>(v), i, n, vv);
 }
 
+// What an attention call leaves whose wait gave up: the flag, and counts of CTAs that joined a group
+// others of which never arrived (include/lora_kv.h: lora_kv_wait_selftest).
+__global__ void kv_wait_selftest_kernel(int32_t* arrivals, int n, int32_t* err) {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    mbar_wait(&bar, 0u, err);  // (phase 0 completes only on an arrival)
+  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) arrivals[i] = 1;
+}
+
 // Blocks over the groups of T rows.
 dim3 rows_grid(const KvPages& pg, int T) {
   const long long n = static_cast<long long>(T) * (pg.heads * pg.D / kKvGroup);
@@ -243,6 +255,8 @@ struct lora_kv_cache {
 
 namespace {
 
+// both attention kernels' arrival counts, groups claimed and CTAs done claiming
+constexpr size_t kArrivalsBytes = (2 * kKvMaxCtas + 2) * sizeof(int32_t);
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxRequests = 16384;
 // Rows a cache head (query rows times q_heads / kv_heads) up to which a request's attention runs
@@ -310,12 +324,12 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
       cudaMalloc(&c->pieces, floats * sizeof(float)) != cudaSuccess ||
       cudaMalloc(&c->prompt_pieces, kv_prompt_workspace_floats(c->num_sms, head_dim) *
                                         sizeof(float)) != cudaSuccess ||
-      cudaMalloc(&c->arrivals, (2 * kKvMaxCtas + 2) * sizeof(int32_t)) != cudaSuccess ||
+      cudaMalloc(&c->arrivals, kArrivalsBytes) != cudaSuccess ||
       cudaMalloc(&c->err, sizeof(int32_t)) != cudaSuccess) {
     cudaGetLastError();
     rc = LORA_ENOMEM;
   } else if (cudaMemsetAsync(c->pages.base, 0, c->bytes, stream) != cudaSuccess ||
-             cudaMemsetAsync(c->arrivals, 0, (2 * kKvMaxCtas + 2) * sizeof(int32_t), stream) != cudaSuccess ||
+             cudaMemsetAsync(c->arrivals, 0, kArrivalsBytes, stream) != cudaSuccess ||
              cudaMemsetAsync(c->err, 0, sizeof(int32_t), stream) != cudaSuccess ||
              cudaStreamSynchronize(stream) != cudaSuccess) {
     rc = LORA_ECUDA;
@@ -420,14 +434,27 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
 
 int lora_kv_get_status(lora_kv_cache_t* c, void* stream_) {
   if (!c) return LORA_EINVAL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int32_t flags = 0;
-  KV_CUDA(c, cudaStreamSynchronize(static_cast<cudaStream_t>(stream_)));
-  KV_CUDA(c, cudaMemcpy(&flags, c->err, 4, cudaMemcpyDeviceToHost));
-  KV_CUDA(c, cudaMemset(c->err, 0, 4));
+  KV_CUDA(c, cudaMemcpyAsync(&flags, c->err, sizeof(flags), cudaMemcpyDeviceToHost, stream));
+  KV_CUDA(c, cudaStreamSynchronize(stream));
+  if (!flags) return LORA_OK;
+  // On the caller's stream, ahead of the calls that follow there.  CTAs that gave up did not arrive
+  // where others had: those counts would have later calls join pieces that are not written yet.
+  KV_CUDA(c, cudaMemsetAsync(c->err, 0, sizeof(flags), stream));
+  if (flags & LORA_ERRF_TIMEOUT)
+    KV_CUDA(c, cudaMemsetAsync(c->arrivals, 0, kArrivalsBytes, stream));
+  KV_CUDA(c, cudaStreamSynchronize(stream));
   if (flags & LORA_ERRF_TIMEOUT)
     return fail(c, LORA_ETIMEOUT, "a kernel wait timed out (flags=%d)", flags);
-  if (flags)
-    return fail(c, LORA_EID, "a slot, page id, length or offset out of range (flags=%d)", flags);
+  return fail(c, LORA_EID, "a slot, page id, length or offset out of range (flags=%d)", flags);
+}
+
+int lora_kv_wait_selftest(lora_kv_cache_t* c, void* stream) {
+  if (!c) return LORA_EINVAL;
+  kv_wait_selftest_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      c->arrivals, 2 * kKvMaxCtas, c->err);
+  KV_CUDA(c, cudaGetLastError());
   return LORA_OK;
 }
 

@@ -189,6 +189,11 @@ class KvCache:
         """LORA_OK, LORA_EID or LORA_ETIMEOUT since the last call (synchronises)."""
         return _lib.lora_kv_get_status(self.handle, _stream(stream))
 
+    def wait_selftest(self, stream=None) -> None:
+        """Leave the cache as a wait that ran out leaves it (``lora_kv_wait_selftest``): ``status``
+        then returns LORA_ETIMEOUT, and the cache is usable again."""
+        self._check(_lib.lora_kv_wait_selftest(self.handle, _stream(stream)))
+
     def nbytes(self) -> int:
         return int(_lib.lora_kv_cache_bytes(self.handle))
 

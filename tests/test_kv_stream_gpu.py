@@ -93,3 +93,29 @@ def test_offsets_whose_difference_passes_32_bits(new):
         assert s.cache.status() == LORA_EID
     assert torch.equal(s.attend(q.to(DEV), new), good)
     assert s.cache.status() == 0
+
+
+def test_calls_after_a_wait_that_gave_up():
+    # few groups over long contexts, which several CTAs share and the last to arrive joins: what was
+    # counted when a wait gave up must not count for them
+    from segmented_rank_gemm_gb300.lora import LORA_ETIMEOUT, LORA_OK
+    from test_kv_gpu import Setup
+    kv, new = [6000, 9000], [70, 1]  # many rows a cache head, few
+    s = Setup(kv, 128, 1, 64, seed=32)
+    q = s.queries(new, 4)
+    args = q.to(DEV), _ints([0, 70, 71]), _ints(kv), _ints(s.table), 70
+    want = s.cache.attend(*args)
+    _close(want, s.expected(q, new, 128 ** -0.5), np.abs(s.hv).max())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        s.cache.wait_selftest(stream)
+        assert s.cache.status(stream) == LORA_ETIMEOUT
+        assert s.cache.status(stream) == LORA_OK
+        for _ in range(3):
+            out = torch.zeros_like(want)
+            torch.cuda.synchronize()
+            s.cache.attend(*args, out=out, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        assert s.cache.status(stream) == LORA_OK
