@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from .kv import KvCache, PageTable
-from .lora import LoraLayer
+from .lora import LoraLayer, on_stream
 from .norm import lora_rms_norm
 
 
@@ -24,7 +24,7 @@ class AttentionBlock:
     all with an e4m3 base, or none of them.  ``norm_weight`` [hidden] is bf16.
 
     ``rotate(q, k, position)``, if given, turns q [T, q_heads, D] and k [T, kv_heads, D] in
-    place before the keys are cached."""
+    place before the keys are cached; its torch operations run on the pass's stream."""
 
     def __init__(self, q: LoraLayer, k: LoraLayer, v: LoraLayer, o: LoraLayer,
                  norm_weight: torch.Tensor, cache: KvCache, eps: float = 1e-6, rotate=None):
@@ -67,7 +67,8 @@ class AttentionBlock:
         D = self.cache.head_dim
         q, k, v, ctx = (r[:T].view(T, -1, D) for r in (self.qr, self.kr, self.vr, self.ctx))
         if self.rotate is not None:
-            self.rotate(q, k, pages.position[:T])
+            with on_stream(stream):
+                self.rotate(q, k, pages.position[:T])
         self.cache.append(k, v, pages.kv_slot[:T], stream)
         self.cache.attend(q, pages.q_offsets, pages.kv_len, pages.block_table, max_q, out=ctx,
                           stream=stream)

@@ -12,6 +12,7 @@ destroy on ``close``/garbage collection).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -170,6 +171,17 @@ def _stream(stream) -> int:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def on_stream(stream):
+    """Torch operations inside run on ``stream`` (None: the current one, a torch stream, or a
+    handle), as a call that takes it does."""
+    handle = _stream(stream)
+    if handle == _stream(None):
+        return contextlib.nullcontext()
+    if handle == 0:
+        return torch.cuda.stream(torch.cuda.default_stream())
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle))
 
 
 def _ptr(t) -> int:

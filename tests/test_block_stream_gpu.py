@@ -1,0 +1,52 @@
+"""The attention block on a stream that is not the current one, and what it refuses before it has
+changed anything."""
+import numpy as np
+import pytest
+import torch
+
+from test_block_gpu import B, HIDDEN, _Block, _rotate
+
+pytestmark = pytest.mark.gpu
+
+DEV, BF16 = "cuda", torch.bfloat16
+
+
+def _batch(blk, new, seed):
+    g = torch.Generator().manual_seed(seed)
+    x, h = (torch.randn(sum(new), HIDDEN, generator=g).to(BF16).to(DEV) for _ in range(2))
+    ids = torch.tensor([0, 3, -1, 1, 4, 2], dtype=torch.int32, device=DEV)
+    return torch.tensor(new, dtype=torch.int32, device=DEV), ids, x, h
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_rotation_on_the_blocks_stream(handle):
+    seen = []
+
+    def rotate(q, k, position):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        _rotate(q, k, position)
+
+    here, there = (_Block(False, 200, rotate) for _ in range(2))
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+    for i, new in enumerate(([40, 3, 0, 100, 17, 1], [1, 1, 60, 1, 100, 1], [1] * 6)):
+        counts, ids, x, h = _batch(here, new, i)
+        h2, y2 = h.clone(), torch.empty_like(x)
+        here.pages.step(counts, ids)
+        y = here.block.forward(x, h, here.pages, max(new))
+        torch.cuda.synchronize()
+        assert seen.pop() == torch.cuda.current_stream().cuda_stream
+        # the current stream is busy while the block runs beside it
+        torch.cuda._sleep(20_000_000)
+        there.pages.step(counts, ids, given)
+        there.block.forward(x, h2, there.pages, max(new), y2, given)
+        side.synchronize()
+        assert seen.pop() == side.cuda_stream and not seen
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+        assert there.cache.status() == 0 and there.pages.status()[3] == 0
+    # the default stream, by its handle
+    here.pages.step(counts, ids, 0)
+    here.block.forward(x, h, here.pages, 1, stream=0)
+    assert seen.pop() == torch.cuda.default_stream().cuda_stream
+    torch.cuda.synchronize()
