@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from .kv import KvCache, PageTable
-from .lora import LoraLayer, on_stream
+from .lora import LoraLayer, empty, on_stream
 from .norm import lora_rms_norm
 
 
@@ -73,6 +73,6 @@ class AttentionBlock:
         self.cache.attend(q, pages.q_offsets, pages.kv_len, pages.block_table, max_q, out=ctx,
                           stream=stream)
         if y is None:
-            y = torch.empty_like(x)
+            y = empty(x.shape, x.dtype, x.device, stream)
         self.o.set_batch(ids, stream)
         return self.o.forward(self.ctx[:T], y, stream)

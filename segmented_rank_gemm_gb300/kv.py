@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from .lora import LORA_EINVAL, LoraError, _stream, library
+from .lora import LORA_EINVAL, LoraError, _stream, empty, library
 
 _lib = library()
 _I32, _BF16 = torch.int32, torch.bfloat16
@@ -154,9 +154,9 @@ class KvCache:
         T = kv_slot.shape[0]
         shape = (T, self.kv_heads, self.head_dim)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=torch.bfloat16, device=kv_slot.device)
+            k_out = empty(shape, _BF16, kv_slot.device, stream)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=torch.bfloat16, device=kv_slot.device)
+            v_out = empty(shape, _BF16, kv_slot.device, stream)
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             _rows(name, t, shape)
             if not t.is_contiguous():
@@ -173,7 +173,7 @@ class KvCache:
         B = kv_len.shape[0]
         shape = (T, q_heads, self.head_dim)
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            out = empty(shape, _BF16, q.device, stream)
         if block_table.dim() != 2 or block_table.shape[0] < B:
             _bad("block_table must be [B, max_blocks]")
         if scale is None:

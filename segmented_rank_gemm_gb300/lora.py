@@ -184,6 +184,15 @@ def on_stream(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(handle))
 
 
+def empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for a call on ``stream`` to write: memory of that stream, since memory of another
+    one may still be in use there, or be given away there too early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t) -> int:
     if t is None:
         return 0
@@ -436,7 +445,7 @@ class LoraLayer:
             raise ValueError("x must be a CUDA tensor of the layer dtype")
         T = int(x.shape[0])
         if y is None:
-            y = torch.empty(T, self.N, dtype=self.dtype, device=x.device)
+            y = empty((T, self.N), self.dtype, x.device, stream)
         lora_forward(self.handle, x, y, T, stream)
         return y
 
@@ -452,7 +461,7 @@ class LoraLayer:
                     or not t.is_contiguous():
                 raise ValueError(f"{name} must be a dense CUDA tensor {shape} of {ok[0]}")
         if y is None:
-            y = torch.empty(T, self.N, dtype=self.dtype, device=x.device)
+            y = empty((T, self.N), self.dtype, x.device, stream)
         lora_forward_e4m3(self.handle, x, xq, sx, y, T, stream)
         return y
 

@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import torch
 
-from .lora import LORA_BF16, LORA_EINVAL, LORA_F32, LoraError, _stream, library
+from .lora import LORA_BF16, LORA_EINVAL, LORA_F32, LoraError, _stream, empty, library
 
 _lib = library()
 _DTYPES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
@@ -58,6 +58,6 @@ def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, xq=N
              stream=None):
     """``lora_rms_norm`` returning y; ``y`` is allocated if not given."""
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = empty(x.shape, x.dtype, x.device, stream)
     lora_rms_norm(x, weight, eps, residual, residual_out, y, xq, sx, stream)
     return y
