@@ -137,7 +137,8 @@ int lora_kv_read(lora_kv_cache_t* cache, const int32_t* kv_slot_dev, int T, void
  * the cache; the results of such requests are unspecified.
  * One call at a time per cache: calls share its workspace, so calls on several streams must
  * be ordered by the caller.
- * Limits: 1 <= B <= max_requests, 0 <= T <= 1 << 20, q_heads / kv_heads <= 64.
+ * Limits: 1 <= B <= max_requests, 0 <= T <= 1 << 20, q_heads / kv_heads <= 64; scale finite, and
+ * |scale| k_scale at most 7e36 (from about 7.3e36 on it is refused).
  * Errors: LORA_EINVAL, LORA_ECUDA.
  */
 int lora_kv_attend(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_heads,

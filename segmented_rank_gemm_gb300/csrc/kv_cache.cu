@@ -389,6 +389,11 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
       (static_cast<long long>(max_blocks) << c->pages.page_shift) > INT_MAX ||
       static_cast<long long>(B) * max_blocks > INT_MAX || !std::isfinite(scale))
     return fail(c, LORA_EINVAL, "max_q=%d, max_blocks=%d, scale=%g", max_q, max_blocks, scale);
+  // from products with the keys to scores in units of log2(e); the kernel for
+  // few rows multiplies it by kKvUnit
+  const float scale_log2 = scale * c->k_scale * 1.44269504088896341f;
+  if (!std::isfinite(scale_log2 * kKvUnit))
+    return fail(c, LORA_EINVAL, "scale=%g times k_scale=%g is too large", scale, c->k_scale);
   if (ldq < q_heads * D || ldo < q_heads * D || ldq % 8 || ldo % 8)
     return fail(c, LORA_EINVAL, "row distances %d, %d: multiples of 8 from %d up", ldq, ldo,
                 q_heads * D);
@@ -413,7 +418,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.max_q = max_q;
   a.group = q_heads / heads;
   a.group_magic = static_cast<uint32_t>((1ull << 32) / a.group + 1);
-  a.scale_log2 = scale * c->k_scale * 1.44269504088896341f;
+  a.scale_log2 = scale_log2;
   a.v_scale = c->v_scale;
   a.out = out;
   a.ldo = ldo;
