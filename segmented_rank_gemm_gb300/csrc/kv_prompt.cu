@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t p_at = tP + lanes + half * 32, o_at = tO + lanes + half * D;
     uint8_t* const scratch = sm + L::kScratch + warp * kScratchWarp;
-    const float unit = fmaxf(fabsf(a.scale_log2), 1e-30f);  // to scores in units of log2(e); never 0,
-                                                            // so that a masked score stays -inf
+    // from products to scores in units of log2(e); never 0, so that a masked score stays -inf (with
+    // a scale of 0 the keys are decoded to zeros)
+    const float unit = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
     // the softmax warps wait for one another, bounded like every wait
     uint32_t meetings = 0;
     auto meet_all = [&]() {
@@ -737,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const uint32_t sel_lo = vo & 1 ? 0x1054u : 0x5410u, sel_hi = vo & 1 ? 0x3276u : 0x7632u;
     const uint32_t sel[2] = {vd & 1 ? sel_hi : sel_lo, vd & 1 ? sel_lo : sel_hi};
     const bool swap = D == 128 && kc >= 2;  // these lanes decode their last 16 dimensions first
-    // 2^120, with the sign of the softmax's scale (whose size the scores are multiplied by)
-    const uint32_t k_unit = a.scale_log2 < 0.f ? 0xFB80FB80u : 0x7B807B80u;
+    // 2^120, with the sign of the softmax's scale (whose size the scores are multiplied by); 0 for 0
+    const uint32_t k_unit = a.scale_log2 < 0.f ? 0xFB80FB80u : a.scale_log2 > 0.f ? 0x7B807B80u : 0u;
     uint32_t n = 0;  // tiles decoded
     Segment g = {};
     // A segment's queries, copied a row's 16-byte pieces on consecutive lanes (rows past the last are

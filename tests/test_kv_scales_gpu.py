@@ -28,3 +28,17 @@ def test_products_of_scales_that_overflow_are_refused(scale, k_scale, fits):
             s.attend(q.to(DEV), new, scale, out=out)
         assert e.value.code == LORA_EINVAL and (out == 7).all()
     assert s.cache.status() == 0
+
+
+@pytest.mark.parametrize("scale,size", [(0.0, 1e33), (-0.0, 1.0), (3e-33, 1e32), (-2e-31, 1e30),
+                                        (1e-36, 3e36), (1e-30, 1.0), (2e-38, 1e5)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiny_scales_on_both_sides_of_the_row_threshold(scale, size, D):
+    # queries so large that scores are of ordinary size, or vanish; 24 rows a cache head and less go to
+    # one kernel, 28 and more to the other
+    kv, new = [130, 77, 300, 65, 40], [1, 6, 7, 40, 2]
+    s = Setup(kv, D, 1, 64, seed=42)
+    q = s.queries(new, 4, spread=size)
+    out = s.attend(q.to(DEV), new, scale)
+    assert s.cache.status() == 0
+    _close(out, s.expected(q, new, scale), np.abs(s.hv).max())
