@@ -92,7 +92,7 @@ int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_s
  * Create a cache of num_pages pages for kv_heads heads of head_dim dimensions.
  *   head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; 1 <= kv_heads <= 256;
  *   1 <= num_pages; num_pages * page_size < 2^31; 1 <= max_requests <= 16384: the most
- *   requests of an attention call; k_scale, v_scale: finite and positive.
+ *   requests of an attention call; k_scale, v_scale: positive, and finite times 7 (up to 4.8e37).
  * The pages are zero (value 0) until written; the call synchronises `stream`.  The cache
  * owns its pages and the attention's workspace.
  * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_ECUDA (then *out is NULL).

@@ -302,8 +302,8 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
   while (shift <= 8 && page_size != 1 << shift) ++shift;
   if (shift > 8 || num_pages < 1 || static_cast<long long>(num_pages) * page_size > INT_MAX ||
       kv_heads < 1 || kv_heads > 256 || (head_dim != 64 && head_dim != 128) || max_requests < 1 ||
-      max_requests > kMaxRequests || !(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) ||
-      !std::isfinite(v_scale))
+      max_requests > kMaxRequests || !(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(7.f * k_scale) ||
+      !std::isfinite(7.f * v_scale))
     return LORA_EINVAL;
   lora_kv_cache* c = new (std::nothrow) lora_kv_cache;
   if (!c) return LORA_ENOMEM;

@@ -42,3 +42,25 @@ def test_tiny_scales_on_both_sides_of_the_row_threshold(scale, size, D):
     out = s.attend(q.to(DEV), new, scale)
     assert s.cache.status() == 0
     _close(out, s.expected(q, new, scale), np.abs(s.hv).max())
+
+
+@pytest.mark.parametrize("g", [4.8e37, 4.9e37, 1e38, 3e38])
+def test_largest_scales_of_the_cache(g):
+    # the scale of a group is max|x| / (7 g) in fp32: refused where 7 g is none
+    from segmented_rank_gemm_gb300.kv import KvCache
+    from segmented_rank_gemm_gb300.lora import LORA_EINVAL, LoraError
+    if not np.isfinite(np.float32(7) * np.float32(g)):
+        for scales in ((g, 1.0), (1.0, g)):
+            with pytest.raises(LoraError) as e:
+                KvCache(4, 16, 2, 64, 1, *scales)
+            assert e.value.code == LORA_EINVAL
+        return
+    gen = torch.Generator().manual_seed(43)
+    k, v = ((torch.rand(64, 2, 64, generator=gen) * 2 - 1).mul(3e38).bfloat16() for _ in range(2))
+    cache = KvCache(4, 16, 2, 64, 1, g, g)
+    slots = _ints(np.arange(64))
+    cache.append(k.to(DEV), v.to(DEV), slots)
+    for got, x in zip(cache.read(slots), (k, v)):
+        want = torch.from_numpy(ref.held(_np(x), g).astype(np.float32)).bfloat16()
+        assert want.abs().max() > 1e38 and torch.equal(got.cpu(), want)
+    cache.close()
