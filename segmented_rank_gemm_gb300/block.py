@@ -6,8 +6,8 @@
 Every projection is a mixed-adapter layer (``lora.LoraLayer``); ``PageTable.step`` gives the
 batch's rows their adapter slots, positions and cache slots, so that the requests' lengths and
 pages never leave the GPU.  Prompts and single tokens share a batch.  A pass makes no host
-synchronisation and no allocation, and can be captured in a CUDA graph (with the batch's
-``PageTable.step`` or after it).
+synchronisation and, with y given, no allocation, and can be captured in a CUDA graph (with the
+batch's ``PageTable.step`` or after it).
 """
 from __future__ import annotations
 
@@ -29,7 +29,8 @@ class AttentionBlock:
     def __init__(self, q: LoraLayer, k: LoraLayer, v: LoraLayer, o: LoraLayer,
                  norm_weight: torch.Tensor, cache: KvCache, eps: float = 1e-6, rotate=None):
         D = cache.head_dim
-        if q.N % D or k.N != cache.kv_heads * D or v.N != k.N or o.K != q.N:
+        if q.N % (cache.kv_heads * D) or q.N > 64 * cache.kv_heads * D \
+                or k.N != cache.kv_heads * D or v.N != k.N or o.K != q.N:
             raise ValueError("the projections' widths do not fit the cache's heads")
         if not q.K == k.K == v.K or len({layer.fp8_base for layer in (q, k, v)}) != 1:
             raise ValueError("q, k and v must take the same rows")
@@ -51,8 +52,13 @@ class AttentionBlock:
         """x and the running residual ``h`` [T, hidden] (overwritten by h + x) of the batch that
         ``pages.step`` mapped last; ``max_q`` bounds a request's new tokens.  Returns y."""
         T = x.shape[0]
-        if T > self.max_tokens:
+        # (whatever can be refused is, before h and the cache change; x and h by the norm)
+        if T > min(self.max_tokens, pages.token_slot.shape[0]):
             raise ValueError("more rows than max_tokens")
+        if pages.page_size != self.cache.page_size or pages.max_requests > self.cache.max_requests:
+            raise ValueError("the page table does not fit the cache")
+        if max_q < 1:
+            raise ValueError("max_q must be positive")
         n, nq, sn = self.n[:T], None, None
         if self.nq is not None:
             nq, sn = self.nq[:T], self.sn[:T]

@@ -50,3 +50,26 @@ def test_rotation_on_the_blocks_stream(handle):
     here.block.forward(x, h, here.pages, 1, stream=0)
     assert seen.pop() == torch.cuda.default_stream().cuda_stream
     torch.cuda.synchronize()
+
+
+def test_refusals_come_before_the_residual_changes():
+    from segmented_rank_gemm_gb300.block import AttentionBlock
+    from segmented_rank_gemm_gb300.kv import KvCache, PageTable
+    blk = _Block(False, 60)
+    new = [3, 1, 1, 20, 1, 1]
+    counts, ids, x, h = _batch(blk, new, 7)
+    before = h.clone()
+    small = PageTable(200, 16, B, 40, sum(new) - 1)
+    pages = PageTable(200, 32, B, 40, 60)
+    more = PageTable(200, 16, B + 1, 40, 60)
+    for table, max_q in ((small, 20), (pages, 20), (more, 20), (blk.pages, 0), (blk.pages, -3)):
+        with pytest.raises(ValueError):
+            blk.block.forward(x, h, table, max_q)
+        assert torch.equal(h, before)
+    slots = torch.arange(200 * 16, dtype=torch.int32, device=DEV)
+    k, v = blk.cache.read(slots)
+    assert not k.any() and not v.any()
+    # heads that the cache's do not divide
+    q, kl, vl, o = blk.layers
+    with pytest.raises(ValueError):
+        AttentionBlock(q, kl, vl, o, blk.w, KvCache(8, 16, 3, 64, B))
