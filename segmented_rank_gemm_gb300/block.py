@@ -59,6 +59,11 @@ class AttentionBlock:
             raise ValueError("the page table does not fit the cache")
         if max_q < 1:
             raise ValueError("max_q must be positive")
+        if y is None:
+            y = empty(x.shape, x.dtype, x.device, stream)
+        elif y.dtype != torch.bfloat16 or y.shape != (T, self.o.N) or not y.is_cuda \
+                or not y.is_contiguous():
+            raise ValueError("y must be a dense CUDA bf16 tensor of x's shape")
         n, nq, sn = self.n[:T], None, None
         if self.nq is not None:
             nq, sn = self.nq[:T], self.sn[:T]
@@ -78,7 +83,5 @@ class AttentionBlock:
         self.cache.append(k, v, pages.kv_slot[:T], stream)
         self.cache.attend(q, pages.q_offsets, pages.kv_len, pages.block_table, max_q, out=ctx,
                           stream=stream)
-        if y is None:
-            y = empty(x.shape, x.dtype, x.device, stream)
         self.o.set_batch(ids, stream)
         return self.o.forward(self.ctx[:T], y, stream)

@@ -440,12 +440,19 @@ class LoraLayer:
         self._ids = token_slot
         set_batch_segments(self.handle, token_slot, int(token_slot.shape[0]), stream)
 
+    def _output(self, T: int, y, device, stream) -> torch.Tensor:
+        """y, or a new one: T rows of N for a forward to write."""
+        if y is None:
+            return empty((T, self.N), self.dtype, device, stream)
+        if y.dtype != self.dtype or not y.is_cuda or not y.is_contiguous() or y.numel() < T * self.N:
+            raise ValueError("y must be a dense CUDA tensor of the layer dtype, at least [T, N]")
+        return y
+
     def forward(self, x: torch.Tensor, y: torch.Tensor = None, stream=None) -> torch.Tensor:
         if x.dtype != self.dtype or not x.is_cuda:
             raise ValueError("x must be a CUDA tensor of the layer dtype")
         T = int(x.shape[0])
-        if y is None:
-            y = empty((T, self.N), self.dtype, x.device, stream)
+        y = self._output(T, y, x.device, stream)
         lora_forward(self.handle, x, y, T, stream)
         return y
 
@@ -460,8 +467,7 @@ class LoraLayer:
             if not t.is_cuda or t.dtype not in ok or tuple(t.shape) != shape \
                     or not t.is_contiguous():
                 raise ValueError(f"{name} must be a dense CUDA tensor {shape} of {ok[0]}")
-        if y is None:
-            y = empty((T, self.N), self.dtype, x.device, stream)
+        y = self._output(T, y, x.device, stream)
         lora_forward_e4m3(self.handle, x, xq, sx, y, T, stream)
         return y
 

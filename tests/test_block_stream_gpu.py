@@ -73,3 +73,38 @@ def test_refusals_come_before_the_residual_changes():
     q, kl, vl, o = blk.layers
     with pytest.raises(ValueError):
         AttentionBlock(q, kl, vl, o, blk.w, KvCache(8, 16, 3, 64, B))
+
+
+def _wrong_outputs(T, N):
+    return (torch.empty(T - 1, N, dtype=BF16, device=DEV), torch.empty(T, N - 8, dtype=BF16, device=DEV),
+            torch.empty(T, N, device=DEV), torch.empty(T, N, dtype=BF16),
+            torch.empty(T, N + 8, dtype=BF16, device=DEV)[:, :N])
+
+
+def test_outputs_that_do_not_fit_are_refused():
+    from segmented_rank_gemm_gb300 import workloads
+    from test_block_gpu import _layer
+    blk = _Block(False, 60)
+    new = [3, 1, 1, 20, 1, 1]
+    counts, ids, x, h = _batch(blk, new, 7)
+    before = h.clone()
+    blk.pages.step(counts, ids)
+    for y in _wrong_outputs(27, HIDDEN):
+        with pytest.raises(ValueError):
+            blk.block.forward(x, h, blk.pages, 20, y)
+        assert torch.equal(h, before)
+    for fp8_base in (False, True):
+        wl = workloads.synthetic(5, 40, 64, 72, S=2, ranks=4, R=4, base_frac=0.2)
+        layer = _layer(wl, 40, fp8_base)
+        xl = wl.x.to(DEV)
+        layer.set_batch(wl.token_slot.to(DEV))
+        xq = torch.zeros(40, 64, dtype=torch.uint8, device=DEV)
+        sx = torch.ones(40, device=DEV)
+        for y in _wrong_outputs(40, 72):
+            with pytest.raises(ValueError):
+                layer.forward(xl, y)
+            if fp8_base:
+                with pytest.raises(ValueError):
+                    layer.forward_e4m3(xl, xq, sx, y)
+        assert layer.status() == 0
+        layer.close()
