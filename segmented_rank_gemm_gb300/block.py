@@ -32,6 +32,10 @@ class AttentionBlock:
         if q.N % (cache.kv_heads * D) or q.N > 64 * cache.kv_heads * D \
                 or k.N != cache.kv_heads * D or v.N != k.N or o.K != q.N:
             raise ValueError("the projections' widths do not fit the cache's heads")
+        if o.N != q.K:
+            raise ValueError("o must give rows as wide as the block's")
+        if any(layer.dtype != torch.bfloat16 for layer in (q, k, v, o)):
+            raise ValueError("the projections must be bf16 layers")
         if not q.K == k.K == v.K or len({layer.fp8_base for layer in (q, k, v)}) != 1:
             raise ValueError("q, k and v must take the same rows")
         self.q, self.k, self.v, self.o = q, k, v, o

@@ -108,3 +108,16 @@ def test_outputs_that_do_not_fit_are_refused():
                     layer.forward_e4m3(xl, xq, sx, y)
         assert layer.status() == 0
         layer.close()
+
+
+def test_layers_that_do_not_fit_are_refused():
+    from segmented_rank_gemm_gb300.block import AttentionBlock
+    from segmented_rank_gemm_gb300.lora import LoraLayer
+    blk = _Block(False, 16)
+    q, k, v, o = blk.layers
+    wide = LoraLayer(torch.zeros(q.N, HIDDEN + 8, dtype=BF16, device=DEV), 5, 8, 16)
+    f32 = [LoraLayer(torch.zeros(layer.K, layer.N, device=DEV), 5, 8, 16) for layer in blk.layers]
+    for bad in ((q, k, v, wide), (f32[0], k, v, o), (q, f32[1], v, o), (q, k, f32[2], o), (q, k, v, f32[3]),
+                f32):
+        with pytest.raises(ValueError):
+            AttentionBlock(*bad, blk.w, blk.cache)
