@@ -80,7 +80,8 @@ class AttentionBlock:
             else:
                 layer.forward_e4m3(n, nq, sn, rows[:T], stream)
         D = self.cache.head_dim
-        q, k, v, ctx = (r[:T].view(T, -1, D) for r in (self.qr, self.kr, self.vr, self.ctx))
+        q, k, v, ctx = (r[:T].view(T, r.shape[1] // D, D)
+                        for r in (self.qr, self.kr, self.vr, self.ctx))
         if self.rotate is not None:
             with on_stream(stream):
                 self.rotate(q, k, pages.position[:T])

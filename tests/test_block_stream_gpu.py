@@ -121,3 +121,17 @@ def test_layers_that_do_not_fit_are_refused():
                 f32):
         with pytest.raises(ValueError):
             AttentionBlock(*bad, blk.w, blk.cache)
+
+
+@pytest.mark.parametrize("fp8_base", [False, True])
+def test_batch_without_rows(fp8_base):
+    blk = _Block(fp8_base, 60, _rotate)
+    counts, ids, x, h = _batch(blk, [2, 0, 0, 3, 0, 0], 8)
+    blk.pages.step(counts, ids)
+    blk.block.forward(x, h, blk.pages, 3)
+    blk.pages.step(torch.zeros_like(counts), ids)
+    y = blk.block.forward(x[:0], h[:0], blk.pages, 1)
+    assert y.shape == (0, HIDDEN) and y.dtype == BF16
+    torch.cuda.synchronize()
+    assert blk.pages.kv_len.tolist() == [2, 0, 0, 3, 0, 0] and blk.cache.status() == 0
+    assert all(layer.status() == 0 for layer in blk.layers)
