@@ -16,7 +16,8 @@
  * enqueue work and return without synchronising except where they say so; LORA_OK or a
  * negative lora_status (lora_layer.h) is returned; host-detectable errors enqueue nothing;
  * device-detectable errors never trap but raise a flag.  No call but lora_kv_cache_create
- * allocates; every other one can be captured in a CUDA graph.
+ * allocates; every other one can be captured in a CUDA graph.  The current device has to be the
+ * one a cache was created on (LORA_EINVAL else), and the arrays' own.
  *
  * Pages.  A page holds page_size consecutive positions of one request, for every head.
  * block_table [B, max_blocks] int32 names request b's pages in order; entries past

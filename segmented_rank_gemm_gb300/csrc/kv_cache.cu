@@ -287,6 +287,12 @@ void free_all(lora_kv_cache* c) {
     if (p) cudaFree(p);
 }
 
+// Whether the cache is the current device's: kernels are launched there.
+bool here(const lora_kv_cache* c) {
+  int device = -1;
+  return cudaGetDevice(&device) == cudaSuccess && device == c->device;
+}
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
@@ -346,6 +352,7 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
 int lora_kv_append(lora_kv_cache_t* c, const void* k, int ldk, const void* v, int ldv,
                    const int32_t* slots, int T, void* stream) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   const int width = c->pages.heads * c->pages.D;
   if (T < 0 || T > kMaxTokens) return fail(c, LORA_EINVAL, "T=%d", T);
   if (ldk < width || ldv < width || ldk % 8 || ldv % 8)
@@ -364,6 +371,7 @@ int lora_kv_append(lora_kv_cache_t* c, const void* k, int ldk, const void* v, in
 int lora_kv_read(lora_kv_cache_t* c, const int32_t* slots, int T, void* k_out, void* v_out,
                  void* stream) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   if (T < 0 || T > kMaxTokens) return fail(c, LORA_EINVAL, "T=%d", T);
   if (T == 0) return LORA_OK;
   if (!slots || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
@@ -379,6 +387,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
                    const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T,
                    int max_q, float scale, void* out, int ldo, void* stream) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   const int heads = c->pages.heads, D = c->pages.D;
   if (T < 0 || T > kMaxTokens) return fail(c, LORA_EINVAL, "T=%d", T);
   if (B < 1 || B > c->max_requests)
@@ -439,6 +448,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
 
 int lora_kv_get_status(lora_kv_cache_t* c, void* stream_) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int32_t flags = 0;
   KV_CUDA(c, cudaMemcpyAsync(&flags, c->err, sizeof(flags), cudaMemcpyDeviceToHost, stream));
@@ -457,6 +467,7 @@ int lora_kv_get_status(lora_kv_cache_t* c, void* stream_) {
 
 int lora_kv_wait_selftest(lora_kv_cache_t* c, void* stream) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   kv_wait_selftest_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       c->arrivals, 2 * kKvMaxCtas, c->err);
   KV_CUDA(c, cudaGetLastError());

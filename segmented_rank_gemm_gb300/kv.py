@@ -22,18 +22,19 @@ def _bad(what: str):
     raise LoraError(LORA_EINVAL, what)
 
 
-def _i32(name: str, t, n: int) -> int:
-    """The address of a contiguous CUDA int32 tensor of at least n elements."""
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        _bad("%s must be a contiguous CUDA int32 tensor of at least %d elements" % (name, n))
+def _i32(name: str, t, n: int, device: int) -> int:
+    """The address of a contiguous int32 tensor of at least n elements on the device."""
+    if t.dtype is not _I32 or t.get_device() != device or not t.is_contiguous() or t.numel() < n:
+        _bad("%s must be a contiguous int32 tensor of at least %d elements on the current CUDA "
+             "device" % (name, n))
     return t.data_ptr()
 
 
-def _rows(name: str, t, shape) -> int:
-    """The row distance of a CUDA bf16 tensor [T, heads, dim] whose rows are dense."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.shape != shape:
-        _bad("%s must be a CUDA bf16 tensor of shape %s, not %s %s" % (name, shape, t.dtype,
-                                                                     tuple(t.shape)))
+def _rows(name: str, t, shape, device: int) -> int:
+    """The row distance of a bf16 tensor [T, heads, dim] on the device whose rows are dense."""
+    if t.dtype is not _BF16 or t.get_device() != device or t.shape != shape:
+        _bad("%s must be a bf16 tensor of shape %s on the current CUDA device, not %s %s on %s"
+             % (name, shape, t.dtype, tuple(t.shape), t.device))
     row, head, one = t.stride()
     if (shape[2] > 1 and one != 1) or (shape[1] > 1 and head != shape[2]):
         _bad("%s: the heads of a row must be dense" % name)
@@ -50,31 +51,31 @@ def lora_kv_maps(lens, new, adapter, page_size, block_table, free_pages, n_free,
                  q_offsets, position, kv_slot, token_slot, counts, stream=None) -> None:
     """Block tables and slot maps of one batch (``lora_kv_maps``).  ``adapter`` may be None;
     the token arrays' length is T, ``block_table`` is [B, max_blocks]."""
-    B, T = lens.shape[0], kv_slot.shape[0]
+    B, T, dev = lens.shape[0], kv_slot.shape[0], torch.cuda.current_device()
     if block_table.dim() != 2 or block_table.shape[0] < B:
         _bad("block_table must be [B, max_blocks]")
     rc = _lib.lora_kv_maps(
-        _i32("lens", lens, B), _i32("new", new, B),
-        None if adapter is None else _i32("adapter", adapter, B), B, T, page_size,
-        _i32("block_table", block_table, 1), block_table.shape[1],
-        _i32("free_pages", free_pages, 1), free_pages.shape[0], _i32("n_free", n_free, 1),
-        _i32("kv_len", kv_len, B), _i32("q_offsets", q_offsets, B + 1),
-        _i32("position", position, T), _i32("kv_slot", kv_slot, T),
-        _i32("token_slot", token_slot, T), _i32("counts", counts, 5), _stream(stream))
+        _i32("lens", lens, B, dev), _i32("new", new, B, dev),
+        None if adapter is None else _i32("adapter", adapter, B, dev), B, T, page_size,
+        _i32("block_table", block_table, 1, dev), block_table.shape[1],
+        _i32("free_pages", free_pages, 1, dev), free_pages.shape[0], _i32("n_free", n_free, 1, dev),
+        _i32("kv_len", kv_len, B, dev), _i32("q_offsets", q_offsets, B + 1, dev),
+        _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev),
+        _i32("token_slot", token_slot, T, dev), _i32("counts", counts, 5, dev), _stream(stream))
     _check(rc, "lora_kv_maps")
 
 
 def lora_kv_release(done, lens, page_size, block_table, free_pages, n_free, status,
                     stream=None) -> None:
     """Return the pages of the requests with ``done[b] != 0`` (``lora_kv_release``)."""
-    B = lens.shape[0]
+    B, dev = lens.shape[0], torch.cuda.current_device()
     if block_table.dim() != 2 or block_table.shape[0] < B:
         _bad("block_table must be [B, max_blocks]")
     rc = _lib.lora_kv_release(
-        _i32("done", done, B), _i32("lens", lens, B), B, page_size,
-        _i32("block_table", block_table, 1), block_table.shape[1],
-        _i32("free_pages", free_pages, 1), free_pages.shape[0], _i32("n_free", n_free, 1),
-        _i32("status", status, 1), _stream(stream))
+        _i32("done", done, B, dev), _i32("lens", lens, B, dev), B, page_size,
+        _i32("block_table", block_table, 1, dev), block_table.shape[1],
+        _i32("free_pages", free_pages, 1, dev), free_pages.shape[0], _i32("n_free", n_free, 1, dev),
+        _i32("status", status, 1, dev), _stream(stream))
     _check(rc, "lora_kv_release")
 
 
@@ -143,25 +144,25 @@ class KvCache:
 
     def append(self, k, v, kv_slot, stream=None) -> None:
         """Write k and v [T, kv_heads, head_dim] (bf16; rows may be apart) to ``kv_slot`` [T]."""
-        T = k.shape[0]
+        T, dev = k.shape[0], torch.cuda.current_device()
         shape = (T, self.kv_heads, self.head_dim)
-        ldk, ldv = _rows("k", k, shape), _rows("v", v, shape)
+        ldk, ldv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
         self._check(_lib.lora_kv_append(self.handle, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                        _i32("kv_slot", kv_slot, T), T, _stream(stream)))
+                                        _i32("kv_slot", kv_slot, T, dev), T, _stream(stream)))
 
     def read(self, kv_slot, k_out=None, v_out=None, stream=None):
         """The values held in ``kv_slot`` [T], as bf16 [T, kv_heads, head_dim]."""
-        T = kv_slot.shape[0]
+        T, dev = kv_slot.shape[0], torch.cuda.current_device()
         shape = (T, self.kv_heads, self.head_dim)
         if k_out is None:
             k_out = empty(shape, _BF16, kv_slot.device, stream)
         if v_out is None:
             v_out = empty(shape, _BF16, kv_slot.device, stream)
         for name, t in (("k_out", k_out), ("v_out", v_out)):
-            _rows(name, t, shape)
+            _rows(name, t, shape, dev)
             if not t.is_contiguous():
                 _bad("%s must be contiguous" % name)
-        self._check(_lib.lora_kv_read(self.handle, _i32("kv_slot", kv_slot, T), T,
+        self._check(_lib.lora_kv_read(self.handle, _i32("kv_slot", kv_slot, T, dev), T,
                                       k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
         return k_out, v_out
 
@@ -170,7 +171,7 @@ class KvCache:
         """softmax(scale q K^T) V for q [T, q_heads, head_dim] (bf16; rows may be apart).
         ``scale`` is head_dim ** -0.5 by default; ``max_q`` bounds a request's query rows."""
         T, q_heads = q.shape[0], q.shape[1]
-        B = kv_len.shape[0]
+        B, dev = kv_len.shape[0], torch.cuda.current_device()
         shape = (T, q_heads, self.head_dim)
         if out is None:
             out = empty(shape, _BF16, q.device, stream)
@@ -179,10 +180,10 @@ class KvCache:
         if scale is None:
             scale = self.head_dim ** -0.5
         self._check(_lib.lora_kv_attend(
-            self.handle, q.data_ptr(), _rows("q", q, shape), q_heads,
-            _i32("q_offsets", q_offsets, B + 1), _i32("kv_len", kv_len, B),
-            _i32("block_table", block_table, 1), block_table.shape[1], B, T, max_q, scale,
-            out.data_ptr(), _rows("out", out, shape), _stream(stream)))
+            self.handle, q.data_ptr(), _rows("q", q, shape, dev), q_heads,
+            _i32("q_offsets", q_offsets, B + 1, dev), _i32("kv_len", kv_len, B, dev),
+            _i32("block_table", block_table, 1, dev), block_table.shape[1], B, T, max_q, scale,
+            out.data_ptr(), _rows("out", out, shape, dev), _stream(stream)))
         return out
 
     def status(self, stream=None) -> int:
