@@ -2,7 +2,7 @@
 // (include/lora_kv.h: lora_kv_attend).
 //
 // For one request and one cache head the query rows are columns: with G = q_heads / kv_heads,
-// column c is token c / G, head h G + c % G.  A group is (request, head, 8 NT columns); over its
+// column c is token c / G, head h G + c % G.  A group is (request, head, 8 columns); over its
 // cached positions j, in tiles of 32,
 //     s_jc = scale <k_j, q_c>,   p_jc = 2^(s_jc - m_c),   l_c = sum_j p_jc,   O_c = sum_j p_jc v_j
 // with s in units of log2(e) and m_c a running reference: O_c / l_c does not depend on it, so it
@@ -54,8 +54,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;    // positions of a tile
+constexpr int kCols = 8;     // columns of a group
 constexpr int kStages = 3;   // tiles of a warp's ring
-// Units a group counts before its tiles (512 single tokens: 67.0 us with 2, 68.7 with 3, 71.8 with
+// Units a group counts before its tiles (512 single tokens: 63.5 us with 2, 64.4 with 3, 67.2 with
 // 4), and units of a CTA's range, at least (one request of 1000 positions: 12.8 us with 4, 13.9 with
 // 8, 14.8 with 16; 4 requests of 512 over one head 13.5, 16.2 with 8).
 constexpr int kSetup = 2;
@@ -93,7 +94,6 @@ struct Request {
 
 // Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
 // one before stands ahead of them.)
-template <int NT>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bool report) {
   Request r;
   r.row0 = load_in_order(a.q_offsets + b);
@@ -110,7 +110,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
   const int G = a.group;
   r.tiles = max(1, (r.kv + kTile - 1) / kTile);
-  r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + 8 * NT - 1) / (8 * NT);
+  r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + kCols - 1) / kCols;
   return r;
 }
 
@@ -120,7 +120,6 @@ __device__ __forceinline__ long long request_units(const Request& r, int heads) 
 
 // A position in the sequence of tiles: request, head, column tile, tile (fastest last), and
 // the tile's unit: a group's tiles come after its kSetup units.
-template <int NT>
 struct Cursor {
   Request r;
   int b, head, col, tile;
@@ -130,7 +129,7 @@ struct Cursor {
   __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at,
                                         int snap) {
     b = b_;
-    r = load_request<NT>(a, b, false);
+    r = load_request(a, b, false);
     const int per = r.tiles + kSetup;
     const long long group = quotient(rem, per);
     const int off = static_cast<int>(rem - group * per);
@@ -149,16 +148,16 @@ struct Cursor {
     head = 0;
     do {
       ++b;
-      r = load_request<NT>(a, b, false);
+      r = load_request(a, b, false);
     } while (r.col_tiles == 0);
   }
 };
 
 // ---- partial results ----
-// A piece: m [8 NT], l [8 NT], O [8 NT][D].
-template <int D, int NT>
+// A piece: m [8], l [8], O [8][D].
+template <int D>
 constexpr int piece_floats() {
-  return 8 * NT * (D + 2);
+  return kCols * (D + 2);
 }
 
 struct PieceInfo {
@@ -169,18 +168,17 @@ struct PieceInfo {
   const float* at;
 };
 
-template <int D, int NT>
+template <int D>
 struct State {
-  float o[D / 16][NT][4];  // [dimension pair][column tile][fragment]
-  float2 minus[NT], l[NT];  // -m and l of the fragment's two columns
+  float o[D / 16][4];  // [dimension pair][fragment]
+  float2 minus, l;     // -m and l of the fragment's two columns
 };
 
 // Columns' rows in q and out: the element offset of column c, or -1.
-template <int NT>
 __device__ __forceinline__ long long column_offset(const KvAttendArgs& a, const Request& r, int head,
                                                    int col_tile, int c, int ld) {
   const int G = a.group;
-  const int col = col_tile * 8 * NT + c;
+  const int col = col_tile * kCols + c;
   if (col >= r.q_len * G) return -1;
   const int token = a.token_of(col);
   return static_cast<long long>(r.row0 + token) * ld +
@@ -210,8 +208,8 @@ __device__ __forceinline__ void fetch_two(uint32_t mine, uint32_t dst, const uin
       : "memory");
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(KvAttendArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAttendArgs a) {
   constexpr int kBlock = kv_block_bytes(D), kTileBytes = 2 * kBlock;
   constexpr int KT = D / 16;         // 16-wide steps of D
   constexpr int KW = D / 32;         // 32-bit words of K a lane reads of a token
@@ -243,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b)
-    mine += request_units(load_request<NT>(a, b, blockIdx.x == 0), heads);
+    mine += request_units(load_request(a, b, blockIdx.x == 0), heads);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       long long rem = at - before;
       int b = b0;
       for (; b < b1 - 1; ++b) {  // (the run's last takes what is left)
-        const long long n = request_units(load_request<NT>(a, b, false), heads);
+        const long long n = request_units(load_request(a, b, false), heads);
         if (rem < n) break;
         rem -= n;
       }
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     }
   }
   __syncthreads();
-  Cursor<NT> in;
+  Cursor in;
 #pragma unroll 1
   for (int w = kWarps + warp; w >= 0; w -= kWarps) {  // this warp's first tile; warp 0: the CTA's end too
     if (w > kWarps) continue;
@@ -308,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   const long long w_lo = cut_unit[warp], w_hi = cut_unit[warp + 1];
   const long long cta_lo = cut_unit[0], cta_hi = cut_unit[kWarps];
   float* const warp_pieces =
-      a.pieces + static_cast<size_t>(gridDim.x) * 2 * piece_floats<D, NT>() +
-      static_cast<size_t>(blockIdx.x * kWarps + warp) * 2 * piece_floats<D, NT>();
+      a.pieces + static_cast<size_t>(gridDim.x) * 2 * piece_floats<D>() +
+      static_cast<size_t>(blockIdx.x * kWarps + warp) * 2 * piece_floats<D>();
   if (w_lo < w_hi && in.tile == in.r.tiles) {  // the cut moved to its group's end
     if (w_lo + kSetup < w_hi) in.next_group(a);
     else in.unit = w_hi;
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   if (w_lo < w_hi && in.unit < w_hi) {
     uint8_t* const my_ring = ring + warp * kStages * kTileBytes;
     uint64_t* const bar = full[warp];
-    Cursor<NT> at = in;
+    Cursor at = in;
     const int shift = a.pages.page_shift;
     const uint32_t page_bytes = static_cast<uint32_t>(kBlock) << (shift - 4);  // of one head
     const size_t page_stride = static_cast<size_t>(page_bytes) * heads;
@@ -382,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     aim();
     for (int i = 0; i < kStages; ++i) fetch(i);
 
-    uint32_t qf[KT][NT][2];
-    int lim[NT][2];
-    float2 unit[NT];  // from products to scores in units of log2(e)
-    State<D, NT> st;
+    uint32_t qf[KT][2];
+    int lim[2];
+    float2 unit;  // from products to scores in units of log2(e)
+    State<D> st;
     const int ta = kv_frag_token(g);  // tokens of fragment rows g and g + 8: ta, ta + 8
     const int tv = (t & 1) | (t >> 1) << 1;
     const int G = a.group;
@@ -396,60 +394,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     while (at.unit < w_hi) {
       // the group's queries, the last position each column sees, and an empty state
       const long long group = at.unit - at.tile;
+      const long long off = column_offset(a, at.r, at.head, at.col, g, a.ldq);
+      const uint4* src =
+          reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off + t * (D / 4));
+      uint4 v[KW];
+      float top = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const long long off = column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + g, a.ldq);
-        const uint4* src =
-            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off + t * (D / 4));
-        uint4 v[KW];
-        float top = 0.f;
+      for (int w = 0; w < KW; ++w) {
+        v[w] = off >= 0 ? load_in_order(src + w) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          v[w] = off >= 0 ? load_in_order(src + w) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e with top 2^e in [2^9, 2^10); rows of zeros, infinities or tiny values keep e in range
-        const int e = top > 0.f && top < INFINITY
-                          ? min(120, 9 + 127 - static_cast<int>(__float_as_uint(top) >> 23))
-                          : 0;
-        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e + 127) << 23), a.scale_log2);
-        const float up16 = up * 0x1p-4f;  // of the dimensions whose keys come sixteen times as large
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            qf[2 * w + (i >> 1)][nt][i & 1] =
-                i & 1 ? pack_f16x2(bf16_lo(x[i]) * up16, bf16_hi(x[i]) * up16)
-                      : pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
-        }
-        // (never 0, so that a masked score stays -inf)
-        const float down =
-            fmaxf(kKvUnit * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
-        unit[nt].x = __shfl_sync(0xffffffffu, down, 8 * t);
-        unit[nt].y = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          // (a column past the last has zero queries and is not written: any limit does)
-          const int c = at.col * 8 * NT + nt * 8 + 2 * t + j;
-          lim[nt][j] = at.r.kv - at.r.q_len + min(a.token_of(c), at.r.q_len - 1);
-        }
-        st.minus[nt] = make_float2(-kNone, -kNone);
-        st.l[nt] = make_float2(0.f, 0.f);
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
       }
-      const int lim_lo = at.r.kv - at.r.q_len + a.token_of(at.col * 8 * NT);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^e with top 2^e in [2^9, 2^10); rows of zeros, infinities or tiny values keep e in range
+      const int e = top > 0.f && top < INFINITY
+                        ? min(120, 9 + 127 - static_cast<int>(__float_as_uint(top) >> 23))
+                        : 0;
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e + 127) << 23), a.scale_log2);
+      const float up16 = up * 0x1p-4f;  // of the dimensions whose keys come sixteen times as large
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qf[2 * w + (i >> 1)][i & 1] =
+              i & 1 ? pack_f16x2(bf16_lo(x[i]) * up16, bf16_hi(x[i]) * up16)
+                    : pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+      }
+      // (never 0, so that a masked score stays -inf)
+      const float down =
+          fmaxf(kKvUnit * fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-30f);
+      unit.x = __shfl_sync(0xffffffffu, down, 8 * t);
+      unit.y = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // (a column past the last has zero queries and is not written: any limit does)
+        const int c = at.col * kCols + 2 * t + j;
+        lim[j] = at.r.kv - at.r.q_len + min(a.token_of(c), at.r.q_len - 1);
+      }
+      st.minus = make_float2(-kNone, -kNone);
+      st.l = make_float2(0.f, 0.f);
+      const int lim_lo = at.r.kv - at.r.q_len + a.token_of(at.col * kCols);
       const int lim_hi =
-          at.r.kv - at.r.q_len + a.token_of(min(at.r.q_len * G - 1, at.col * 8 * NT + 8 * NT - 1));
+          at.r.kv - at.r.q_len + a.token_of(min(at.r.q_len * G - 1, at.col * kCols + kCols - 1));
 #pragma unroll
       for (int m = 0; m < KT; ++m)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) st.o[m][nt][j] = 0.f;
+        for (int j = 0; j < 4; ++j) st.o[m][j] = 0.f;
 
       const int count = static_cast<int>(min(static_cast<long long>(at.r.tiles - at.tile), w_hi - at.unit));
       for (int i = 0; i < count; ++i) {
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
         const int pos0 = (at.tile + i) * kTile;
         if (pos0 <= lim_hi) {
           const uint8_t* tile = my_ring + stage * kTileBytes;
-          float2 s[2][NT][2];  // [block][column tile][row g, row g + 8]
+          float2 s[2][2];  // [block][row g, row g + 8]
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint8_t* blk = tile + k * kBlock;
@@ -483,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
               sc[0] = both_lo(both);
               sc[1] = both_hi(both);
             }
-            float acc[NT][4];
+            float acc[4];
 #pragma unroll
             for (int p = 0; p < KW / 2; ++p) {  // the lane's scale groups
               Decode16 dec[2];
@@ -495,83 +488,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                 uint32_t v[2][4];
                 decode4(kw[0][w], dec[0], v[0]);
                 decode4(kw[1][w], dec[1], v[1]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if (w == 0)
-                    mma_f16_first(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[0][nt][0], qf[0][nt][1]);
-                  else
-                    mma_f16(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][nt][0],
-                            qf[2 * w][nt][1]);
-                  mma_f16(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][nt][0],
-                          qf[2 * w + 1][nt][1]);
-                }
+                if (w == 0)
+                  mma_f16_first(acc, v[0][0], v[1][0], v[0][1], v[1][1], qf[0][0], qf[0][1]);
+                else
+                  mma_f16(acc, v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][0], qf[2 * w][1]);
+                mma_f16(acc, v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
               }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              s[k][nt][0] = make_float2(acc[nt][0], acc[nt][1]);
-              s[k][nt][1] = make_float2(acc[nt][2], acc[nt][3]);
-            }
+            s[k][0] = make_float2(acc[0], acc[1]);
+            s[k][1] = make_float2(acc[2], acc[3]);
           }
 
           if (pos0 + kTile - 1 > lim_lo) {  // positions a column does not see
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const int pos = pos0 + k * kKvBlock + ta + r * 8;
-                  if (pos > lim[nt][0]) s[k][nt][r].x = -INFINITY;
-                  if (pos > lim[nt][1]) s[k][nt][r].y = -INFINITY;
-                }
+              for (int r = 0; r < 2; ++r) {
+                const int pos = pos0 + k * kKvBlock + ta + r * 8;
+                if (pos > lim[0]) s[k][r].x = -INFINITY;
+                if (pos > lim[1]) s[k][r].y = -INFINITY;
+              }
           }
-          float2 top[NT];
-          bool over = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            top[nt].x = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
-            top[nt].y = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
-            over |= fmaf(top[nt].x, unit[nt].x, st.minus[nt].x) > kRef + kSlack ||
-                    fmaf(top[nt].y, unit[nt].y, st.minus[nt].y) > kRef + kSlack;
-          }
+          float2 top;
+          top.x = fmaxf(fmaxf(s[0][0].x, s[0][1].x), fmaxf(s[1][0].x, s[1][1].x));
+          top.y = fmaxf(fmaxf(s[0][0].y, s[0][1].y), fmaxf(s[1][0].y, s[1][1].y));
+          const bool over = fmaf(top.x, unit.x, st.minus.x) > kRef + kSlack ||
+                            fmaf(top.y, unit.y, st.minus.y) > kRef + kSlack;
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int d = 4; d <= 16; d <<= 1) {
+              top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, d));
+              top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, d));
+            }
+            const float2 minus = make_float2(fminf(st.minus.x, kRef - top.x * unit.x),
+                                             fminf(st.minus.y, kRef - top.y * unit.y));
+            const float fx = ex2(minus.x - st.minus.x), fy = ex2(minus.y - st.minus.y);
+            st.minus = minus;
+            st.l.x *= fx;
+            st.l.y *= fy;
 #pragma unroll
-              for (int d = 4; d <= 16; d <<= 1) {
-                top[nt].x = fmaxf(top[nt].x, __shfl_xor_sync(0xffffffffu, top[nt].x, d));
-                top[nt].y = fmaxf(top[nt].y, __shfl_xor_sync(0xffffffffu, top[nt].y, d));
-              }
-              const float2 minus = make_float2(fminf(st.minus[nt].x, kRef - top[nt].x * unit[nt].x),
-                                               fminf(st.minus[nt].y, kRef - top[nt].y * unit[nt].y));
-              const float fx = ex2(minus.x - st.minus[nt].x), fy = ex2(minus.y - st.minus[nt].y);
-              st.minus[nt] = minus;
-              st.l[nt].x *= fx;
-              st.l[nt].y *= fy;
-#pragma unroll
-              for (int d = 0; d < KT; ++d) {
-                st.o[d][nt][0] *= fx;
-                st.o[d][nt][1] *= fy;
-                st.o[d][nt][2] *= fx;
-                st.o[d][nt][3] *= fy;
-              }
+            for (int d = 0; d < KT; ++d) {
+              st.o[d][0] *= fx;
+              st.o[d][1] *= fy;
+              st.o[d][2] *= fx;
+              st.o[d][3] *= fy;
             }
           }
 
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint8_t* blk = tile + k * kBlock;
-            uint32_t pf[NT][2];
+            uint32_t pf[2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float2 x = fma2(s[k][nt][r], unit[nt], st.minus[nt]);
-                const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                st.l[nt] = add2(st.l[nt], p);
-                pf[nt][r] = transpose_8x8(pack_f16x2(p.x, p.y));
-              }
+            for (int r = 0; r < 2; ++r) {
+              const float2 x = fma2(s[k][r], unit, st.minus);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              st.l = add2(st.l, p);
+              pf[r] = transpose_8x8(pack_f16x2(p.x, p.y));
             }
             // V: lane group t's four tokens, this lane's LD dimensions
             uint32_t vw[4][VW], vs;
@@ -600,11 +573,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
                 for (int r = 0; r < 2; ++r)
                   decode4(prmt(vw[2 * r][w], vw[2 * r + 1][w], hf ? 0x7632 : 0x5410), dec[r], v[r]);
                 const int m = w * 4 + hf * 2;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma_f16(st.o[m][nt], v[0][0], v[0][1], v[1][0], v[1][1], pf[nt][0], pf[nt][1]);
-                  mma_f16(st.o[m + 1][nt], v[0][2], v[0][3], v[1][2], v[1][3], pf[nt][0], pf[nt][1]);
-                }
+                mma_f16(st.o[m], v[0][0], v[0][1], v[1][0], v[1][1], pf[0], pf[1]);
+                mma_f16(st.o[m + 1], v[0][2], v[0][3], v[1][2], v[1][3], pf[0], pf[1]);
               }
           }
         }
@@ -618,58 +588,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       const bool whole = at.tile + count == at.r.tiles && group >= w_lo;
 
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) {
-          st.l[nt].x += __shfl_xor_sync(0xffffffffu, st.l[nt].x, d);
-          st.l[nt].y += __shfl_xor_sync(0xffffffffu, st.l[nt].y, d);
-        }
+      for (int d = 4; d <= 16; d <<= 1) {
+        st.l.x += __shfl_xor_sync(0xffffffffu, st.l.x, d);
+        st.l.y += __shfl_xor_sync(0xffffffffu, st.l.y, d);
+      }
       if (whole) {
         const float back = kKvUnit * a.v_scale;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < 2; ++j) {
+          const long long off = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.ldo);
+          if (off < 0) continue;
+          const float l = j ? st.l.y : st.l.x;
+          const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const long long off =
-                column_offset<NT>(a, at.r, at.head, at.col, nt * 8 + 2 * t + j, a.ldo);
-            if (off < 0) continue;
-            const float l = j ? st.l[nt].y : st.l[nt].x;
-            const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
+          for (int w = 0; w < LD / 8; ++w) {
+            uint32_t x[4];
 #pragma unroll
-            for (int w = 0; w < LD / 8; ++w) {
-              uint32_t x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[i] = pack_bf16x2(st.o[4 * w + i][nt][j] * f, st.o[4 * w + i][nt][j + 2] * f16);
-              dst[w] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
+            for (int i = 0; i < 4; ++i)
+              x[i] = pack_bf16x2(st.o[4 * w + i][j] * f, st.o[4 * w + i][j + 2] * f16);
+            dst[w] = make_uint4(x[0], x[1], x[2], x[3]);
           }
+        }
       } else {
         // a piece: slot 0 began before this warp's range, slot 1 goes on after it
         const int slot = group < w_lo ? 0 : 1;
         const bool last = at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi;
-        float* piece = last ? reinterpret_cast<float*>(my_ring) : warp_pieces + slot * piece_floats<D, NT>();
+        float* piece = last ? reinterpret_cast<float*>(my_ring) : warp_pieces + slot * piece_floats<D>();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = nt * 8 + 2 * t + j;
-            if (g == 0) {
-              piece[c] = -(j ? st.minus[nt].y : st.minus[nt].x);
-              piece[8 * NT + c] = j ? st.l[nt].y : st.l[nt].x;
-            }
-            float* o = piece + 16 * NT + c * D + g * LD;
-#pragma unroll
-            for (int m = 0; m < KT; m += 2)
-              *reinterpret_cast<float4*>(o + 2 * m) =
-                  make_float4(st.o[m][nt][j], st.o[m][nt][j + 2] * 0x1p-4f, st.o[m + 1][nt][j],
-                              st.o[m + 1][nt][j + 2] * 0x1p-4f);
+        for (int j = 0; j < 2; ++j) {
+          const int c = 2 * t + j;
+          if (g == 0) {
+            piece[c] = -(j ? st.minus.y : st.minus.x);
+            piece[kCols + c] = j ? st.l.y : st.l.x;
           }
+          float* o = piece + 2 * kCols + c * D + g * LD;
+#pragma unroll
+          for (int m = 0; m < KT; m += 2)
+            *reinterpret_cast<float4*>(o + 2 * m) =
+                make_float4(st.o[m][j], st.o[m][j + 2] * 0x1p-4f, st.o[m + 1][j], st.o[m + 1][j + 2] * 0x1p-4f);
+        }
         if (lane == 0)
           info[warp * 2 + slot] =
-              PieceInfo{group, at.r.tiles, min(8 * NT, at.r.q_len * G - at.col * 8 * NT), at.r.row0,
-                        at.head, at.col * 8 * NT, piece};
+              PieceInfo{group, at.r.tiles, min(kCols, at.r.q_len * G - at.col * kCols), at.r.row0,
+                        at.head, at.col * kCols, piece};
       }
       if (at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi) break;
       at.next_group(a);
@@ -682,12 +644,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   // Join column c of n pieces, in the order of the sequence, into dst (a piece) or the output:
   // one warp, the weights 2^(m_i - max m) one piece a lane, then the weighted sum, whose loads
   // do not wait for one another.
-  constexpr int NC = 8 * NT, kPiece = piece_floats<D, NT>(), VL = D / 32, kAhead = 4;
+  constexpr int kPiece = piece_floats<D>(), VL = D / 32, kAhead = 4;
   const auto join_column = [&](auto piece_of, auto load, int n, const PieceInfo& gi, int c, float* dst) {
     using Vec = std::conditional_t<VL == 4, float4, float2>;
     float o[VL] = {};
     const auto ask = [&](int k) {
-      return load(reinterpret_cast<const Vec*>(piece_of(k) + 2 * NC + c * D + lane * VL));
+      return load(reinterpret_cast<const Vec*>(piece_of(k) + 2 * kCols + c * D + lane * VL));
     };
     const auto add = [&](float w, const Vec& x) {
       o[0] += w * x.x, o[1] += w * x.y;
@@ -707,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
       if (i0 + lane < n) {
         const float* p = piece_of(i0 + lane);
         f = ex2(load(p + c) - m);
-        l += f * load(p + NC + c);
+        l += f * load(p + kCols + c);
       }
       const int some = min(32, n - i0);
       if (i0 == 0) {
@@ -723,11 +685,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
     if (dst) {
       if (lane == 0) {
         dst[c] = m;
-        dst[NC + c] = l;
+        dst[kCols + c] = l;
       }
 #pragma unroll
       for (int i = 0; i < VL; i += 2)
-        *reinterpret_cast<float2*>(dst + 2 * NC + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
+        *reinterpret_cast<float2*>(dst + 2 * kCols + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
@@ -796,25 +758,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv_attend_kernel(Kv
   }
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   constexpr int smem = kWarps * kStages * 2 * kv_block_bytes(D);
   static int limit[kAttrDevices] = {};
-  cudaError_t e = ensure_smem_limit(kv_attend_kernel<D, NT>, smem, limit);
+  cudaError_t e = ensure_smem_limit(kv_attend_kernel<D>, smem, limit);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(kKvMaxCtas, a.num_sms * kCtasPerSm);
-  return launch_dependent(kv_attend_kernel<D, NT>, dim3(ctas), kThreads, smem, stream, a);
+  return launch_dependent(kv_attend_kernel<D>, dim3(ctas), kThreads, smem, stream, a);
 }
 
 }  // namespace
 
 size_t kv_attend_workspace_floats(int num_sms, int D) {
   const size_t ctas = std::min(kKvMaxCtas, num_sms * kCtasPerSm);
-  return ctas * 2 * (1 + kWarps) * (D == 128 ? piece_floats<128, 1>() : piece_floats<64, 1>());
+  return ctas * 2 * (1 + kWarps) * (D == 128 ? piece_floats<128>() : piece_floats<64>());
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream) {
-  return a.pages.D == 128 ? launch<128, 1>(a, stream) : launch<64, 1>(a, stream);
+  return a.pages.D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
 }
 
 }  // namespace lora
