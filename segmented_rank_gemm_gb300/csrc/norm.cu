@@ -229,8 +229,9 @@ cudaError_t launch_width(const NormArgs& a, cudaStream_t stream) {
     if (n <= 512) return launch<T, VW, 128, 4, 128>(a, stream);
     if (n <= 1024) return launch<T, VW, 256, 4, 256>(a, stream);
     if (n <= 2048) return launch<T, VW, 512, 4, 512>(a, stream);
-    if (n <= 4096) return launch<T, VW, 1024, 4, 1024>(a, stream);
-    return launch<T, VW, 1024, 8, 1024>(a, stream);
+    if constexpr (kMaxWidth / VW > 4096)
+      if (n > 4096) return launch<T, VW, 1024, 8, 1024>(a, stream);
+    return launch<T, VW, 1024, 4, 1024>(a, stream);
   } else {
     if (n <= 128) return launch<T, VW, 32, 4, 128>(a, stream);
     if (n <= 512) return launch<T, VW, 32, 16, 128>(a, stream);
@@ -238,8 +239,9 @@ cudaError_t launch_width(const NormArgs& a, cudaStream_t stream) {
     if (n <= 2048) return launch<T, VW, 256, 8, 256>(a, stream);
     if (n <= 4096) return launch<T, VW, 512, 8, 512>(a, stream);
     if (n <= 8192) return launch<T, VW, 512, 16, 512>(a, stream);
-    if (n <= 16384) return launch<T, VW, 1024, 16, 1024>(a, stream);
-    return launch<T, VW, 1024, 32, 1024>(a, stream);
+    if constexpr (kMaxWidth / VW > 16384)
+      if (n > 16384) return launch<T, VW, 1024, 32, 1024>(a, stream);
+    return launch<T, VW, 1024, 16, 1024>(a, stream);
   }
 }
 
