@@ -61,7 +61,7 @@ def lora_kv_maps(lens, new, adapter, page_size, block_table, free_pages, n_free,
         _i32("free_pages", free_pages, 1, dev), free_pages.shape[0], _i32("n_free", n_free, 1, dev),
         _i32("kv_len", kv_len, B, dev), _i32("q_offsets", q_offsets, B + 1, dev),
         _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev),
-        _i32("token_slot", token_slot, T, dev), _i32("counts", counts, 5, dev), _stream(stream))
+        _i32("token_slot", token_slot, T, dev), _i32("counts", counts, 5, dev), _stream(stream, dev))
     _check(rc, "lora_kv_maps")
 
 
@@ -75,7 +75,7 @@ def lora_kv_release(done, lens, page_size, block_table, free_pages, n_free, stat
         _i32("done", done, B, dev), _i32("lens", lens, B, dev), B, page_size,
         _i32("block_table", block_table, 1, dev), block_table.shape[1],
         _i32("free_pages", free_pages, 1, dev), free_pages.shape[0], _i32("n_free", n_free, 1, dev),
-        _i32("status", status, 1, dev), _stream(stream))
+        _i32("status", status, 1, dev), _stream(stream, dev))
     _check(rc, "lora_kv_release")
 
 
@@ -148,7 +148,7 @@ class KvCache:
         shape = (T, self.kv_heads, self.head_dim)
         ldk, ldv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
         self._check(_lib.lora_kv_append(self.handle, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                        _i32("kv_slot", kv_slot, T, dev), T, _stream(stream)))
+                                        _i32("kv_slot", kv_slot, T, dev), T, _stream(stream, dev)))
 
     def read(self, kv_slot, k_out=None, v_out=None, stream=None):
         """The values held in ``kv_slot`` [T], as bf16 [T, kv_heads, head_dim]."""
@@ -163,7 +163,7 @@ class KvCache:
             if not t.is_contiguous():
                 _bad("%s must be contiguous" % name)
         self._check(_lib.lora_kv_read(self.handle, _i32("kv_slot", kv_slot, T, dev), T,
-                                      k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
+                                      k_out.data_ptr(), v_out.data_ptr(), _stream(stream, dev)))
         return k_out, v_out
 
     def attend(self, q, q_offsets, kv_len, block_table, max_q: int, scale: float = None, out=None,
@@ -183,7 +183,7 @@ class KvCache:
             self.handle, q.data_ptr(), _rows("q", q, shape, dev), q_heads,
             _i32("q_offsets", q_offsets, B + 1, dev), _i32("kv_len", kv_len, B, dev),
             _i32("block_table", block_table, 1, dev), block_table.shape[1], B, T, max_q, scale,
-            out.data_ptr(), _rows("out", out, shape, dev), _stream(stream)))
+            out.data_ptr(), _rows("out", out, shape, dev), _stream(stream, dev)))
         return out
 
     def status(self, stream=None) -> int:

@@ -163,10 +163,11 @@ def library() -> ctypes.CDLL:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int = None) -> int:
+    """The stream's handle; ``device``: the current device, where the caller has asked for it."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -51,7 +51,7 @@ def lora_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, xq=N
         None if residual_out is None else residual_out.data_ptr(), ldh,
         None if y is None else _dense("y", y, dtype, shape, dev),
         None if xq is None else _dense("xq", xq, torch.float8_e4m3fn, shape, dev),
-        None if sx is None else _dense("sx", sx, torch.float32, (T,), dev), _stream(stream))
+        None if sx is None else _dense("sx", sx, torch.float32, (T,), dev), _stream(stream, dev))
     if rc < 0:
         raise LoraError(rc, "lora_rms_norm")
 
