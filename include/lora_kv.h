@@ -131,8 +131,9 @@ int lora_kv_read(lora_kv_cache_t* cache, const int32_t* kv_slot_dev, int T, void
  * With q rows and n cached tokens, row i of a request sees positions 0 .. n - q + i.  A row
  * that sees nothing is zero, and so are rows outside every request.  Scores, the softmax's
  * maximum and sum and the output's accumulation are fp32; the products run on the tensor
- * cores from q as it is (bf16, or scaled by a power of two into fp16), the cache's exact
- * values, and probabilities as fp16.
+ * cores from q as it is (bf16, or scaled by a power of two into fp16, exactly from 2^-19 of a
+ * row's largest element on), the cache's exact values, and probabilities as fp16.  Scores have to
+ * stay below 2^24 in size: beyond, fp32 holds none of their fractions, and rows may be NaN.
  * Offsets that are not ascending within [0, T], lengths outside [0, max_blocks * page_size]
  * and page ids outside the cache are flagged (lora_kv_get_status) and read nothing outside
  * the cache; the results of such requests are unspecified.

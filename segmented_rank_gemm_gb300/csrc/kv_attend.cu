@@ -17,7 +17,8 @@
 //   O^T tile = V^T (16 dimensions x 16 tokens) P^T
 // in fp16 with fp32 accumulation.  K's and V's decoded values n s 2^-5 are exact in fp16.  A query
 // row is scaled by the power of two that brings its largest element to 2^9 .. 2^10, which its 8
-// significant bits survive down to 2^-23 of that.  p is rounded to fp16 (relative error 2^-11;
+// significant bits survive down to 2^-23 of that (2^-19 in the dimensions whose keys are decoded
+// sixteen times as large, and whose queries are that much smaller).  p is rounded to fp16 (relative error 2^-11;
 // with the reference at 2^6 it is a normal number down to 2^-20 of the maximum) while l sums
 // the fp32 p.
 //
@@ -31,8 +32,8 @@
 // between CTAs, by the last one to arrive, in the order of the pieces: results do not depend on
 // timing.
 //
-// Measured (32 query heads over 8 of 128): 3 contexts of 91 to 107 thousand positions 81.4 us, 350
-// MB at 4.3 TB/s; 512 single tokens over 1 to 2048 positions 62.9 us; one over 1000 12.8 us.  What
+// Measured (32 query heads over 8 of 128): 3 contexts of 91 to 107 thousand positions 82 us, 350
+// MB at 4.3 TB/s; 512 single tokens over 1 to 2048 positions 63 us; one over 1000 12.8 us.  What
 // bounds it: a tile is 617 instructions, half of them the decoding, of which a scheduler's four warps issue
 // three in four cycles in the main loop (the tiles stream at 5.7 TB/s there); before it lie 4.5 us of
 // launch, scan and first loads, and behind it the spread of the warps and the joins, 10 to 15 us.
@@ -57,8 +58,8 @@ constexpr int kTile = 32;    // positions of a tile
 constexpr int kCols = 8;     // columns of a group
 constexpr int kStages = 3;   // tiles of a warp's ring
 // Units a group counts before its tiles (512 single tokens: 63.5 us with 2, 64.4 with 3, 67.2 with
-// 4), and units of a CTA's range, at least (one request of 1000 positions: 12.8 us with 4, 13.9 with
-// 8, 14.8 with 16; 4 requests of 512 over one head 13.5, 16.2 with 8).
+// 4), and units of a CTA's range, at least (one request of 1000 positions: 12.8 us with 4, 12.7 with
+// 8, 14.1 with 16; 4 requests of 512 over one head 11.8, 12.6, 14.2).
 constexpr int kSetup = 2;
 constexpr int kMinSpan = 4;
 constexpr int kCtasPerSm = 2;
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   if (span * blockIdx.x >= total) return;
   const long long raw_lo = span * blockIdx.x, raw_hi = min(total, raw_lo + span);
   // A cut within snap of a group's edge moves there, which spares two pieces (512 tokens beside 8
-  // prompts: 84.8 us without, 83.1 with; 512 tokens alone 63.5 and 63.3, up to 65.5 for wspan / 4).
+  // prompts: 85.9 us without, 84.0 with; 512 tokens alone 62.8 and 63.2, 65.0 for wspan / 4; 256
+  // requests of 2 tokens over 300 positions 48.6 and 44.9).
   const int wspan = static_cast<int>((span + kWarps - 1) / kWarps), snap = min(wspan / 4, 2);
 #pragma unroll
   for (int w = 0; w <= kWarps; ++w) {

@@ -122,9 +122,9 @@ __device__ __forceinline__ void write_group(const uint4 lo, const uint4 hi, floa
 }
 
 // Bound: for large batches the instructions (about 14 a value, a third of them the quotient)
-// beside the bytes, for small ones the launch.  Measured with 8 heads of 128: 8192 tokens append
-// and read 16.7 us (77 MB, 4.6 TB/s; append under a profiler issues in 66% of its cycles); with 16 divisions a group, K and V in separate threads, 32.4 us.  512
-// tokens: 4.1 us for both.
+// beside the bytes, for small ones the launch.  Measured with 8 heads of 128: 8192 tokens 9.5 us (43
+// MB, 4.5 TB/s; under a profiler it issues in 66% of its cycles) and 16.6 with the read-back, where 16
+// divisions a group, K and V in separate threads, took 32.4; 512 tokens 2.1 us.
 // The kernel behind may start at once: what it reads of the cache it reads behind its own wait.
 __global__ void __launch_bounds__(kThreads)
     kv_append_kernel(KvPages pg, const __nv_bfloat16* k, int ldk, const __nv_bfloat16* v, int ldv,
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
   write_group<true>(v0, v1, v_scale, at.v, at.v_scale);
 }
 
-// The read-back.  Bound: bytes.  The pair of lanes that swap halves: a lane that stored its own 32
+// The read-back.  Bound: bytes (8192 tokens of 8 heads of 128 6.8 us, 6.3 TB/s).  The pair of lanes that swap halves: a lane that stored its own 32
 // bytes wrote half sectors twice, 2.5 million sector writes for 8192 tokens instead of 1.6.
 // Values n s g of a group: n s is exact in bf16 (kv_decode.cuh), so a cache of scale 1 gives it
 // as it is.
@@ -261,8 +261,8 @@ constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxRequests = 16384;
 // Rows a cache head (query rows times q_heads / kv_heads) up to which a request's attention runs
 // in the kernel for few rows, which costs by 8 rows what the one for many costs by 256.  Measured
-// over 8 heads of 128 (us, few / many): 64 requests of 1024 positions, 16 rows 54 / 66, 24 rows
-// 70 / 67, 32 rows 87 / 67; 8 of 4096, 41 / 42 at 24 and 48 / 42 at 32; 256 of 300, 72 / 100 and 91 / 99.
+// over 8 heads of 128 (us, few / many): 64 requests of 1024 positions, 16 rows 50 / 67, 24 rows
+// 66 / 67, 32 rows 82 / 67; 8 of 4096, 39 / 42 at 24 and 45 / 42 at 32; 256 of 300, 79 / 97 and 89 / 97.
 constexpr int kFewRows = 24;
 
 int fail(lora_kv_cache* c, int code, const char* fmt, ...) {

@@ -7,7 +7,8 @@
 //     S = Q K^T,   P = 2^(S unit - m),   l += sum P,   O += P V
 // with a running reference m per row that moves only when a score exceeds it by 2^8 (O / l does
 // not depend on m) and fp32 accumulators.  K is decoded to bf16 and V to fp16, both exactly; the
-// queries stay as they came, in bf16, and P is rounded to fp16 under a sum of its fp32 values.
+// queries stay as they came, in bf16, and P is rounded to fp16 under a sum of its fp32 values (2^-11 of
+// it, an eighth of the output's own rounding; 32-bit operands would halve the products' rate at least).
 //
 // Bound: the tensor cores, 4 D operations a score.  One CTA per SM, its warps in roles that meet
 // at barriers in shared memory:

@@ -216,8 +216,9 @@ cudaError_t launch(const NormArgs& a, cudaStream_t stream) {
 // rows of bf16 unless said): 1024 wide 7.6 with a warp a row, 9.5 with 128 threads of one chunk; 4096
 // wide 42.1 with 128 threads of four chunks, 45.2 with 256 of two, 52.0 with 512 of one; 8192
 // wide 80.6 with 256 of four, 97.8 with 512 of two; 32768 wide (2048 rows) 100 with 1024 of four,
-// 154 with 512 of eight; 4-byte floats, 14336 wide (4096 rows) 157 and 168 with the same.  Rows that no 16-byte vector fits (odd widths or distances) go by 4-byte pairs or by
-// elements: 1001 wide 13.4 us, 4090 wide 46.8, 4095 wide 68.6, where 256 threads of eight and 512 of 16 elements
+// 154 with 512 of eight; 4-byte floats, 14336 wide (4096 rows) 157 and 168 with the same.  Rows
+// that no 16-byte vector fits (odd widths or distances) go by 4-byte pairs or by elements: 1001
+// wide 13.4 us, 4090 wide 46.8, 4095 wide 68.6, where 256 threads of eight and 512 of 16 elements
 // took 22.7, 104 and 104.
 template <typename T, int VW>
 cudaError_t launch_width(const NormArgs& a, cudaStream_t stream) {
