@@ -314,6 +314,7 @@ def prepare(case, seed):
     st.update(q=d["q"], table=d["table"], kv_len=_ints(d["kv"]), max_q=max(d["new"]),
               q_offsets=_ints(np.concatenate(([0], np.cumsum(d["new"]))).tolist()),
               max_kv=max(d["kv"]), group_offsets=_ints(d["first"]),
+              prefix_row=_ints(d["first"][:-1]), prefix_len=_ints(d["shared"]),
               shared=_ints(d["share"].tolist()), out=torch.empty_like(d["q"]))
     if own:
         st["cache"] = _own_cache(d["pages"], case, case["requests"])
@@ -482,8 +483,8 @@ def _own_run(st):
         return cache.attend(st["q"], st["q_offsets"], st["kv_len"], st["table"], st["max_q"],
                             out=st["out"], causal=False)
     return cache.attend_shared(st["q"], st["q_offsets"], st["kv_len"], st["table"], st["max_q"],
-                               st["group_offsets"], st["shared"], out=st["out"],
-                               workspace=st["workspace"])
+                               st["group_offsets"], st["prefix_row"], st["prefix_len"],
+                               st["shared"], out=st["out"], workspace=st["workspace"])
 
 
 def run(state):
