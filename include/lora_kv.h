@@ -9,8 +9,12 @@
  *                     it takes, and per new token its position, its cache slot and its
  *                     request's adapter slot (what set_batch_segments takes)
  *   lora_kv_append    per block: the new tokens' keys and values into the cache
+ *                     (lora_kv_append_rotated: queries and keys turned by their positions first)
  *   lora_kv_attend    per block: their queries over everything their requests have cached
+ *                     (lora_kv_attend_shared: prefixes that requests share are read once for all of
+ *                     them; lora_kv_attend_cross: an encoder's states, without a causal mask)
  *   lora_kv_release   finished requests' pages back to the free stack
+ *                     (lora_kv_fork: a request starts with another's pages)
  *
  * The conventions of lora_layer.h hold: "stream" is a cudaStream_t passed as void*; calls
  * enqueue work and return without synchronising except where they say so; LORA_OK or a
@@ -90,6 +94,35 @@ int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_s
                     int stack_size, int32_t* n_free_dev, int32_t* status_dev, void* stream);
 
 /*
+ * Requests that start with the pages of others: for every b with parent_dev[b] >= 0, the first
+ * whole pages of request p = parent_dev[b] become the first of request b:
+ *     shared_dev[b] = want_dev[b] rounded down to whole pages, at most p's whole pages
+ *     len_dev[b] = shared_dev[b], and those entries of p's row of block_table are copied to b's.
+ *   parent_dev [B]  -1: request b stays as it is.  A parent has itself no parent in the call.
+ *   want_dev [B]    positions to share (or NULL: all whole pages).
+ *   len_dev, shared_dev [B], block_table: updated for those b.
+ *   status_dev [1]  0, or 1 (a parent below -1, from B up or with a parent in the call, its length
+ *                   negative or past max_blocks pages, a negative want_dev[b], or a request b that
+ *                   holds something: its length must be 0); then nothing is changed.
+ * The pages stay its parent's: they are valid
+ * while the parent holds them, and lora_kv_release_shared returns only what lies behind them.
+ * Errors: LORA_EINVAL, LORA_ECUDA.
+ */
+int lora_kv_fork(const int32_t* parent_dev, const int32_t* want_dev, int32_t* len_dev,
+                 int32_t* shared_dev, int B, int page_size, int32_t* block_table, int max_blocks,
+                 int32_t* status_dev, void* stream);
+
+/*
+ * lora_kv_release for requests that may have been forked: a request's first shared_dev[b] positions
+ * are not its own, so the pages behind them alone go back; shared_dev[b] becomes 0 with len_dev[b].
+ * status_dev is 1 also where shared_dev[b] is negative, not whole pages or above len_dev[b].
+ */
+int lora_kv_release_shared(const int32_t* done_dev, int32_t* len_dev, int32_t* shared_dev, int B,
+                           int page_size, const int32_t* block_table, int max_blocks,
+                           int32_t* free_pages, int stack_size, int32_t* n_free_dev,
+                           int32_t* status_dev, void* stream);
+
+/*
  * Create a cache of num_pages pages for kv_heads heads of head_dim dimensions.
  *   head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; 1 <= kv_heads <= 256;
  *   1 <= num_pages; num_pages * page_size < 2^31; 1 <= max_requests <= 16384: the most
@@ -110,6 +143,28 @@ int lora_kv_cache_create(lora_kv_cache_t** out, int num_pages, int page_size, in
  */
 int lora_kv_append(lora_kv_cache_t* cache, const void* k_dev, int ldk, const void* v_dev, int ldv,
                    const int32_t* kv_slot_dev, int T, void* stream);
+
+/*
+ * lora_kv_append with the rotation of queries and keys by their positions on the way.
+ *   q_dev, q_out    rows of q_heads * head_dim bf16, ldq and ldqo elements apart; q_out may be q_dev
+ *                   (with ldqo = ldq), or else does not overlap it; nor k and v, whose columns may
+ *                   lie beside it in the same rows.  1 <= q_heads <= 16384.
+ *   position [T]    each row's position, 0 .. max_position - 1.
+ *   angles          [max_position, rotary_dim / 2] pairs (cos, sin) fp32, 16-byte aligned: row p, pair
+ *                   i is the cosine and sine of p times pair i's frequency.
+ *   rotary_dim      the first dimensions of a head, which are turned: a multiple of 32 up to
+ *                   head_dim.  Pair i is dimensions i and i + rotary_dim / 2, or 2 i and 2 i + 1 if
+ *                   `interleaved`.
+ * A pair (a, b) with (c, s) becomes (a c - b s, b c + a s) in fp32, every product and sum rounded to
+ * nearest by itself.  Queries are rounded to bf16; keys are quantised from fp32.  Everything else
+ * as lora_kv_append; a row with a position outside the table is flagged, and neither its query nor
+ * its slot is written; one with slot -1 has its query turned.  Errors: LORA_EINVAL, LORA_ECUDA.
+ */
+int lora_kv_append_rotated(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_heads,
+                           void* q_out, int ldqo, const void* k_dev, int ldk, const void* v_dev,
+                           int ldv, const int32_t* position, const int32_t* kv_slot_dev, int T,
+                           const float* angles, int max_position, int rotary_dim, int interleaved,
+                           void* stream);
 
 /*
  * The values held in T slots, as bf16 (rounded from the fp32 product n s g): k_out and v_out
@@ -147,6 +202,46 @@ int lora_kv_attend(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_hea
                    const int32_t* q_offsets, const int32_t* kv_len, const int32_t* block_table,
                    int max_blocks, int B, int T, int max_q, float scale, void* out_dev, int ldo,
                    void* stream);
+
+/*
+ * lora_kv_attend without the causal mask: every row of a request sees all n of its cached
+ * positions -- a decoder's tokens over their request's encoder states, whose number has nothing
+ * to do with theirs.  Rows of a request with none are zero.  Everything else as lora_kv_attend.
+ */
+int lora_kv_attend_cross(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_heads,
+                         const int32_t* q_offsets, const int32_t* kv_len,
+                         const int32_t* block_table, int max_blocks, int B, int T, int max_q,
+                         float scale, void* out_dev, int ldo, void* stream);
+
+/*
+ * lora_kv_attend for requests that share prefixes by groups: the same result, but a prefix is read
+ * and decoded once for all rows of its group.
+ *   group_offsets [groups + 1]  group g is requests group_offsets[g] .. group_offsets[g+1] - 1.
+ *                   1 <= groups <= B; ascending, within [0, B].
+ *   prefix_row, prefix_len [groups]  the group's prefix: the first prefix_len[g] positions, whole
+ *                   pages (or 0), of the pages in row prefix_row[g] of block_table -- a member's,
+ *                   or those of the request that members were forked from (lora_kv_fork).
+ *   shared_len [B]  the first shared_len[b] positions of request b are its group's prefix:
+ *                   prefix_len[g], all before its new tokens.  With 0 the request, in a group or
+ *                   not, is attended as in lora_kv_attend.
+ *   workspace       lora_kv_shared_workspace bytes of device memory for T rows, 16-byte aligned, for
+ *                   the time of the call; it overlaps neither q nor out.
+ * Sharing pays where a group has many rows that see few keys of their own; requests whose rows fill
+ * the kernel's tiles by themselves (256 query rows a cache head) gain nothing by it.
+ * What lora_kv_attend flags is flagged, and prefixes that are not as above; results of the requests
+ * concerned, and of their group, are unspecified.  Limits and errors: as lora_kv_attend.
+ */
+int lora_kv_attend_shared(lora_kv_cache_t* cache, const void* q_dev, int ldq, int q_heads,
+                          const int32_t* q_offsets, const int32_t* kv_len,
+                          const int32_t* block_table, int max_blocks, int B, int T, int max_q,
+                          const int32_t* group_offsets, const int32_t* prefix_row,
+                          const int32_t* prefix_len, int groups, const int32_t* shared_len,
+                          float scale, void* out_dev, int ldo, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/* Bytes lora_kv_attend_shared needs for T rows: 8 (head_dim + 2) a row and query head.
+ * LORA_EINVAL for a T or q_heads out of range. */
+int64_t lora_kv_shared_workspace(const lora_kv_cache_t* cache, int T, int q_heads);
 
 /*
  * Synchronise `stream`, read and clear the cache's device error flags: LORA_OK, LORA_EID (a

@@ -59,6 +59,34 @@ def attend(q, k, v, scale):
     return out
 
 
+def attend_all(q, k, v, scale):
+    """As ``attend`` without the causal mask: every query sees all L positions (none: zeros)."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    out = np.zeros(q.shape)
+    group = q.shape[1] // k.shape[1]
+    for h in range(q.shape[1] if len(k) else 0):
+        s = scale * q[:, h] @ k[:, h // group].T
+        w = np.exp(s - s.max(-1, keepdims=True))
+        out[:, h] = (w / w.sum(-1, keepdims=True)) @ v[:, h // group]
+    return out
+
+
+def rotated(x, cos, sin, interleaved, dtype=np.float32):
+    """x [T, H, D] with its first dimensions turned by angles of [T, R / 2] cosines and sines, pairs
+    (i, i + R / 2) or (2 i, 2 i + 1): (a c - b s, b c + a s), each operation in ``dtype``."""
+    x = np.asarray(x, dtype)
+    cos, sin = (np.asarray(c, dtype)[:, None, :] for c in (cos, sin))
+    half = cos.shape[-1]
+    at = (np.arange(0, 2 * half, 2), np.arange(1, 2 * half, 2)) if interleaved else (
+        np.arange(half), np.arange(half, 2 * half))
+    out = x.copy()
+    with np.errstate(all="ignore"):
+        a, b = x[..., at[0]], x[..., at[1]]
+        out[..., at[0]] = a * cos - b * sin
+        out[..., at[1]] = b * cos + a * sin
+    return out
+
+
 def maps(lens, new, adapter, page, table, free, n_free, T):
     """lora_kv_maps in plain Python.  Returns the dict of its outputs (table a copy)."""
     B, blocks = table.shape

@@ -46,6 +46,7 @@
 
 #include "kv_decode.cuh"
 #include "kv_kernels.h"
+#include "kv_span.cuh"
 #include "lora_common.cuh"
 #include "lora_kernels.h"
 
@@ -89,14 +90,28 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
 }
 
 // ---- requests, groups and the sequence of tiles ----
+// The tiles start at position `first`, and the positions of a request's queries' limits count from
+// there: token t sees see + slope t (a span's; a whole causal request: 0, kv - q_len and 1).
 struct Request {
   int row0, q_len, kv, tiles, col_tiles;
+  int first, see, slope, table_row;
+  SpanKind kind;
+  __device__ __forceinline__ int last_seen(int token) const { return see + slope * token; }
 };
 
 // Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
 // one before stands ahead of them.)
+template <bool SPANS>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bool report) {
   Request r;
+  const int G = a.group;
+  if constexpr (SPANS) {
+    const Span s = load_span(a, b, report);
+    r = Request{s.row0, s.q_len, s.kv, 0, 0, s.first, s.see, s.slope, s.table_row, s.kind};
+    r.tiles = max(1, (r.kv - r.first + kTile - 1) / kTile);
+    r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + kCols - 1) / kCols;
+    return r;
+  }
   r.row0 = load_in_order(a.q_offsets + b);
   const int end = load_in_order(a.q_offsets + b + 1);
   r.kv = load_in_order(a.kv_len + b);
@@ -109,7 +124,11 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
     r.kv = min(max(r.kv, 0), cap);
   }
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
-  const int G = a.group;
+  r.first = 0;
+  r.see = r.kv - r.q_len;
+  r.slope = 1;
+  r.table_row = b;
+  r.kind = kSpanWhole;
   r.tiles = max(1, (r.kv + kTile - 1) / kTile);
   r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + kCols - 1) / kCols;
   return r;
@@ -121,6 +140,7 @@ __device__ __forceinline__ long long request_units(const Request& r, int heads) 
 
 // A position in the sequence of tiles: request, head, column tile, tile (fastest last), and
 // the tile's unit: a group's tiles come after its kSetup units.
+template <bool SPANS>
 struct Cursor {
   Request r;
   int b, head, col, tile;
@@ -130,7 +150,7 @@ struct Cursor {
   __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at,
                                         int snap) {
     b = b_;
-    r = load_request(a, b, false);
+    r = load_request<SPANS>(a, b, false);
     const int per = r.tiles + kSetup;
     const long long group = quotient(rem, per);
     const int off = static_cast<int>(rem - group * per);
@@ -149,7 +169,7 @@ struct Cursor {
     head = 0;
     do {
       ++b;
-      r = load_request(a, b, false);
+      r = load_request<SPANS>(a, b, false);
     } while (r.col_tiles == 0);
   }
 };
@@ -166,6 +186,7 @@ struct PieceInfo {
   int tiles;        // of the group
   int cols;         // its columns
   int row0, head, first_col;
+  SpanKind kind;
   const float* at;
 };
 
@@ -209,7 +230,7 @@ __device__ __forceinline__ void fetch_two(uint32_t mine, uint32_t dst, const uin
       : "memory");
 }
 
-template <int D>
+template <int D, bool SPANS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAttendArgs a) {
   constexpr int kBlock = kv_block_bytes(D), kTileBytes = 2 * kBlock;
   constexpr int KT = D / 16;         // 16-wide steps of D
@@ -238,11 +259,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   if (a.many_follow) griddep_launch_dependents();
 
   // the sequence's length and this CTA's range; where each warp starts
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const int count_b = SPANS ? a.B + a.groups : a.B;
+  const int per = (count_b + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, count_b), b1 = min(b0 + per, count_b);
   long long mine = 0;
   for (int b = b0; b < b1; ++b)
-    mine += request_units(load_request(a, b, blockIdx.x == 0), heads);
+    mine += request_units(load_request<SPANS>(a, b, blockIdx.x == 0), heads);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -286,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
       long long rem = at - before;
       int b = b0;
       for (; b < b1 - 1; ++b) {  // (the run's last takes what is left)
-        const long long n = request_units(load_request(a, b, false), heads);
+        const long long n = request_units(load_request<SPANS>(a, b, false), heads);
         if (rem < n) break;
         rem -= n;
       }
@@ -295,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
     }
   }
   __syncthreads();
-  Cursor in;
+  Cursor<SPANS> in;
 #pragma unroll 1
   for (int w = kWarps + warp; w >= 0; w -= kWarps) {  // this warp's first tile; warp 0: the CTA's end too
     if (w > kWarps) continue;
@@ -318,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   if (w_lo < w_hi && in.unit < w_hi) {
     uint8_t* const my_ring = ring + warp * kStages * kTileBytes;
     uint64_t* const bar = full[warp];
-    Cursor at = in;
+    Cursor<SPANS> at = in;
     const int shift = a.pages.page_shift;
     const uint32_t page_bytes = static_cast<uint32_t>(kBlock) << (shift - 4);  // of one head
     const size_t page_stride = static_cast<size_t>(page_bytes) * heads;
@@ -337,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         src_b = in.b;
         src_tile = in.tile & ~31;
         const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
-        const int32_t* row = a.table + static_cast<size_t>(in.b) * a.max_blocks;
-        const int pos = (src_tile + lane) * kTile;
-        const bool some = in.r.kv > 0;
+        const int32_t* row = a.table + static_cast<size_t>(in.r.table_row) * a.max_blocks;
+        const int pos = in.r.first + (src_tile + lane) * kTile;
+        const bool some = in.r.kv > in.r.first;
         int id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
         int id1 = some ? __ldg(row + min((pos + kKvBlock) >> shift, last)) : 0;
         const unsigned pages = a.pages.num_pages;
@@ -434,13 +456,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
       for (int j = 0; j < 2; ++j) {
         // (a column past the last has zero queries and is not written: any limit does)
         const int c = at.col * kCols + 2 * t + j;
-        lim[j] = at.r.kv - at.r.q_len + min(a.token_of(c), at.r.q_len - 1);
+        lim[j] = at.r.last_seen(min(a.token_of(c), at.r.q_len - 1));
       }
       st.minus = make_float2(-kNone, -kNone);
       st.l = make_float2(0.f, 0.f);
-      const int lim_lo = at.r.kv - at.r.q_len + a.token_of(at.col * kCols);
+      const int lim_lo = at.r.last_seen(a.token_of(at.col * kCols));
       const int lim_hi =
-          at.r.kv - at.r.q_len + a.token_of(min(at.r.q_len * G - 1, at.col * kCols + kCols - 1));
+          at.r.last_seen(a.token_of(min(at.r.q_len * G - 1, at.col * kCols + kCols - 1)));
 #pragma unroll
       for (int m = 0; m < KT; ++m)
 #pragma unroll
@@ -594,7 +616,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         st.l.x += __shfl_xor_sync(0xffffffffu, st.l.x, d);
         st.l.y += __shfl_xor_sync(0xffffffffu, st.l.y, d);
       }
-      if (whole) {
+      if (SPANS && whole && at.r.kind != kSpanWhole) {
+        // to be joined with the other part of its rows
+        const PartRows to(a, at.r.kind);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const long long row = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D);
+          if (row < 0) continue;
+          if (g == 0) to.ml[row / D] = make_float2(-(j ? st.minus.y : st.minus.x), j ? st.l.y : st.l.x);
+          float* o = to.o + row + g * LD;
+#pragma unroll
+          for (int m = 0; m < KT; m += 2)
+            *reinterpret_cast<float4*>(o + 2 * m) =
+                make_float4(st.o[m][j], st.o[m][j + 2] * 0x1p-4f, st.o[m + 1][j], st.o[m + 1][j + 2] * 0x1p-4f);
+        }
+      } else if (whole) {
         const float back = kKvUnit * a.v_scale;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -633,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         if (lane == 0)
           info[warp * 2 + slot] =
               PieceInfo{group, at.r.tiles, min(kCols, at.r.q_len * G - at.col * kCols), at.r.row0,
-                        at.head, at.col * kCols, piece};
+                        at.head, at.col * kCols, at.r.kind, piece};
       }
       if (at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi) break;
       at.next_group(a);
@@ -692,6 +728,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
 #pragma unroll
       for (int i = 0; i < VL; i += 2)
         *reinterpret_cast<float2*>(dst + 2 * kCols + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
+    } else if (SPANS && gi.kind != kSpanWhole) {
+      const int G = a.group, token = a.token_of(gi.first_col + c);
+      const PartRows to(a, gi.kind);
+      const size_t row = static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G;
+      if (lane == 0) to.ml[row] = make_float2(m, l);
+#pragma unroll
+      for (int i = 0; i < VL; i += 2)
+        *reinterpret_cast<float2*>(to.o + row * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
@@ -760,14 +804,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   }
 }
 
-template <int D>
+template <int D, bool SPANS>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   constexpr int smem = kWarps * kStages * 2 * kv_block_bytes(D);
   static int limit[kAttrDevices] = {};
-  cudaError_t e = ensure_smem_limit(kv_attend_kernel<D>, smem, limit);
+  cudaError_t e = ensure_smem_limit(kv_attend_kernel<D, SPANS>, smem, limit);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(kKvMaxCtas, a.num_sms * kCtasPerSm);
-  return launch_dependent(kv_attend_kernel<D>, dim3(ctas), kThreads, smem, stream, a);
+  return launch_dependent(kv_attend_kernel<D, SPANS>, dim3(ctas), kThreads, smem, stream, a);
 }
 
 }  // namespace
@@ -777,8 +821,9 @@ size_t kv_attend_workspace_floats(int num_sms, int D) {
   return ctas * 2 * (1 + kWarps) * (D == 128 ? piece_floats<128>() : piece_floats<64>());
 }
 
-cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream) {
-  return a.pages.D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+cudaError_t launch_kv_attend(const KvAttendArgs& a, bool spans, cudaStream_t stream) {
+  if (spans) return a.pages.D == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
+  return a.pages.D == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
 }
 
 }  // namespace lora

@@ -15,15 +15,12 @@
 #include "lora_kv.h"
 #include "kv_decode.cuh"
 #include "kv_kernels.h"
+#include "kv_quant.cuh"
 
 namespace lora {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float e4m3_value(uint8_t b) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-}
 
 // A group of 16 dimensions of one token and head, of K and of V, a thread: twice 32 bytes of
 // values, 8 of codes and one scale.  Threads run along the token's row, so both directions move
@@ -51,74 +48,6 @@ __device__ __forceinline__ Group locate(const KvPages& pg, const int32_t* slots,
   x.k_scale = blk + kv_k_scale_at(pg.D, token, group);
   x.v_scale = blk + kv_v_scale_at(pg.D, token, group);
   return x;
-}
-
-// Codes of 16 values whose quotients by s round to -7 .. 7, y = 1 / s correctly rounded.  The
-// quotient is Markstein's: q = x y is corrected twice by its remainder, x - q s, exact in one
-// fused multiply-add once q is within one unit in the last place, which makes the last result the
-// correctly rounded x / s -- as a division, with one reciprocal for the group.  Adding
-// 1.5 2^23 rounds to an integer, ties to even, and leaves it in the low bits; a shifted add
-// puts it in its nibble, and what the sums carry besides is one constant.
-template <bool IS_V>
-__device__ __forceinline__ uint2 codes_of(const uint32_t (&w)[8], float s, float y) {
-  const float2 y2 = make_float2(y, y), minus_s = make_float2(-s, -s);
-  const float2 magic = make_float2(12582912.f, 12582912.f);
-  uint32_t code[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    code[h] = 0x11111111u * (8u - 0x4B400000u);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = make_float2(bf16_lo(w[4 * h + j]), bf16_hi(w[4 * h + j]));
-      float2 q = mul2(x, y2);
-      q = fma2(fma2(q, minus_s, x), y2, q);
-      q = fma2(fma2(q, minus_s, x), y2, q);
-      q = add2(q, magic);
-      code[h] += __float_as_uint(q.x) << (4 * kv_nibble(IS_V, 2 * j));
-      code[h] += __float_as_uint(q.y) << (4 * kv_nibble(IS_V, 2 * j + 1));
-    }
-  }
-  return make_uint2(code[0], code[1]);
-}
-
-// Writes the group at src, of a cache of scale g.
-template <bool IS_V>
-__device__ __forceinline__ void write_group(const uint4 lo, const uint4 hi, float g, uint8_t* codes,
-                                            uint8_t* scale) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  // the largest magnitude; a NaN if there is one
-  __nv_bfloat162 top2 = __habs2(reinterpret_cast<const __nv_bfloat162&>(w[0]));
-#pragma unroll
-  for (int j = 1; j < 8; ++j)
-    top2 = __hmax2_nan(top2, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[j])));
-  float top = __bfloat162float(__hmax_nan(top2.x, top2.y));
-  const bool nan = top != top;
-  if (nan) {
-    top = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
-  }
-  const uint8_t sb = static_cast<uint8_t>(
-      __nv_cvt_float_to_fp8(__fdiv_rn(top, 7.f * g), __NV_SATFINITE, __NV_E4M3));
-  const float s = e4m3_value(sb) * g;
-  const float y = __frcp_rn(s);
-  uint2 code;
-  // (the range keeps every product and remainder of a quotient from a half up a normal number)
-  if (!nan && s > 0x1p-60f && s < 0x1p60f && top * y < 7.49f) {
-    code = codes_of<IS_V>(w, s, y);
-  } else {  // zeros, saturated scales, the smallest scales, NaN: division and clamp by element
-    code = make_uint2(0u, 0u);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float x = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-      float q = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
-      q = q != q ? 0.f : fminf(fmaxf(q, -7.f), 7.f);
-      (j < 8 ? code.x : code.y) |= static_cast<uint32_t>(static_cast<int>(q) + 8)
-                                   << (4 * kv_nibble(IS_V, j & 7));
-    }
-  }
-  *reinterpret_cast<uint2*>(codes) = code;
-  *scale = sb;
 }
 
 // Bound: for large batches the instructions (about 14 a value, a third of them the quotient)
@@ -258,6 +187,7 @@ namespace {
 // both attention kernels' arrival counts, groups claimed and CTAs done claiming
 constexpr size_t kArrivalsBytes = (2 * kKvMaxCtas + 2) * sizeof(int32_t);
 constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxQueryHeads = 256 * 64;  // cache heads times queries of one
 constexpr int kMaxRequests = 16384;
 // Rows a cache head (query rows times q_heads / kv_heads) up to which a request's attention runs
 // in the kernel for few rows, which costs by 8 rows what the one for many costs by 256.  Measured
@@ -291,6 +221,18 @@ void free_all(lora_kv_cache* c) {
 bool here(const lora_kv_cache* c) {
   int device = -1;
   return cudaGetDevice(&device) == cudaSuccess && device == c->device;
+}
+
+// Whether rows of wa elements lda apart and rows of wb elements ldb apart (bf16, T of both) may share
+// memory: rows of one array whose columns are apart do not.
+bool rows_meet(const void* pa, int lda, int wa, const void* pb, int ldb, int wb, int T) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+  if (a + (static_cast<size_t>(T - 1) * lda + wa) * 2 <= b || b + (static_cast<size_t>(T - 1) * ldb + wb) * 2 <= a)
+    return false;
+  if (lda != ldb) return true;
+  const uintptr_t row = static_cast<uintptr_t>(lda) * 2;
+  const uintptr_t off = b >= a ? (b - a) % row : (row - (a - b) % row) % row;  // b's column in a's rows, bytes
+  return off < static_cast<uintptr_t>(wa) * 2 || off + static_cast<uintptr_t>(wb) * 2 > row;
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -383,10 +325,61 @@ int lora_kv_read(lora_kv_cache_t* c, const int32_t* slots, int T, void* k_out, v
   return LORA_OK;
 }
 
-int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
-                   const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T,
-                   int max_q, float scale, void* out, int ldo, void* stream) {
+int lora_kv_append_rotated(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, void* q_out, int ldqo,
+                           const void* k, int ldk, const void* v, int ldv, const int32_t* position,
+                           const int32_t* slots, int T, const float* angles, int max_position,
+                           int rotary_dim, int interleaved, void* stream) {
   if (!c) return LORA_EINVAL;
+  if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
+  const int D = c->pages.D, width = c->pages.heads * D;
+  if (T < 0 || T > kMaxTokens) return fail(c, LORA_EINVAL, "T=%d", T);
+  if (q_heads < 1 || q_heads > kMaxQueryHeads) return fail(c, LORA_EINVAL, "q_heads=%d", q_heads);
+  if (rotary_dim < 32 || rotary_dim > D || rotary_dim % 32 || max_position < 1)
+    return fail(c, LORA_EINVAL, "rotary_dim=%d: a multiple of 32 up to %d; max_position=%d", rotary_dim, D,
+                max_position);
+  if (ldq < q_heads * D || ldqo < q_heads * D || ldk < width || ldv < width || ldq % 8 || ldqo % 8 ||
+      ldk % 8 || ldv % 8)
+    return fail(c, LORA_EINVAL, "row distances %d, %d, %d, %d: multiples of 8 from %d and %d up", ldq, ldqo, ldk,
+                ldv, q_heads * D, width);
+  if (T == 0) return LORA_OK;
+  if (!q || !q_out || !k || !v || !position || !slots || !angles || !aligned16(q) || !aligned16(q_out) ||
+      !aligned16(k) || !aligned16(v) || !aligned16(angles))
+    return fail(c, LORA_EINVAL, "null argument, or rows or angles not 16-byte aligned");
+  if ((q != q_out || ldq != ldqo) && rows_meet(q, ldq, q_heads * D, q_out, ldqo, q_heads * D, T))
+    return fail(c, LORA_EINVAL, "q and q_out overlap without being the same");
+  if (rows_meet(k, ldk, width, q_out, ldqo, q_heads * D, T) || rows_meet(v, ldv, width, q_out, ldqo, q_heads * D, T))
+    return fail(c, LORA_EINVAL, "k or v and q_out overlap");
+  KvRotateArgs a;
+  a.pages = c->pages;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.ldq = ldq;
+  a.ldqo = ldqo;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.q_heads = q_heads;
+  a.position = position;
+  a.slots = slots;
+  a.T = T;
+  a.angles = reinterpret_cast<const float2*>(angles);
+  a.max_position = max_position;
+  a.rotary = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.err = c->err;
+  KV_CUDA(c, launch_kv_rotate(a, static_cast<cudaStream_t>(stream)));
+  return LORA_OK;
+}
+
+namespace {
+
+// The call of one of the attention entry points, checked; a.T is 0 where there is nothing to do.
+int attend_args(lora_kv_cache* c, KvAttendArgs& a, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
+                const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T, int max_q,
+                float scale, void* out, int ldo) {
   if (!here(c)) return fail(c, LORA_EINVAL, "the cache is on device %d", c->device);
   const int heads = c->pages.heads, D = c->pages.D;
   if (T < 0 || T > kMaxTokens) return fail(c, LORA_EINVAL, "T=%d", T);
@@ -406,6 +399,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   if (ldq < q_heads * D || ldo < q_heads * D || ldq % 8 || ldo % 8)
     return fail(c, LORA_EINVAL, "row distances %d, %d: multiples of 8 from %d up", ldq, ldo,
                 q_heads * D);
+  a.T = T;
   if (T == 0) return LORA_OK;
   if (!q || !q_offsets || !kv_len || !block_table || !out || !aligned16(q) || !aligned16(out))
     return fail(c, LORA_EINVAL, "null argument, or q or out not 16-byte aligned");
@@ -413,7 +407,6 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   const size_t qn = (static_cast<size_t>(T - 1) * ldq + q_heads * D) * 2;
   const size_t on = (static_cast<size_t>(T - 1) * ldo + q_heads * D) * 2;
   if (qb < ob + on && ob < qb + qn) return fail(c, LORA_EINVAL, "q and out overlap");
-  KvAttendArgs a;
   a.pages = c->pages;
   a.q = q;
   a.ldq = ldq;
@@ -423,7 +416,6 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.table = block_table;
   a.max_blocks = max_blocks;
   a.B = B;
-  a.T = T;
   a.max_q = max_q;
   a.group = q_heads / heads;
   a.group_magic = static_cast<uint32_t>((1ull << 32) / a.group + 1);
@@ -440,9 +432,91 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   a.err = c->err;
   a.num_sms = c->num_sms;
   a.many_follow = static_cast<long long>(max_q) * a.group > kFewRows;
-  KV_CUDA(c, launch_kv_attend(a, static_cast<cudaStream_t>(stream)));
-  if (a.many_follow)
-    KV_CUDA(c, launch_kv_prompt(a, static_cast<cudaStream_t>(stream)));
+  a.causal = 1;
+  a.group_offsets = a.prefix_row = a.prefix_len = a.shared = nullptr;
+  a.groups = 0;
+  return LORA_OK;
+}
+
+int launch_attention(lora_kv_cache* c, const KvAttendArgs& a, bool spans, void* stream) {
+  KV_CUDA(c, launch_kv_attend(a, spans, static_cast<cudaStream_t>(stream)));
+  if (a.many_follow) KV_CUDA(c, launch_kv_prompt(a, spans, static_cast<cudaStream_t>(stream)));
+  return LORA_OK;
+}
+
+// Bytes of a row's unnormalised results, of both parts.
+size_t part_bytes(const lora_kv_cache* c, int q_heads) {
+  return static_cast<size_t>(q_heads) * 2 * (c->pages.D + 2) * sizeof(float);
+}
+
+}  // namespace
+
+int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
+                   const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T,
+                   int max_q, float scale, void* out, int ldo, void* stream) {
+  if (!c) return LORA_EINVAL;
+  KvAttendArgs a;
+  const int rc = attend_args(c, a, q, ldq, q_heads, q_offsets, kv_len, block_table, max_blocks, B, T, max_q,
+                             scale, out, ldo);
+  return rc != LORA_OK || a.T == 0 ? rc : launch_attention(c, a, false, stream);
+}
+
+int lora_kv_attend_cross(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
+                         const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T,
+                         int max_q, float scale, void* out, int ldo, void* stream) {
+  if (!c) return LORA_EINVAL;
+  KvAttendArgs a;
+  const int rc = attend_args(c, a, q, ldq, q_heads, q_offsets, kv_len, block_table, max_blocks, B, T, max_q,
+                             scale, out, ldo);
+  if (rc != LORA_OK || a.T == 0) return rc;
+  a.causal = 0;
+  return launch_attention(c, a, true, stream);
+}
+
+int64_t lora_kv_shared_workspace(const lora_kv_cache_t* c, int T, int q_heads) {
+  if (!c || T < 0 || T > kMaxTokens || q_heads < 1 || q_heads > kMaxQueryHeads) return LORA_EINVAL;
+  return static_cast<int64_t>(part_bytes(c, q_heads) * T);
+}
+
+int lora_kv_attend_shared(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
+                          const int32_t* kv_len, const int32_t* block_table, int max_blocks, int B, int T,
+                          int max_q, const int32_t* group_offsets, const int32_t* prefix_row,
+                          const int32_t* prefix_len, int groups, const int32_t* shared_len,
+                          float scale, void* out, int ldo, void* workspace, int64_t workspace_bytes,
+                          void* stream) {
+  if (!c) return LORA_EINVAL;
+  KvAttendArgs a;
+  int rc = attend_args(c, a, q, ldq, q_heads, q_offsets, kv_len, block_table, max_blocks, B, T, max_q, scale, out,
+                       ldo);
+  if (rc != LORA_OK) return rc;
+  if (groups < 1 || groups > B) return fail(c, LORA_EINVAL, "groups=%d of %d requests", groups, B);
+  if (a.T == 0) return LORA_OK;
+  const size_t need = part_bytes(c, q_heads) * T;
+  if (!group_offsets || !prefix_row || !prefix_len || !shared_len || !workspace || !aligned16(workspace) || workspace_bytes < 0 ||
+      static_cast<size_t>(workspace_bytes) < need)
+    return fail(c, LORA_EINVAL, "null argument, or a workspace of less than %zu bytes or not 16-byte aligned", need);
+  const char *wb = static_cast<const char*>(workspace), *ob = static_cast<const char*>(out),
+             *qb = static_cast<const char*>(q);
+  const size_t row = static_cast<size_t>(q_heads) * c->pages.D;
+  if ((wb < ob + ((T - 1) * static_cast<size_t>(ldo) + row) * 2 && ob < wb + need) ||
+      (wb < qb + ((T - 1) * static_cast<size_t>(ldq) + row) * 2 && qb < wb + need))
+    return fail(c, LORA_EINVAL, "the workspace overlaps q or out");
+  a.group_offsets = group_offsets;
+  a.prefix_row = prefix_row;
+  a.prefix_len = prefix_len;
+  a.groups = groups;
+  a.shared = shared_len;
+  float* part = static_cast<float*>(workspace);
+  const size_t rows = static_cast<size_t>(T) * q_heads;
+  for (int i = 0; i < 2; ++i) {
+    a.part_o[i] = part + i * rows * c->pages.D;
+    a.part_ml[i] = reinterpret_cast<float2*>(part + 2 * rows * c->pages.D) + i * rows;
+  }
+  // (a group's rows are many where its requests' are not)
+  a.many_follow = static_cast<long long>(T) * a.group > kFewRows;
+  rc = launch_attention(c, a, true, stream);
+  if (rc != LORA_OK) return rc;
+  KV_CUDA(c, launch_kv_share_join(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;
 }
 

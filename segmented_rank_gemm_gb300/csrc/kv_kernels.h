@@ -109,15 +109,40 @@ struct KvAttendArgs {
   int32_t* prompt_claim;     // groups claimed, CTAs done claiming (zeroed)
   int32_t* err;
   int num_sms;
+  // What the kernels' span variants (kv_span.cuh) read besides.
+  int causal;  // 0: a row sees everything its request has cached
+  const int32_t *group_offsets, *prefix_row, *prefix_len;  // [groups + 1], [groups], [groups] (or null)
+  const int32_t* shared;  // [B] (or null)
+  int groups;
+  // Unnormalised results that are joined afterwards, of every row and head of T: O [D], and the
+  // reference m with the sum l.  [0]: of a request's own positions, [1]: of its group's prefix.
+  float* part_o[2];
+  float2* part_ml[2];
 };
 
 constexpr int kKvMaxCtas = 1024;
 
 // Floats of the partial results' workspace.
 size_t kv_attend_workspace_floats(int num_sms, int D);
-cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream);
+// spans: the variant over kv_span.cuh's spans instead of whole causal requests.
+cudaError_t launch_kv_attend(const KvAttendArgs& a, bool spans, cudaStream_t stream);
 // The kernel for requests of many rows (kv_prompt.cu); it leaves the other rows alone.
 size_t kv_prompt_workspace_floats(int num_sms, int D);
-cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_prompt(const KvAttendArgs& a, bool spans, cudaStream_t stream);
+struct KvRotateArgs {
+  KvPages pages;
+  const void *q, *k, *v;
+  void* q_out;
+  int ldq, ldqo, ldk, ldv, q_heads;
+  const int32_t *position, *slots;
+  int T;
+  const float2* angles;  // [max_position][rotary / 2] (cos, sin)
+  int max_position, rotary, interleaved;
+  float k_scale, v_scale;
+  int32_t* err;
+};
+cudaError_t launch_kv_rotate(const KvRotateArgs& a, cudaStream_t stream);
+// Joins the results of rows with a shared prefix (kv_share.cu).
+cudaError_t launch_kv_share_join(const KvAttendArgs& a, cudaStream_t stream);
 
 }  // namespace lora

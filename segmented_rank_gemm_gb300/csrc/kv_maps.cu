@@ -211,9 +211,10 @@ __global__ void __launch_bounds__(kThreads) kv_maps_kernel(MapsArgs a) {
   }
 }
 
+// shared: positions at the start of a request that are not its own (whole pages), or null.
 __global__ void __launch_bounds__(kThreads)
-    kv_release_kernel(const int32_t* __restrict__ done, int32_t* __restrict__ len, int B,
-                      int page_shift, const int32_t* __restrict__ table, int max_blocks,
+    kv_release_kernel(const int32_t* __restrict__ done, int32_t* __restrict__ len, int32_t* __restrict__ shared,
+                      int B, int page_shift, const int32_t* __restrict__ table, int max_blocks,
                       int32_t* __restrict__ free_pages, int stack_size, int32_t* n_free,
                       int32_t* status) {
   extern __shared__ int32_t first[];  // [B + 1]
@@ -225,11 +226,12 @@ __global__ void __launch_bounds__(kThreads)
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long pages = 0, none = 0;
   int bad = 0;
+  const auto kept = [&](int b) { return shared ? shared[b] >> page_shift : 0; };  // pages that stay
   for (int b = b0; b < b1; ++b) {
     if (!done[b]) continue;
-    const int n = len[b];
-    if (n < 0 || n > cap) bad = 1;
-    else pages += (n + static_cast<long long>(P) - 1) >> page_shift;
+    const int n = len[b], s = shared ? shared[b] : 0;
+    if (n < 0 || n > cap || s < 0 || s > n || (s & (P - 1))) bad = 1;
+    else pages += ((n + static_cast<long long>(P) - 1) >> page_shift) - kept(b);
   }
   const int held = *n_free;
   long long page0 = pages, all, unused;
@@ -241,20 +243,56 @@ __global__ void __launch_bounds__(kThreads)
     for (int b = b0; b < b1; ++b) {
       first[b] = p;
       if (!done[b]) continue;
-      p += (len[b] + P - 1) >> page_shift;
+      p += ((len[b] + P - 1) >> page_shift) - kept(b);
       len[b] = 0;
     }
     if (tid == 0) first[B] = static_cast<int>(all);
     __syncthreads();
     for (int j = tid; j < static_cast<int>(all); j += kThreads) {
       const int b = owner(first, B, j);
-      free_pages[held + j] = table[static_cast<size_t>(b) * max_blocks + (j - first[b])];
+      free_pages[held + j] = table[static_cast<size_t>(b) * max_blocks + kept(b) + (j - first[b])];
+    }
+    if (shared) {
+      __syncthreads();  // shared has been read
+      for (int b = b0; b < b1; ++b)
+        if (done[b]) shared[b] = 0;
     }
   }
   if (tid == 0) {
     if (flags == 0) *n_free = held + static_cast<int>(all);
     *status = flags;
   }
+}
+
+// One CTA, as a fork changes little: its requests are checked, then a warp copies a row at a time.
+__global__ void __launch_bounds__(kThreads)
+    kv_fork_kernel(const int32_t* __restrict__ parent, const int32_t* __restrict__ want, int32_t* len,
+                   int32_t* shared, int B, int page_shift, int32_t* table, int max_blocks, int32_t* status) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const long long cap = static_cast<long long>(max_blocks) << page_shift;
+  int bad = 0;
+  for (int b = tid; b < B; b += kThreads) {
+    const int p = parent[b];
+    if (p < 0) {
+      bad |= p != -1;
+      continue;
+    }
+    bad |= p >= B || len[b] != 0 || (want && want[b] < 0);
+    if (p < B) bad |= parent[p] != -1 || len[p] < 0 || len[p] > cap;
+  }
+  const int flags = __syncthreads_or(bad) ? kBadLength : 0;
+  if (flags == 0) {
+    for (int b = tid >> 5; b < B; b += kThreads / 32) {
+      const int p = parent[b];
+      if (p < 0) continue;
+      const int whole = len[p] >> page_shift;  // (a parent's length does not change here)
+      const int pages = want ? min(want[b] >> page_shift, whole) : whole;
+      for (int j = lane; j < pages; j += 32)
+        table[static_cast<size_t>(b) * max_blocks + j] = table[static_cast<size_t>(p) * max_blocks + j];
+      if (lane == 0) len[b] = shared[b] = pages << page_shift;
+    }
+  }
+  if (tid == 0) *status = flags;
 }
 
 int page_shift_of(int page_size) {
@@ -299,9 +337,11 @@ int lora_kv_maps(const int32_t* len_dev, const int32_t* new_dev, const int32_t* 
              : LORA_ECUDA;
 }
 
-int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_size,
-                    const int32_t* block_table, int max_blocks, int32_t* free_pages,
-                    int stack_size, int32_t* n_free_dev, int32_t* status_dev, void* stream) {
+namespace {
+
+int release(const int32_t* done_dev, int32_t* len_dev, int32_t* shared_dev, int B, int page_size,
+            const int32_t* block_table, int max_blocks, int32_t* free_pages, int stack_size,
+            int32_t* n_free_dev, int32_t* status_dev, void* stream) {
   if (!table_ok(B, page_size, max_blocks, stack_size)) return LORA_EINVAL;
   if (!done_dev || !len_dev || !block_table || !free_pages || !n_free_dev || !status_dev)
     return LORA_EINVAL;
@@ -310,8 +350,36 @@ int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_s
   if (smem > 40 * 1024 && ensure_smem_limit(kv_release_kernel, smem, limit) != cudaSuccess)
     return LORA_ECUDA;
   kv_release_kernel<<<1, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(
-      done_dev, len_dev, B, page_shift_of(page_size), block_table, max_blocks, free_pages, stack_size,
+      done_dev, len_dev, shared_dev, B, page_shift_of(page_size), block_table, max_blocks, free_pages, stack_size,
       n_free_dev, status_dev);
+  return cudaGetLastError() == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+}  // namespace
+
+int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_size,
+                    const int32_t* block_table, int max_blocks, int32_t* free_pages,
+                    int stack_size, int32_t* n_free_dev, int32_t* status_dev, void* stream) {
+  return release(done_dev, len_dev, nullptr, B, page_size, block_table, max_blocks, free_pages, stack_size,
+                 n_free_dev, status_dev, stream);
+}
+
+int lora_kv_release_shared(const int32_t* done_dev, int32_t* len_dev, int32_t* shared_dev, int B,
+                           int page_size, const int32_t* block_table, int max_blocks,
+                           int32_t* free_pages, int stack_size, int32_t* n_free_dev,
+                           int32_t* status_dev, void* stream) {
+  if (!shared_dev) return LORA_EINVAL;
+  return release(done_dev, len_dev, shared_dev, B, page_size, block_table, max_blocks, free_pages, stack_size,
+                 n_free_dev, status_dev, stream);
+}
+
+int lora_kv_fork(const int32_t* parent_dev, const int32_t* want_dev, int32_t* len_dev,
+                 int32_t* shared_dev, int B, int page_size, int32_t* block_table, int max_blocks,
+                 int32_t* status_dev, void* stream) {
+  if (!table_ok(B, page_size, max_blocks, 1)) return LORA_EINVAL;
+  if (!parent_dev || !len_dev || !shared_dev || !block_table || !status_dev) return LORA_EINVAL;
+  kv_fork_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      parent_dev, want_dev, len_dev, shared_dev, B, page_shift_of(page_size), block_table, max_blocks, status_dev);
   return cudaGetLastError() == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
 

@@ -47,6 +47,7 @@
 
 #include "kv_decode.cuh"
 #include "kv_kernels.h"
+#include "kv_span.cuh"
 #include "lora_common.cuh"
 #include "lora_kernels.h"
 
@@ -131,14 +132,26 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 }
 
 // ---- requests, groups and the sequence of tiles ----
+// The tiles start at position `first`, and limits count from there: token t sees see + slope t (a
+// whole causal request: 0, kv - q_len and 1).
 struct Request {
   int row0, q_len, kv, rows, parts;  // rows of one head, groups of a head
+  int first, see, slope, table_row;
+  SpanKind kind;
 };
 
 // Request b; one that is not for this kernel has 0 rows.  (Bad ones are reported by the other
 // kernel, which runs on every call.)
+template <bool SPANS>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b) {
   Request r;
+  if constexpr (SPANS) {
+    const Span s = load_span(a, b, false);
+    r = Request{s.row0, s.q_len, s.kv, s.q_len * a.group, 0, s.first, s.see, s.slope, s.table_row, s.kind};
+    if (r.rows <= a.few_rows) r.rows = 0;
+    r.parts = (r.rows + kRows - 1) / kRows;
+    return r;
+  }
   r.row0 = __ldg(a.q_offsets + b);
   const int end = __ldg(a.q_offsets + b + 1);
   // (in this order: the difference of any two offsets need not be an int)
@@ -149,11 +162,16 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b) {
   r.rows = r.q_len * a.group;
   if (r.rows <= a.few_rows) r.rows = 0;
   r.parts = (r.rows + kRows - 1) / kRows;
+  r.first = 0;
+  r.see = r.kv - r.q_len;
+  r.slope = 1;
+  r.table_row = b;
+  r.kind = kSpanWhole;
   return r;
 }
 // Tiles of a request's group `part`: up to the last position its last row sees.
 __device__ __forceinline__ int group_tiles(const KvAttendArgs& a, const Request& r, int part) {
-  const int last = r.kv - r.q_len + a.token_of(min((part + 1) * kRows, r.rows) - 1);
+  const int last = r.see + r.slope * a.token_of(min((part + 1) * kRows, r.rows) - 1);
   return max(1, (last + kTile) / kTile);
 }
 // Units of one head of a request, and of the first parts of it, by the lanes of a warp.
@@ -176,9 +194,9 @@ __device__ __forceinline__ long long head_units(const KvAttendArgs& a, const Req
 __device__ __forceinline__ int first_part(const KvAttendArgs& a, const Request& r, int tiles) {
   if (tiles <= 1) return 0;
   // its last row's token sees position kTile (tiles - 1)
-  const long long token = static_cast<long long>(kTile) * (tiles - 1) - (r.kv - r.q_len);
+  const long long token = static_cast<long long>(kTile) * (tiles - 1) - r.see;
   if (token <= 0) return 0;
-  if (token >= r.q_len) return r.parts;
+  if (token >= r.q_len || r.slope == 0) return r.parts;
   return static_cast<int>(token) * a.group / kRows;
 }
 // Groups are dealt whole in kBuckets classes of size, the largest first: the least tiles of class i
@@ -194,6 +212,7 @@ __device__ __forceinline__ int2 bucket_parts(const KvAttendArgs& a, const Reques
 }
 
 // A position in the sequence of tiles, and the tile's unit.
+template <bool SPANS>
 struct Cursor {
   Request r;
   int b, head, part, tile, tiles;
@@ -203,7 +222,7 @@ struct Cursor {
   __device__ __forceinline__ void start(const KvAttendArgs& a, int b_, long long rem, long long at,
                                         int snap, int lane) {
     b = b_;
-    r = load_request(a, b);
+    r = load_request<SPANS>(a, b);
     const long long per = head_units(a, r, lane);
     head = static_cast<int>(quotient(rem, per));
     rem -= head * per;
@@ -244,7 +263,7 @@ struct Cursor {
         head = 0;
         do {
           ++b;
-          r = load_request(a, b);
+          r = load_request<SPANS>(a, b);
         } while (r.parts == 0);
       }
     }
@@ -254,8 +273,9 @@ struct Cursor {
 
 // A CTA's range of the sequence, walked a segment (one group's tiles tile .. tile + count - 1) at a
 // time.
+template <bool SPANS>
 struct Walk {
-  Cursor at;
+  Cursor<SPANS> at;
   long long end;
   int count;
   __device__ __forceinline__ bool first(const KvAttendArgs& a) {
@@ -282,8 +302,9 @@ struct Segment {
   int rows;       // of the group, at most 256
   int first_row;  // its first row in the request
   int row0;       // the request's first row in q and out
-  int see;        // token t of the request sees positions 0 .. see + t
+  int see, slope;  // token t of the request sees positions 0 .. see + slope t, from its first on
   int head;
+  SpanKind kind;
   long long unit;  // of the group's first tile
 };
 
@@ -321,7 +342,7 @@ struct Barriers {
   uint64_t meet, idle[3];                              // (256) (commit)
 };
 
-template <int D>
+template <int D, bool SPANS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) {
   using L = Smem<D>;
   extern __shared__ uint8_t raw[];
@@ -361,12 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
 
   // The sequence's length and this CTA's cuts.  A thread sums a run of consecutive requests; those
   // with many groups are summed by its warp.
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const int count_b = SPANS ? a.B + a.groups : a.B;
+  const int per = (count_b + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, count_b), b1 = min(b0 + per, count_b);
   int most = 0;  // tiles of the largest group
   const auto request_units = [&](int b, bool mine) {  // of request b (mine), by all lanes
     Request r = {};
-    if (mine) r = load_request(a, b);
+    if (mine) r = load_request<SPANS>(a, b);
     if (r.parts) most = max(most, group_tiles(a, r, r.parts - 1));
     long long n = 0;
     if (r.parts <= 4)
@@ -374,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     for (unsigned big = __ballot_sync(0xffffffffu, r.parts > 4); big; big &= big - 1) {
       const int k = __ffs(big) - 1;
       Request x;
-      x.kv = __shfl_sync(0xffffffffu, r.kv, k);
-      x.q_len = __shfl_sync(0xffffffffu, r.q_len, k);
+      x.see = __shfl_sync(0xffffffffu, r.see, k);
+      x.slope = SPANS ? __shfl_sync(0xffffffffu, r.slope, k) : 1;
       x.rows = __shfl_sync(0xffffffffu, r.rows, k);
       x.parts = __shfl_sync(0xffffffffu, r.parts, k);
       const long long sum = head_units(a, x, lane);
@@ -415,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     for (int i = 0; i < kBuckets; ++i) {
       int n = 0;
       for (int b = b0; b < b1; ++b) {
-        const int2 parts = bucket_parts(a, load_request(a, b), most, i);
+        const int2 parts = bucket_parts(a, load_request<SPANS>(a, b), most, i);
         n += (parts.y - parts.x) * heads;
       }
       n = __reduce_add_sync(0xffffffffu, n);
@@ -487,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (active) {
         // the last position this row sees, from the segment's first tile on (a row past the
         // last is written nowhere)
-        const int lim = g.see + a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) - g.tile * kTile;
+        const int lim = g.see + (SPANS ? g.slope : 1) * a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) -
+                        g.tile * kTile;
         uint32_t at = (step + half) % 3;  // S's place
         for (int j = 0; j < g.count; ++j, ++n) {
           uint32_t pv_there = 1;  // the product before has been seen to be done
@@ -576,25 +599,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
                            static_cast<size_t>(blockIdx.x * 2 + (g.tile > 0 ? 0 : 1)) * piece_floats<D>();
       if (active) {
         // 128 bytes of every row at a time, from one row a lane to 8 lanes a row
-        const float f = whole ? (l == 0.f ? 0.f : kKvUnit * a.v_scale / l) : 1.f;
+        // (raw: fp32 as it is, to a piece or to be joined with the other part of its rows)
+        const bool part = SPANS && whole && g.kind != kSpanWhole, raw = !whole || part;
+        const float f = raw ? 1.f : l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
         const float2 by = make_float2(f, f), none = make_float2(0.f, 0.f);
         const auto at = [&](int x, int k) {  // 16-byte piece k of row x
           return reinterpret_cast<uint4*>(scratch + x * 128 + ((k ^ (x & 7)) << 4));
         };
         // where they go: from the group's first token (or row of the piece) on, in bytes
         const int first_token = a.token_of(g.first_row);
+        const PartRows to(a, g.kind);
+        const size_t first_row = static_cast<size_t>(g.row0 + first_token) * a.q_heads + g.head * G;  // of the parts
         uint8_t* const base =
-            whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                               static_cast<size_t>(g.row0 + first_token) * a.ldo + g.head * G * D)
-                  : reinterpret_cast<uint8_t*>(piece + 2 * kRows);
+            part     ? reinterpret_cast<uint8_t*>(to.o + first_row * D)
+            : whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                 static_cast<size_t>(g.row0 + first_token) * a.ldo + g.head * G * D)
+                    : reinterpret_cast<uint8_t*>(piece + 2 * kRows);
         const int x0 = half * 128 + (warp & 3) * 32;
         const bool all = x0 + 32 <= g.rows;
         uint8_t* dst[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t x = x0 + i * 4 + (lane >> 3), c = g.first_row + x, token = a.token_of(c);
-          const uint32_t row_bytes = whole ? static_cast<uint32_t>(a.ldo) * 2 : 0;
-          const uint32_t in_row = whole ? (c - token * G) * (D * 2) : x * (D * 4);
+          const uint32_t row_bytes = part ? a.q_heads * (D * 4u) : whole ? static_cast<uint32_t>(a.ldo) * 2 : 0;
+          const uint32_t in_row = whole ? (c - token * G) * (part ? D * 4 : D * 2) : x * (D * 4);
           dst[i] = base + static_cast<uint64_t>(token - first_token) * row_bytes + in_row + (lane & 7) * 16;
         }
         const auto put = [&](const uint32_t (&o)[32], int off) {  // 32 words of this lane's row
@@ -621,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           tmem_ld_32x32b_x32(o_at + d, o[0]);
           tmem_ld_32x32b_x32(o_at + d + 32, o[1]);
           tmem_ld_wait();
-          if (whole) {
+          if (!raw) {
             uint32_t x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -640,6 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
         if (!whole) {
           piece[half * 128 + row] = m;
           piece[kRows + half * 128 + row] = l;
+        }
+        if (part && half * 128 + row < g.rows) {
+          const int c = g.first_row + half * 128 + row, token = a.token_of(c);
+          to.ml[first_row + static_cast<size_t>(token - first_token) * a.q_heads + c - token * G] = make_float2(m, l);
         }
       }
       if (!whole) {
@@ -671,7 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
 #pragma unroll 4
             for (int i = 0; i < pieces; ++i)
               sum += ex2(__ldcg(piece_of(i) + tid) - top) * __ldcg(piece_of(i) + kRows + tid);
-            row_join[tid] = make_float2(top, sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum);
+            const bool part = SPANS && g.kind != kSpanWhole;
+            row_join[tid] = make_float2(top, part ? 1.f : sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum);
+            if (part) {
+              const int c = g.first_row + tid, token = a.token_of(c);
+              PartRows(a, g.kind).ml[static_cast<size_t>(g.row0 + token) * a.q_heads + g.head * G + c - token * G] =
+                  make_float2(top, sum);
+            }
           }
           meet_all();
           if (!ok) break;
@@ -707,6 +745,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
               if (x >= g.rows) break;
               const float f = row_join[x].y;
               const int c = g.first_row + x, token = a.token_of(c);
+              if (SPANS && g.kind != kSpanWhole) {
+                float2* to = reinterpret_cast<float2*>(
+                    PartRows(a, g.kind).o +
+                    (static_cast<size_t>(g.row0 + token) * a.q_heads + g.head * G + c - token * G) * D);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d) to[d * 32 + lane] = make_float2(o[k][2 * d], o[k][2 * d + 1]);
+                continue;
+              }
               uint32_t* out = reinterpret_cast<uint32_t*>(
                   static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(g.row0 + token) * a.ldo +
                   (g.head * G + c - token * G) * D);
@@ -968,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     const int step = min(kTile, 1 << shift);          // positions of a copy
     const bool copies = lane * kKvBlock < kTile && lane * kKvBlock % step == 0;
     const uint32_t bytes = step / kKvBlock * kv_block_bytes(D);
-    Walk walk;
+    Walk<SPANS> walk;
     bool some = false;
     // Whole groups: a lane's two counts of a warp's requests in a class, classes first, and the
     // groups up to them.
@@ -996,19 +1042,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (rem >= c0) rem -= c0, ++entry;
       const int bucket = entry / (kThreads / 32), first = entry % (kThreads / 32) * 32;
       // the thread of that warp whose requests have it, then the request
-      const int x0 = min((first + lane) * per, a.B), x1 = min(x0 + per, a.B);
+      const int x0 = min((first + lane) * per, count_b), x1 = min(x0 + per, count_b);
       int n = 0;
       for (int b = x0; b < x1; ++b) {
-        const int2 parts = bucket_parts(a, load_request(a, b), most, bucket);
+        const int2 parts = bucket_parts(a, load_request<SPANS>(a, b), most, bucket);
         n += (parts.y - parts.x) * heads;
       }
       const int incl = scan_lanes(n);
       k = __ffs(__ballot_sync(0xffffffffu, rem < incl)) - 1;
       rem -= __shfl_sync(0xffffffffu, incl - n, k);
-      Cursor& c = walk.at;
+      Cursor<SPANS>& c = walk.at;
       int2 parts;
       for (c.b = (first + k) * per;; ++c.b) {
-        c.r = load_request(a, c.b);
+        c.r = load_request<SPANS>(a, c.b);
         parts = bucket_parts(a, c.r, most, bucket);
         n = (parts.y - parts.x) * heads;
         if (rem < n) break;
@@ -1039,11 +1085,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       ok = mbar_wait(&bar.seg_empty[place], (seg / kSegments & 1) ^ 1, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const Cursor& c = walk.at;
+      const Cursor<SPANS>& c = walk.at;
       const int rows = some ? min(kRows, c.r.rows - c.part * kRows) : 0;
       if (lane == 0) {
         segments[place] = some ? Segment{walk.count, c.tile, c.tiles, rows, c.part * kRows, c.r.row0,
-                                         c.r.kv - c.r.q_len, c.head, c.unit - c.tile}
+                                         c.r.see, c.r.slope, c.head, c.r.kind, c.unit - c.tile}
                                : Segment{};
         mbar_arrive(&bar.seg_full[place]);
       }
@@ -1057,12 +1103,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
                                static_cast<size_t>(c.r.row0 + token) * a.ldq + c.head * G * D,
                            G * D * 2);
       }
-      const int32_t* const pages = a.table + static_cast<size_t>(c.b) * a.max_blocks;
+      const int32_t* const pages = a.table + static_cast<size_t>(c.r.table_row) * a.max_blocks;
       const int last = max(0, (c.r.kv - 1) >> shift);  // the request's last page
       // the page of a tile's position (of the last page past the end: masked, and within the cache)
       const auto page_of = [&](int j) {
-        const int pos = (c.tile + j) * kTile + lane * kKvBlock;
-        return copies && c.r.kv > 0 ? __ldg(pages + min(pos >> shift, last)) : 0;
+        const int pos = c.r.first + (c.tile + j) * kTile + lane * kKvBlock;
+        return copies && c.r.kv > c.r.first ? __ldg(pages + min(pos >> shift, last)) : 0;
       };
       int id = page_of(0);
       for (int j = 0; j < walk.count; ++j, ++n) {
@@ -1116,12 +1162,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   griddep_wait();
 }
 
-template <int D>
+template <int D, bool SPANS>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   static int limit[kAttrDevices] = {};
-  cudaError_t e = ensure_smem_limit(kv_prompt_kernel<D>, Smem<D>::kBytes, limit);
+  cudaError_t e = ensure_smem_limit(kv_prompt_kernel<D, SPANS>, Smem<D>::kBytes, limit);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kv_prompt_kernel<D>, dim3(std::min(kKvMaxCtas, a.num_sms)), kThreads,
+  return launch_dependent(kv_prompt_kernel<D, SPANS>, dim3(std::min(kKvMaxCtas, a.num_sms)), kThreads,
                           Smem<D>::kBytes, stream, a);
 }
 
@@ -1132,8 +1178,9 @@ size_t kv_prompt_workspace_floats(int num_sms, int D) {
          (D == 128 ? piece_floats<128>() : piece_floats<64>());
 }
 
-cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream) {
-  return a.pages.D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+cudaError_t launch_kv_prompt(const KvAttendArgs& a, bool spans, cudaStream_t stream) {
+  if (spans) return a.pages.D == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
+  return a.pages.D == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
 }
 
 }  // namespace lora

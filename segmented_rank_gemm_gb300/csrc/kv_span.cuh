@@ -1,0 +1,84 @@
+// kv_span.cuh -- what the attention kernels' span variants run over (include/lora_kv.h:
+// lora_kv_attend_shared, lora_kv_attend_cross).
+//
+// A span is a run of consecutive query rows and a run of cached positions from a page's start on.  A
+// call's spans are its groups' prefixes (the rows of all members, which see all of it) and then its
+// requests (their rows, over what lies behind the prefix).  Where a request has no prefix, its span
+// gives its output; else the two spans' results meet in kv_share.cu, by the rule for a softmax
+// over two sets of positions: with p = 2^(s - m), o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv_decode.cuh"
+#include "kv_kernels.h"
+#include "lora_kernels.h"
+
+namespace lora {
+
+enum SpanKind { kSpanWhole = 0, kSpanTail = 1, kSpanPrefix = 2 };
+
+struct Span {
+  int row0, q_len;  // its rows; one with bad offsets has none
+  int first, kv;    // positions first .. kv - 1, of the request in row `table_row` of the table
+  int see, slope;   // its token t sees positions first .. first + see + slope t
+  int table_row;
+  SpanKind kind;
+};
+
+// Span v of a call's groups + B, checked.
+__device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool report) {
+  Span s;
+  const int cap = a.max_blocks << a.pages.page_shift, in_page = (1 << a.pages.page_shift) - 1;
+  bool bad;
+  if (v < a.groups) {
+    int from = load_in_order(a.group_offsets + v), to = load_in_order(a.group_offsets + v + 1);
+    bad = from < 0 || to < from || to > a.B;
+    s.table_row = load_in_order(a.prefix_row + v);
+    s.kv = load_in_order(a.prefix_len + v);
+    bad = bad || s.table_row < 0 || s.table_row >= a.B || s.kv < 0 || s.kv > cap || (s.kv & in_page);
+    if (bad) from = to = 0;
+    s.row0 = load_in_order(a.q_offsets + from);
+    const int end = load_in_order(a.q_offsets + to);
+    bad = bad || s.row0 < 0 || end < s.row0 || end > a.T;
+    s.q_len = bad || s.kv == 0 ? 0 : end - s.row0;
+    if (bad) s.kv = s.table_row = 0;
+    s.first = 0;
+    s.see = s.kv - 1;
+    s.slope = 0;
+    s.kind = kSpanPrefix;
+  } else {
+    const int b = v - a.groups;
+    s.row0 = load_in_order(a.q_offsets + b);
+    const int end = load_in_order(a.q_offsets + b + 1);
+    s.kv = load_in_order(a.kv_len + b);
+    const int share = a.groups ? load_in_order(a.shared + b) : 0;
+    // (in this order: the difference of any two offsets need not be an int)
+    bad = s.row0 < 0 || end < s.row0 || end > a.T || end - s.row0 > a.max_q;
+    s.q_len = bad ? 0 : end - s.row0;
+    if (s.kv < 0 || s.kv > cap) {
+      bad = true;
+      s.kv = min(max(s.kv, 0), cap);
+    }
+    // every row of a request sees all of its group's prefix, whose pages are whole
+    bad = bad || (s.q_len > 0 && (share < 0 || (share & in_page) || share > max(0, s.kv - s.q_len)));
+    s.first = min(max(share, 0), s.kv) & ~in_page;
+    s.see = (a.causal ? s.kv - s.q_len : s.kv - 1) - s.first;
+    s.slope = a.causal ? 1 : 0;
+    s.table_row = b;
+    s.kind = s.first > 0 ? kSpanTail : kSpanWhole;
+  }
+  if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
+  return s;
+}
+
+// Where a span's unnormalised results go: row r's head h at index r q_heads + h.
+struct PartRows {
+  float* o;    // [.][D]
+  float2* ml;  // m, l
+  __device__ __forceinline__ PartRows(const KvAttendArgs& a, SpanKind kind)
+      : o(a.part_o[kind == kSpanPrefix]), ml(a.part_ml[kind == kSpanPrefix]) {}
+};
+
+}  // namespace lora

@@ -1,5 +1,5 @@
-"""ctypes binding of the paged 4-bit key/value cache, the attention over it and a batch's block
-tables and slot maps (``include/lora_kv.h``).
+"""ctypes binding of the paged 4-bit key/value cache, the rotation and the attentions over it and a
+batch's block tables and slot maps (``include/lora_kv.h``).
 
 The functions carry the C names; they check what the C entry points cannot see (types, devices,
 sizes and strides of the tensors) and raise ``LoraError`` with LORA_EINVAL, so that no
@@ -79,6 +79,57 @@ def lora_kv_release(done, lens, page_size, block_table, free_pages, n_free, stat
     _check(rc, "lora_kv_release")
 
 
+def lora_kv_release_shared(done, lens, shared, page_size, block_table, free_pages, n_free, status,
+                           stream=None) -> None:
+    """``lora_kv_release`` of requests whose first ``shared[b]`` positions are another's
+    (``lora_kv_release_shared``)."""
+    B, dev = lens.shape[0], torch.cuda.current_device()
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        _bad("block_table must be [B, max_blocks]")
+    rc = _lib.lora_kv_release_shared(
+        _i32("done", done, B, dev), _i32("lens", lens, B, dev), _i32("shared", shared, B, dev), B,
+        page_size, _i32("block_table", block_table, 1, dev), block_table.shape[1],
+        _i32("free_pages", free_pages, 1, dev), free_pages.shape[0], _i32("n_free", n_free, 1, dev),
+        _i32("status", status, 1, dev), _stream(stream, dev))
+    _check(rc, "lora_kv_release_shared")
+
+
+def lora_kv_fork(parent, want, lens, shared, page_size, block_table, status, stream=None) -> None:
+    """Requests that start with the whole pages of ``parent[b]`` (-1: unchanged), up to ``want[b]``
+    positions if given (``lora_kv_fork``)."""
+    B, dev = lens.shape[0], torch.cuda.current_device()
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        _bad("block_table must be [B, max_blocks]")
+    rc = _lib.lora_kv_fork(
+        _i32("parent", parent, B, dev), None if want is None else _i32("want", want, B, dev),
+        _i32("lens", lens, B, dev), _i32("shared", shared, B, dev), B, page_size,
+        _i32("block_table", block_table, 1, dev), block_table.shape[1],
+        _i32("status", status, 1, dev), _stream(stream, dev))
+    _check(rc, "lora_kv_fork")
+
+
+class Rotary:
+    """The angles of a rotation of queries and keys by position, for ``KvCache.append_rotated``:
+    ``angles`` [max_position, rotary_dim / 2, 2] fp32, the cosine and sine, computed in 64 bits, of
+    p * frequency[i].  The first ``rotary_dim`` dimensions of a head are turned, a multiple of 32:
+    pair i is dimensions i and i + rotary_dim / 2, or 2 i and 2 i + 1 if ``interleaved``.
+    ``frequencies`` [rotary_dim / 2] default to theta ** (-2 i / rotary_dim)."""
+
+    def __init__(self, max_position: int, rotary_dim: int, theta: float = 10000.0,
+                 interleaved: bool = False, frequencies=None, device="cuda"):
+        if max_position < 1 or rotary_dim < 32 or rotary_dim % 32:
+            raise ValueError("max_position must be positive, rotary_dim a multiple of 32")
+        if frequencies is None:
+            i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+            frequencies = theta ** (-2 * i / rotary_dim)
+        elif tuple(frequencies.shape) != (rotary_dim // 2,):
+            raise ValueError("frequencies must be [rotary_dim / 2]")
+        angle = torch.outer(torch.arange(max_position, dtype=torch.float64, device=device),
+                            frequencies.to(device=device, dtype=torch.float64))
+        self.angles = torch.stack((angle.cos(), angle.sin()), -1).float()
+        self.max_position, self.rotary_dim, self.interleaved = max_position, rotary_dim, interleaved
+
+
 class PageTable:
     """The pages of up to ``max_requests`` requests and the maps of their current batch.
 
@@ -102,7 +153,8 @@ class PageTable:
         self.kv_len, self.q_offsets = zeros(max_requests), zeros(max_requests + 1)
         self.position, self.kv_slot = zeros(max_tokens), zeros(max_tokens)
         self.token_slot = zeros(max_tokens)
-        self._status = zeros(1)
+        self.shared_len = zeros(max_requests)  # positions that are another request's pages
+        self._status, self._fork_status = zeros(1), zeros(1)
 
     def step(self, new, adapter=None, stream=None) -> None:
         """``new`` [max_requests] int32 (CUDA): tokens each request adds, 0 for idle ones;
@@ -111,10 +163,22 @@ class PageTable:
                      self.free_pages, self.n_free, self.kv_len, self.q_offsets, self.position,
                      self.kv_slot, self.token_slot, self.counts, stream)
 
+    def fork(self, parent, want=None, stream=None) -> None:
+        """Request b starts with the whole pages of request ``parent[b]`` (-1: unchanged), up to
+        ``want[b]`` positions if given; it must be empty.  ``shared_len`` then says how many
+        positions that are.  The parent has to outlive it: it goes on holding the pages."""
+        lora_kv_fork(parent, want, self.kv_len, self.shared_len, self.page_size, self.block_table,
+                     self._fork_status, stream)
+
+    def fork_status(self) -> int:
+        """Error flags of the last fork (which then changed nothing).  Synchronises."""
+        return int(self._fork_status)
+
     def release(self, done, stream=None) -> None:
-        """The pages of requests with ``done[b] != 0`` are free again, their length 0."""
-        lora_kv_release(done, self.kv_len, self.page_size, self.block_table, self.free_pages,
-                        self.n_free, self._status, stream)
+        """The pages of requests with ``done[b] != 0`` (but for those that are another's) are free
+        again, their length 0."""
+        lora_kv_release_shared(done, self.kv_len, self.shared_len, self.page_size,
+                               self.block_table, self.free_pages, self.n_free, self._status, stream)
 
     def status(self):
         """(new tokens of the batch, free pages, pages taken, error flags of the last step and
@@ -150,6 +214,26 @@ class KvCache:
         self._check(_lib.lora_kv_append(self.handle, k.data_ptr(), ldk, v.data_ptr(), ldv,
                                         _i32("kv_slot", kv_slot, T, dev), T, _stream(stream, dev)))
 
+    def append_rotated(self, q, k, v, position, kv_slot, rotary: Rotary, q_out=None, stream=None):
+        """``append`` with q [T, q_heads, head_dim] and k turned by ``position`` [T] first
+        (``rotary``: a ``Rotary``).  The turned queries go to ``q_out`` (which may be q; a new
+        tensor if not given), which is returned; k itself stays as it is."""
+        T, q_heads, dev = q.shape[0], q.shape[1], torch.cuda.current_device()
+        shape, q_shape = (T, self.kv_heads, self.head_dim), (T, q_heads, self.head_dim)
+        ldq, ldk, ldv = _rows("q", q, q_shape, dev), _rows("k", k, shape, dev), _rows("v", v, shape, dev)
+        angles = rotary.angles
+        if angles.dtype is not torch.float32 or angles.get_device() != dev or not angles.is_contiguous() \
+                or angles.shape != (rotary.max_position, rotary.rotary_dim // 2, 2):
+            _bad("the angles must be fp32 [max_position, rotary_dim / 2, 2] on the current CUDA device")
+        position, kv_slot = _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev)
+        if q_out is None:
+            q_out = empty(q_shape, _BF16, q.device, stream)
+        self._check(_lib.lora_kv_append_rotated(
+            self.handle, q.data_ptr(), ldq, q_heads, q_out.data_ptr(), _rows("q_out", q_out, q_shape, dev),
+            k.data_ptr(), ldk, v.data_ptr(), ldv, position, kv_slot, T, angles.data_ptr(),
+            rotary.max_position, rotary.rotary_dim, rotary.interleaved, _stream(stream, dev)))
+        return q_out
+
     def read(self, kv_slot, k_out=None, v_out=None, stream=None):
         """The values held in ``kv_slot`` [T], as bf16 [T, kv_heads, head_dim]."""
         T, dev = kv_slot.shape[0], torch.cuda.current_device()
@@ -166,10 +250,8 @@ class KvCache:
                                       k_out.data_ptr(), v_out.data_ptr(), _stream(stream, dev)))
         return k_out, v_out
 
-    def attend(self, q, q_offsets, kv_len, block_table, max_q: int, scale: float = None, out=None,
-               stream=None):
-        """softmax(scale q K^T) V for q [T, q_heads, head_dim] (bf16; rows may be apart).
-        ``scale`` is head_dim ** -0.5 by default; ``max_q`` bounds a request's query rows."""
+    def _attend(self, call, q, q_offsets, kv_len, block_table, max_q, scale, out, stream, more=()):
+        """One of the attention entry points; ``more`` are its arguments behind max_q."""
         T, q_heads = q.shape[0], q.shape[1]
         B, dev = kv_len.shape[0], torch.cuda.current_device()
         shape = (T, q_heads, self.head_dim)
@@ -179,12 +261,51 @@ class KvCache:
             _bad("block_table must be [B, max_blocks]")
         if scale is None:
             scale = self.head_dim ** -0.5
-        self._check(_lib.lora_kv_attend(
+        before, behind = more if more else ((), ())
+        self._check(call(
             self.handle, q.data_ptr(), _rows("q", q, shape, dev), q_heads,
             _i32("q_offsets", q_offsets, B + 1, dev), _i32("kv_len", kv_len, B, dev),
-            _i32("block_table", block_table, 1, dev), block_table.shape[1], B, T, max_q, scale,
-            out.data_ptr(), _rows("out", out, shape, dev), _stream(stream, dev)))
+            _i32("block_table", block_table, 1, dev), block_table.shape[1], B, T, max_q, *before, scale,
+            out.data_ptr(), _rows("out", out, shape, dev), *behind, _stream(stream, dev)))
         return out
+
+    def attend(self, q, q_offsets, kv_len, block_table, max_q: int, scale: float = None, out=None,
+               stream=None, causal: bool = True):
+        """softmax(scale q K^T) V for q [T, q_heads, head_dim] (bf16; rows may be apart).
+        ``scale`` is head_dim ** -0.5 by default; ``max_q`` bounds a request's query rows.
+        Without ``causal`` every row sees all that its request has cached, an encoder's states say
+        (``lora_kv_attend_cross``)."""
+        return self._attend(_lib.lora_kv_attend if causal else _lib.lora_kv_attend_cross, q, q_offsets,
+                            kv_len, block_table, max_q, scale, out, stream)
+
+    def shared_workspace(self, tokens: int, q_heads: int):
+        """What ``attend_shared`` needs for ``tokens`` rows, to be kept from call to call (calls
+        that may run at the same time need one each)."""
+        n = _lib.lora_kv_shared_workspace(self.handle, tokens, q_heads)
+        if n < 0:
+            _bad("tokens=%d, q_heads=%d" % (tokens, q_heads))
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def attend_shared(self, q, q_offsets, kv_len, block_table, max_q: int, group_offsets, prefix_row,
+                      prefix_len, shared_len, scale: float = None, out=None, workspace=None,
+                      stream=None):
+        """``attend`` for requests that share prefixes by groups, each prefix read once for all of
+        its group (``lora_kv_attend_shared``): group g is requests ``group_offsets[g]`` ..
+        ``group_offsets[g + 1] - 1``; the first ``shared_len[b]`` positions of a member are
+        ``prefix_len[g]`` (whole pages, those in row ``prefix_row[g]`` of the table), or 0: it is
+        attended by itself."""
+        B, dev, groups = kv_len.shape[0], torch.cuda.current_device(), group_offsets.shape[0] - 1
+        group_at = _i32("group_offsets", group_offsets, 2, dev)
+        prefix_at = _i32("prefix_row", prefix_row, groups, dev), _i32("prefix_len", prefix_len, groups, dev)
+        shared_at = _i32("shared_len", shared_len, B, dev)
+        if workspace is None:
+            n = _lib.lora_kv_shared_workspace(self.handle, q.shape[0], q.shape[1])
+            workspace = empty((max(n, 0),), torch.uint8, q.device, stream)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _bad("workspace must be a contiguous tensor on the current CUDA device")
+        return self._attend(_lib.lora_kv_attend_shared, q, q_offsets, kv_len, block_table, max_q, scale,
+                            out, stream, ((group_at, *prefix_at, groups, shared_at),
+                                          (workspace.data_ptr(), workspace.numel() * workspace.element_size())))
 
     def status(self, stream=None) -> int:
         """LORA_OK, LORA_EID or LORA_ETIMEOUT since the last call (synchronises)."""

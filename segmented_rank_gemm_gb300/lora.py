@@ -43,7 +43,9 @@ LAYER_FUNCTIONS = ("lora_layer_create", "lora_layer_create_pooled", "lora_layer_
 # every entry point declared in include/lora_kv.h
 KV_FUNCTIONS = ("lora_kv_maps", "lora_kv_release", "lora_kv_cache_create", "lora_kv_append",
                 "lora_kv_read", "lora_kv_attend", "lora_kv_get_status", "lora_kv_cache_bytes",
-                "lora_kv_wait_selftest", "lora_kv_last_error", "lora_kv_cache_destroy")
+                "lora_kv_wait_selftest", "lora_kv_last_error", "lora_kv_cache_destroy",
+                "lora_kv_fork", "lora_kv_release_shared", "lora_kv_append_rotated",
+                "lora_kv_attend_cross", "lora_kv_attend_shared", "lora_kv_shared_workspace")
 # every entry point declared in include/lora_norm.h
 NORM_FUNCTIONS = ("lora_rms_norm",)
 ABI_FUNCTIONS = LAYER_FUNCTIONS + KV_FUNCTIONS + NORM_FUNCTIONS
@@ -134,6 +136,15 @@ def _load() -> ctypes.CDLL:
     L.lora_kv_read.argtypes = [vp, vp, i32, vp, vp, vp]
     L.lora_kv_attend.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, f32, vp, i32,
                                  vp]
+    L.lora_kv_fork.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, vp, vp]
+    L.lora_kv_release_shared.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp]
+    L.lora_kv_append_rotated.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp,
+                                         i32, i32, i32, vp]
+    L.lora_kv_attend_cross.argtypes = L.lora_kv_attend.argtypes
+    L.lora_kv_attend_shared.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32,
+                                        vp, f32, vp, i32, vp, i64, vp]
+    L.lora_kv_shared_workspace.argtypes = [vp, i32, i32]
+    L.lora_kv_shared_workspace.restype = i64
     L.lora_kv_get_status.argtypes = [vp, vp]
     L.lora_kv_wait_selftest.argtypes = [vp, vp]
     L.lora_kv_cache_bytes.argtypes = [vp]
@@ -144,7 +155,8 @@ def _load() -> ctypes.CDLL:
     L.lora_kv_cache_destroy.restype = None
     for name in ("lora_kv_maps", "lora_kv_release", "lora_kv_cache_create", "lora_kv_append",
                  "lora_kv_read", "lora_kv_attend", "lora_kv_get_status",
-                 "lora_kv_wait_selftest"):
+                 "lora_kv_wait_selftest", "lora_kv_fork", "lora_kv_release_shared",
+                 "lora_kv_append_rotated", "lora_kv_attend_cross", "lora_kv_attend_shared"):
         getattr(L, name).restype = i32
     L.lora_rms_norm.argtypes = [vp, i32, vp, i32, vp, f32, i32, i32, i32, vp, i32, vp, vp, vp, vp]
     L.lora_rms_norm.restype = i32
