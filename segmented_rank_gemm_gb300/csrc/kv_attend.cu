@@ -636,6 +636,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         for (int j = 0; j < 2; ++j) {
           const long long off = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.ldo);
           if (off < 0) continue;
+          if (SPANS && a.groups && g == 0)
+            a.part_ml[0][column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D) / D] = kv_row_done();
           const float l = j ? st.l.y : st.l.x;
           const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
@@ -738,6 +740,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         *reinterpret_cast<float2*>(to.o + row * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
+      if (SPANS && a.groups && lane == 0)
+        a.part_ml[0][static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G] =
+            kv_row_done();
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
       uint32_t* out = reinterpret_cast<uint32_t*>(
           static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(gi.row0 + token) * a.ldo +

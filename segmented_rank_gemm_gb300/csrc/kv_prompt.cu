@@ -63,10 +63,13 @@ constexpr int kRaw = 3;         // packed tiles
 // cycles measured), and units that the pieces of a group cut in two cost (13000 each).
 constexpr int kSetup = 6;
 constexpr int kPieces = 15;
+// The same where pieces are joined by a kernel of their own (kv_share.cu), rows of all groups at once,
+// and cost what writing them does.
+constexpr int kPiecesLater = 2;
 // A cut this near to a group's edge moves there: a group cut in two costs its CTAs about as much as
 // this many tiles, as long as that is little of a range.
-__device__ __forceinline__ int snap_of(long long span) {
-  return static_cast<int>(min(max(span / 12, 8ll), min(span / 4, 1ll << 20)));
+__device__ __forceinline__ int snap_of(long long span, bool later) {
+  return static_cast<int>(later ? min(span / 4, 2ll) : min(max(span / 12, 8ll), min(span / 4, 1ll << 20)));
 }
 constexpr float kRef = 6.f;     // P is 2^kRef at the reference
 constexpr float kSlack = 8.f;   // how far (in powers of two) a score may exceed the reference
@@ -311,8 +314,9 @@ struct Segment {
 // Floats of a piece: m, l [256], O [256][D].
 template <int D>
 constexpr int piece_floats() {
-  return kRows * (D + 2);
+  return kv_prompt_piece_floats(D);
 }
+static_assert(kRows == kKvPromptRows, "the rows of a piece");
 
 constexpr int kScratchWarp = 4096;  // a softmax warp's 32 rows of 128 bytes, on their way out
 template <int D>
@@ -428,10 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     most = max(most, warp_most[w]);
   }
   const long long span = max(static_cast<long long>(kSetup + 4), quotient(total + gridDim.x - 1, gridDim.x));
-  const int snap = snap_of(span);
+  const bool later = SPANS && a.groups > 0;  // pieces of rows in two parts are joined with those
+  const int snap = snap_of(span, later);
   // Whole groups, claimed one by one, unless the largest would outlast the rest by more than its
   // cutting costs.
-  const bool whole = most + kSetup <= span + kPieces;
+  const bool whole = most + kSetup <= span + (later ? kPiecesLater : kPieces);
   if (whole) {
 #pragma unroll 1
     for (int i = 0; i < kBuckets; ++i) {
@@ -669,12 +674,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           piece[half * 128 + row] = m;
           piece[kRows + half * 128 + row] = l;
         }
-        if (part && half * 128 + row < g.rows) {
+        // (a group that is cut names its pieces for each of its rows, in the CTA with the first one)
+        if (SPANS && a.groups && (whole || g.tile == 0) && half * 128 + row < g.rows) {
           const int c = g.first_row + half * 128 + row, token = a.token_of(c);
-          to.ml[first_row + static_cast<size_t>(token - first_token) * a.q_heads + c - token * G] = make_float2(m, l);
+          const int first_cut = whole ? 0 : static_cast<int>(quotient(g.unit + snap, span)) + 1;
+          const int last_cut = whole ? 0 : static_cast<int>(quotient(g.unit + g.tiles - snap + span - 1, span)) - 1;
+          to.ml[first_row + static_cast<size_t>(token - first_token) * a.q_heads + c - token * G] =
+              g.kind == kSpanWhole ? kv_row_done()
+              : whole              ? make_float2(m, l)
+                                   : KvPieces(first_cut, last_cut - first_cut + 2, half * 128 + row).packed();
         }
       }
-      if (!whole) {
+      if (!whole && (!SPANS || g.kind == kSpanWhole)) {
         // The cuts within the group, as their CTAs see them, and the pieces between them: the
         // first cut's CTA before it (piece 1), then pieces 0.
         const int first_cut = static_cast<int>(quotient(g.unit + snap, span)) + 1;
@@ -693,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
         if (last_cta) {
           const auto piece_of = [&](int i) {
             return a.prompt_pieces +
-                   static_cast<size_t>(i == 0 ? (first_cut - 1) * 2 + 1 : (first_cut + i - 1) * 2) * piece_floats<D>();
+                   static_cast<size_t>(kv_prompt_piece(first_cut, i)) * piece_floats<D>();
           };
           // a row's maximum and the factor of its sum first, one row a thread
           if (tid < g.rows) {
@@ -703,13 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
 #pragma unroll 4
             for (int i = 0; i < pieces; ++i)
               sum += ex2(__ldcg(piece_of(i) + tid) - top) * __ldcg(piece_of(i) + kRows + tid);
-            const bool part = SPANS && g.kind != kSpanWhole;
-            row_join[tid] = make_float2(top, part ? 1.f : sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum);
-            if (part) {
-              const int c = g.first_row + tid, token = a.token_of(c);
-              PartRows(a, g.kind).ml[static_cast<size_t>(g.row0 + token) * a.q_heads + g.head * G + c - token * G] =
-                  make_float2(top, sum);
-            }
+            row_join[tid] = make_float2(top, sum == 0.f ? 0.f : kKvUnit * a.v_scale / sum);
           }
           meet_all();
           if (!ok) break;
@@ -745,14 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
               if (x >= g.rows) break;
               const float f = row_join[x].y;
               const int c = g.first_row + x, token = a.token_of(c);
-              if (SPANS && g.kind != kSpanWhole) {
-                float2* to = reinterpret_cast<float2*>(
-                    PartRows(a, g.kind).o +
-                    (static_cast<size_t>(g.row0 + token) * a.q_heads + g.head * G + c - token * G) * D);
-#pragma unroll
-                for (int d = 0; d < D / 64; ++d) to[d * 32 + lane] = make_float2(o[k][2 * d], o[k][2 * d + 1]);
-                continue;
-              }
               uint32_t* out = reinterpret_cast<uint32_t*>(
                   static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(g.row0 + token) * a.ldo +
                   (g.head * G + c - token * G) * D);

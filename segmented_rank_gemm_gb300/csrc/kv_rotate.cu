@@ -164,12 +164,15 @@ template <int D, bool APART>
 __global__ void __launch_bounds__(kThreads) kv_rotate_kernel(KvRotateArgs a, unsigned kv_blocks) {
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x < kv_blocks)
-    write_pair<D, APART, false>(a, blockIdx.x * kThreads + threadIdx.x);
-  else if (blockIdx.x < 2 * kv_blocks)
-    write_pair<D, APART, true>(a, (blockIdx.x - kv_blocks) * kThreads + threadIdx.x);
+  // the blocks of keys and values evenly among those of queries: how many of the former come before
+  const unsigned long long n = 2 * kv_blocks;
+  const unsigned before = static_cast<unsigned>(blockIdx.x * n / gridDim.x);
+  if ((blockIdx.x + 1) * n / gridDim.x == before)
+    turn_queries<D, APART>(a, (blockIdx.x - before) * kThreads + threadIdx.x);
+  else if (before & 1)
+    write_pair<D, APART, true>(a, (before >> 1) * kThreads + threadIdx.x);
   else
-    turn_queries<D, APART>(a, (blockIdx.x - 2 * kv_blocks) * kThreads + threadIdx.x);
+    write_pair<D, APART, false>(a, (before >> 1) * kThreads + threadIdx.x);
 }
 
 template <int D, bool APART>

@@ -2,8 +2,11 @@
 // lora_kv_attend_shared): o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the row's two
 // results, M the larger of m_0 and m_1, in fp32, rounded once.
 //
+// A result that the kernel for many rows has in pieces (a group cut between CTAs) is joined here as
+// well, by the same rule, with all rows of the batch at once.
+//
 // Bound: bytes (D fp32 twice in, D bf16 out of a row and head, mostly from L2) and, for a decode
-// batch, the launch.  A warp takes kHeads heads of one row, whose loads are all under way together.
+// batch, the launch and one trip to L2.  A warp takes a head of one row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -19,20 +22,71 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;
 
-// The last of offsets[0 .. n) that is <= x (which offsets[0] is): the lanes of a warp cut the
-// range in 32.
-__device__ __forceinline__ int last_not_above(const int32_t* offsets, int n, int x, int lane) {
-  int lo = 0, len = n;  // the answer is in [lo, lo + len)
-  while (len > 1) {
-    const int step = (len + 31) / 32, at = lo + lane * step;
-    const bool below = lane * step < len && load_in_order(offsets + at) <= x;
-    const int k = max(0, 31 - __clz(__ballot_sync(0xffffffffu, below)));
-    len = min(step, len - k * step);
-    lo += k * step;
+template <int VL>
+__device__ __forceinline__ void load_o(const float* src, float (&o)[VL]) {
+#pragma unroll
+  for (int k = 0; k < VL; k += 2) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(src + k));
+    o[k] = x.x;
+    o[k + 1] = x.y;
   }
-  return lo;
+}
+
+// Joins a row's pieces: their common reference m, the sum l, and this lane's dimensions of O.
+template <int D>
+__device__ __forceinline__ float2 join_pieces(const KvAttendArgs& a, KvPieces p, int lane, float (&o)[D / 32]) {
+  constexpr int VL = D / 32, kPiece = kv_prompt_piece_floats(D);
+  // (counts out of range are those of a call that was flagged: nothing wrote them)
+  const int n = p.first_cut >= 1 && p.first_cut + p.count <= min(kKvMaxCtas, a.num_sms) + 1 && p.row < kKvPromptRows
+                    ? p.count
+                    : 0;
+  const auto piece = [&](int k) {
+    return a.prompt_pieces + static_cast<size_t>(kv_prompt_piece(p.first_cut, k)) * kPiece + p.row;
+  };
+  float m = -1.7e38f, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < VL; ++i) o[i] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const bool mine = k0 + lane < n;
+    const float mk = mine ? __ldcg(piece(k0 + lane)) : -1.7e38f;
+    const float lk = mine ? __ldcg(piece(k0 + lane) + kKvPromptRows) : 0.f;
+    float top = fmaxf(m, mk);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float back = ex2(m - top), f = ex2(mk - top);
+    m = top;
+    float sum = f * lk;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * back + sum;
+#pragma unroll
+    for (int i = 0; i < VL; ++i) o[i] *= back;
+    const int some = min(32, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < some; ++k) {
+      float x[VL];
+      load_o<VL>(piece(k0 + k) + 2 * kKvPromptRows + p.row * (D - 1) + lane * VL, x);
+      const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+      for (int i = 0; i < VL; ++i) o[i] += w * x[i];
+    }
+  }
+  return make_float2(m, l);
+}
+
+// The groups agree with their requests: one with a prefix is a member, and has its group's.
+__device__ void check_request(const KvAttendArgs& a, int b) {
+  const Span s = load_span(a, a.groups + b, false);
+  if (s.q_len == 0 || s.kind == kSpanWhole) return;
+  int lo = 0, hi = a.groups;  // the last group that starts at b or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.group_offsets[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  if (b < a.group_offsets[lo] || b >= a.group_offsets[lo + 1] || a.shared[b] != a.prefix_len[lo])
+    atomicOr(a.err, LORA_ERRF_BAD_ID);
 }
 
 template <int D>
@@ -40,65 +94,36 @@ __global__ void __launch_bounds__(kThreads) kv_share_join_kernel(KvAttendArgs a,
   griddep_wait();
   const int lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) >= row_blocks) {
-    // The groups agree with their requests: one with a prefix is a member, and has its group's.
     const int b = (blockIdx.x - row_blocks) * kThreads + threadIdx.x;
-    if (b >= a.B) return;
-    const Span s = load_span(a, a.groups + b, false);
-    if (s.q_len > 0 && s.kind != kSpanWhole) {
-      int lo = 0, hi = a.groups;  // the last group that starts at b or before
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.group_offsets[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      if (b < a.group_offsets[lo] || b >= a.group_offsets[lo + 1] || a.shared[b] != a.prefix_len[lo])
-        atomicOr(a.err, LORA_ERRF_BAD_ID);
-    }
+    if (b < a.B) check_request(a, b);
     return;
   }
-  const int chunks = (a.q_heads + kHeads - 1) / kHeads;
-  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int row = static_cast<int>(item / chunks), head0 = static_cast<int>(item % chunks) * kHeads;
-  if (row >= a.T || row < load_in_order(a.q_offsets) || row >= load_in_order(a.q_offsets + a.B)) return;
-  const int b = last_not_above(a.q_offsets, a.B, row, lane);
-  if (load_span(a, a.groups + b, false).kind == kSpanWhole) return;
+  const long long at = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int row = static_cast<int>(at / a.q_heads), head = static_cast<int>(at - static_cast<long long>(row) * a.q_heads);
+  if (row >= a.T) return;
+  // all that a row in two whole parts needs, asked for at once
   constexpr int VL = D / 32;
-  float2 ml[kHeads][2];
-  float o[kHeads][2][VL];
+  const int lo = load_in_order(a.q_offsets), hi = load_in_order(a.q_offsets + a.B);
+  float2 ml0 = __ldcg(a.part_ml[0] + at), ml1 = __ldcg(a.part_ml[1] + at);
+  float o0[VL], o1[VL];
+  load_o<VL>(a.part_o[0] + at * D + lane * VL, o0);
+  load_o<VL>(a.part_o[1] + at * D + lane * VL, o1);
+  if (row < lo || row >= hi || kv_is_row_done(ml0)) return;
+  if (KvPieces::are(ml0)) ml0 = join_pieces<D>(a, KvPieces(ml0), lane, o0);
+  if (KvPieces::are(ml1)) ml1 = join_pieces<D>(a, KvPieces(ml1), lane, o1);
+  const float m = fmaxf(ml0.x, ml1.x), w0 = ex2(ml0.x - m), w1 = ex2(ml1.x - m);
+  const float l = w0 * ml0.y + w1 * ml1.y;
+  const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l, f0 = w0 * f, f1 = w1 * f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(row) * a.ldo +
+                                              head * D + lane * VL);
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    const size_t at = static_cast<size_t>(row) * a.q_heads + min(head0 + h, a.q_heads - 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ml[h][i] = __ldcs(a.part_ml[i] + at);
-      const float2* src = reinterpret_cast<const float2*>(a.part_o[i] + at * D + lane * VL);
-#pragma unroll
-      for (int k = 0; k < VL / 2; ++k) {
-        const float2 x = __ldcs(src + k);
-        o[h][i][2 * k] = x.x;
-        o[h][i][2 * k + 1] = x.y;
-      }
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    if (head0 + h >= a.q_heads) break;
-    const float m = fmaxf(ml[h][0].x, ml[h][1].x);
-    const float w0 = ex2(ml[h][0].x - m), w1 = ex2(ml[h][1].x - m);
-    const float l = w0 * ml[h][0].y + w1 * ml[h][1].y;
-    const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l, f0 = w0 * f, f1 = w1 * f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                static_cast<size_t>(row) * a.ldo + (head0 + h) * D + lane * VL);
-#pragma unroll
-    for (int k = 0; k < VL / 2; ++k)
-      out[k] = pack_bf16x2(f0 * o[h][0][2 * k] + f1 * o[h][1][2 * k],
-                           f0 * o[h][0][2 * k + 1] + f1 * o[h][1][2 * k + 1]);
-  }
+  for (int k = 0; k < VL / 2; ++k)
+    out[k] = pack_bf16x2(f0 * o0[2 * k] + f1 * o1[2 * k], f0 * o0[2 * k + 1] + f1 * o1[2 * k + 1]);
 }
 
 template <int D>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
-  const long long items = static_cast<long long>(a.T) * ((a.q_heads + kHeads - 1) / kHeads);
+  const long long items = static_cast<long long>(a.T) * a.q_heads;
   const int row_blocks = static_cast<int>((items + kThreads / 32 - 1) / (kThreads / 32));
   return launch_dependent(kv_share_join_kernel<D>, dim3(row_blocks + (a.B + kThreads - 1) / kThreads), kThreads,
                           0, stream, a, row_blocks);

@@ -73,6 +73,32 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
   return s;
 }
 
+// Pieces of the kernel for many rows (kv_prompt.cu): m [256], l [256], O [256][D]; a CTA has two, and
+// the i-th of a group that is first cut in front of CTA first_cut is this one.
+constexpr int kKvPromptRows = 256;
+__host__ __device__ constexpr int kv_prompt_piece_floats(int D) { return kKvPromptRows * (D + 2); }
+__host__ __device__ constexpr int kv_prompt_piece(int first_cut, int i) {
+  return i == 0 ? (first_cut - 1) * 2 + 1 : (first_cut + i - 1) * 2;
+}
+// In the place of a row's (m, l): its group's result is `count` pieces, where it is row `row`.
+struct KvPieces {
+  int first_cut, count, row;
+  __device__ __forceinline__ KvPieces(int first_cut_, int count_, int row_)
+      : first_cut(first_cut_), count(count_), row(row_) {}
+  __device__ __forceinline__ explicit KvPieces(float2 ml) {
+    const uint32_t v = __float_as_uint(ml.x);
+    first_cut = v >> 21, count = v >> 10 & 0x7FF, row = v & 0x3FF;
+  }
+  static __device__ __forceinline__ bool are(float2 ml) { return ml.y == -1.f; }  // (a sum is not negative)
+  __device__ __forceinline__ float2 packed() const {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(first_cut) << 21 | count << 10 | row), -1.f);
+  }
+};
+// In the place of a request's (m, l): its row has no second part and is written already.
+__device__ __forceinline__ float2 kv_row_done() { return make_float2(0.f, -2.f); }
+__device__ __forceinline__ bool kv_is_row_done(float2 ml) { return ml.y == -2.f; }
+static_assert(kKvMaxCtas < 1 << 11 && kKvPromptRows <= 1 << 10, "what KvPieces holds");
+
 // Where a span's unnormalised results go: row r's head h at index r q_heads + h.
 struct PartRows {
   float* o;    // [.][D]
