@@ -226,6 +226,39 @@ int lora_forward_e4m3(lora_layer_t* layer, const void* x_dev, const void* xq_dev
                       const float* sx_dev, void* y_dev, int T, void* stream);
 
 /*
+ * What lora_forward_fused does with a row's sum v = x W + low-rank term before it is rounded:
+ *     y = act(v + bias) * factor + residual        in fp32, rounded to bf16 once.
+ * A null bias, factor or residual is left out; LORA_ACT_NONE leaves v as it is.
+ *   bias            [N] bf16.
+ *   factor, residual  T rows of N bf16, ldf and ldr elements apart (multiples of 8 from N up).  Each
+ *                   may be y itself (the same address and ld = N), and else does not overlap it.
+ * All 16-byte aligned.  GELU is x (1 + erf(x / sqrt 2)) / 2, GELU_TANH its approximation
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2, SILU x / (1 + e^-x).
+ */
+enum lora_activation { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3,
+                       LORA_ACT_SILU = 4 };
+typedef struct lora_epilogue {
+    const void* bias;
+    int activation;
+    const void* factor;
+    int ldf;
+    const void* residual;
+    int ldr;
+} lora_epilogue_t;
+
+/*
+ * lora_forward (or, with xq and sx, lora_forward_e4m3) for a bf16 layer or one with an e4m3 base, with
+ * the epilogue above: a decoder's gate projection times its up projection, or a projection onto the
+ * running residual, without a pass over y of its own.  *epilogue is read during the call; what it
+ * points to is read on the GPU, and comes from earlier work on `stream`.  No host synchronisation,
+ * no allocation; can be captured in a CUDA graph.
+ * Errors: as those calls; LORA_EINVAL for an fp32 layer, a null epilogue, or one not as above.
+ */
+int lora_forward_fused(lora_layer_t* layer, const void* x_dev, const void* xq_dev,
+                       const float* sx_dev, void* y_dev, int T, const lora_epilogue_t* epilogue,
+                       void* stream);
+
+/*
  * The whole layer for callers holding host buffers: copies x_host [T,K] and
  * token_slot_host [T] to layer-owned device staging, runs set_batch_segments and
  * lora_forward, and copies y back to y_host [T,N].  All on `stream`, asynchronously:

@@ -1,7 +1,9 @@
-"""The attention half of a decoder block with an adapter a request, over a 4-bit cache.
+"""The two halves of a decoder block with an adapter a request, the first over a 4-bit cache.
 
     h += x;  n = norm(h) w;  q, k, v = P_q(n), P_k(n), P_v(n);  k, v into the cache
     y = P_o(softmax(scale q K^T) V)
+
+    h += y;  n = norm(h) w;  z = P_down(act(P_gate(n)) * P_up(n))
 
 Every projection is a mixed-adapter layer (``lora.LoraLayer``); ``PageTable.step`` gives the
 batch's rows their adapter slots, positions and cache slots, so that the requests' lengths and
@@ -13,8 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from .kv import KvCache, PageTable
-from .lora import LoraLayer, empty, on_stream
+from .kv import KvCache, PageTable, Rotary
+from .lora import ACTIVATIONS, LoraLayer, empty, on_stream
 from .norm import lora_rms_norm
 
 
@@ -23,11 +25,14 @@ class AttentionBlock:
     hidden -> kv_heads head_dim (k and v) and q_heads head_dim -> hidden, in bf16; q, k and v
     all with an e4m3 base, or none of them.  ``norm_weight`` [hidden] is bf16.
 
-    ``rotate(q, k, position)``, if given, turns q [T, q_heads, D] and k [T, kv_heads, D] in
-    place before the keys are cached; its torch operations run on the pass's stream."""
+    ``rotary``, if given, turns queries and keys by their positions on the way into the cache.
+    ``rotate(q, k, position)``, if given instead, turns q [T, q_heads, D] and k [T, kv_heads, D] in
+    place before the keys are cached; its torch operations run on the pass's stream.  ``share``:
+    passes may be given groups of requests that share prefixes."""
 
     def __init__(self, q: LoraLayer, k: LoraLayer, v: LoraLayer, o: LoraLayer,
-                 norm_weight: torch.Tensor, cache: KvCache, eps: float = 1e-6, rotate=None):
+                 norm_weight: torch.Tensor, cache: KvCache, eps: float = 1e-6, rotate=None,
+                 rotary: Rotary = None, share: bool = False):
         D = cache.head_dim
         if q.N % (cache.kv_heads * D) or q.N > 64 * cache.kv_heads * D \
                 or k.N != cache.kv_heads * D or v.N != k.N or o.K != q.N:
@@ -38,8 +43,11 @@ class AttentionBlock:
             raise ValueError("the projections must be bf16 layers")
         if not q.K == k.K == v.K or len({layer.fp8_base for layer in (q, k, v)}) != 1:
             raise ValueError("q, k and v must take the same rows")
+        if rotary is not None and (rotate is not None or rotary.rotary_dim > D):
+            raise ValueError("rotate or a rotary of at most the head's dimensions")
         self.q, self.k, self.v, self.o = q, k, v, o
         self.norm_weight, self.cache, self.eps, self.rotate = norm_weight, cache, eps, rotate
+        self.rotary = rotary
         self.max_tokens = min(layer.max_tokens for layer in (q, k, v, o))
 
         def rows(width, dtype=torch.bfloat16):
@@ -50,11 +58,14 @@ class AttentionBlock:
         self.qr, self.kr, self.vr = rows(q.N), rows(k.N), rows(v.N)
         self.nq = rows(q.K, torch.float8_e4m3fn) if q.fp8_base else None
         self.sn = rows(1, torch.float32).view(-1) if q.fp8_base else None
+        self.parts = cache.shared_workspace(self.max_tokens, q.N // D) if share else None
 
     def forward(self, x: torch.Tensor, h: torch.Tensor, pages: PageTable, max_q: int, y=None,
-                stream=None) -> torch.Tensor:
+                stream=None, groups=None) -> torch.Tensor:
         """x and the running residual ``h`` [T, hidden] (overwritten by h + x) of the batch that
-        ``pages.step`` mapped last; ``max_q`` bounds a request's new tokens.  Returns y."""
+        ``pages.step`` mapped last; ``max_q`` bounds a request's new tokens.  Returns y.
+        ``groups``: (group_offsets, prefix_row, prefix_len) of ``KvCache.attend_shared``, whose
+        members' prefixes are ``pages.shared_len``."""
         T = x.shape[0]
         # (whatever can be refused is, before h and the cache change; x and h by the norm)
         if T > min(self.max_tokens, pages.token_slot.shape[0]):
@@ -63,6 +74,8 @@ class AttentionBlock:
             raise ValueError("the page table does not fit the cache")
         if max_q < 1:
             raise ValueError("max_q must be positive")
+        if groups is not None and self.parts is None:
+            raise ValueError("groups need a block made with share")
         if y is None:
             y = empty(x.shape, x.dtype, x.device, stream)
         elif y.dtype != torch.bfloat16 or y.shape != (T, self.o.N) or not y.is_cuda \
@@ -82,11 +95,75 @@ class AttentionBlock:
         D = self.cache.head_dim
         q, k, v, ctx = (r[:T].view(T, r.shape[1] // D, D)
                         for r in (self.qr, self.kr, self.vr, self.ctx))
-        if self.rotate is not None:
-            with on_stream(stream):
-                self.rotate(q, k, pages.position[:T])
-        self.cache.append(k, v, pages.kv_slot[:T], stream)
-        self.cache.attend(q, pages.q_offsets, pages.kv_len, pages.block_table, max_q, out=ctx,
-                          stream=stream)
+        if self.rotary is not None:
+            self.cache.append_rotated(q, k, v, pages.position[:T], pages.kv_slot[:T], self.rotary,
+                                      q_out=q, stream=stream)
+        else:
+            if self.rotate is not None:
+                with on_stream(stream):
+                    self.rotate(q, k, pages.position[:T])
+            self.cache.append(k, v, pages.kv_slot[:T], stream)
+        batch = (q, pages.q_offsets, pages.kv_len, pages.block_table, max_q)
+        if groups is None:
+            self.cache.attend(*batch, out=ctx, stream=stream)
+        else:
+            self.cache.attend_shared(*batch, *groups, pages.shared_len, out=ctx,
+                                     workspace=self.parts, stream=stream)
         self.o.set_batch(ids, stream)
         return self.o.forward(self.ctx[:T], y, stream)
+
+
+class MlpBlock:
+    """``gate``, ``up`` and ``down`` are LoraLayers: hidden -> width (gate and up) and width ->
+    hidden, in bf16; gate and up both with an e4m3 base, or neither.  ``norm_weight`` [hidden] is
+    bf16; ``activation`` one of ``lora.ACTIVATIONS``.
+
+    The gate's product ends in act(.) times the up projection's rows, and, in a pass with
+    ``residual``, the down projection's in the sum with h: three products and a norm, no other
+    pass over the rows."""
+
+    def __init__(self, gate: LoraLayer, up: LoraLayer, down: LoraLayer, norm_weight: torch.Tensor,
+                 activation: str = "silu", eps: float = 1e-6):
+        if not (gate.K == up.K == down.N and gate.N == up.N == down.K):
+            raise ValueError("gate and up must give the rows that down takes, down rows like theirs")
+        if any(layer.dtype != torch.bfloat16 for layer in (gate, up, down)):
+            raise ValueError("the projections must be bf16 layers")
+        if gate.fp8_base != up.fp8_base:
+            raise ValueError("gate and up must take the same rows")
+        if activation not in ACTIVATIONS:
+            raise ValueError("activation must be one of %s" % sorted(filter(None, ACTIVATIONS)))
+        self.gate, self.up, self.down = gate, up, down
+        self.norm_weight, self.activation, self.eps = norm_weight, activation, eps
+        self.max_tokens = min(layer.max_tokens for layer in (gate, up, down))
+
+        def rows(width, dtype=torch.bfloat16):
+            return torch.empty(self.max_tokens, width, dtype=dtype, device=norm_weight.device)
+
+        # the batch's intermediate rows; kept, so that a captured graph owns no others
+        self.n, self.mid = rows(gate.K), rows(gate.N)
+        self.nq = rows(gate.K, torch.float8_e4m3fn) if gate.fp8_base else None
+        self.sn = rows(1, torch.float32).view(-1) if gate.fp8_base else None
+
+    def forward(self, x: torch.Tensor, h: torch.Tensor, token_slot: torch.Tensor, y=None,
+                residual: bool = False, stream=None) -> torch.Tensor:
+        """x and the running residual ``h`` [T, hidden] (overwritten by h + x), and the rows' adapter
+        slots.  Returns y, or h + y with ``residual`` (y may then be h)."""
+        T = x.shape[0]
+        if T > self.max_tokens or token_slot.shape[0] < T:
+            raise ValueError("more rows than max_tokens or than adapter slots")
+        if y is None:
+            y = empty(x.shape, x.dtype, x.device, stream)
+        elif y.dtype != torch.bfloat16 or y.shape != (T, self.down.N) or not y.is_cuda \
+                or not y.is_contiguous():
+            raise ValueError("y must be a dense CUDA bf16 tensor of x's shape")
+        n, mid, nq, sn = self.n[:T], self.mid[:T], None, None
+        if self.nq is not None:
+            nq, sn = self.nq[:T], self.sn[:T]
+        lora_rms_norm(x, self.norm_weight, self.eps, h, h, n, nq, sn, stream)
+        ids = token_slot[:T]
+        for layer in (self.up, self.gate, self.down):
+            layer.set_batch(ids, stream)
+        self.up.forward_fused(n, mid, xq=nq, sx=sn, stream=stream)
+        self.gate.forward_fused(n, mid, activation=self.activation, factor=mid, xq=nq, sx=sn,
+                                stream=stream)
+        return self.down.forward_fused(mid, y, residual=h if residual else None, stream=stream)

@@ -202,6 +202,17 @@ struct ExpandArgs {
   const int32_t* row_base;  // [S] first pool row of each slot
   const int32_t* rank;  // [S]
 };
+// What is done with a row's sum before it is rounded (include/lora_layer.h: lora_epilogue_t):
+// y = act(sum + bias) * factor + residual, in fp32.
+struct GemmEpilogue {
+  bool on = false;
+  const void* bias = nullptr;  // [N] bf16
+  int act = 0;                 // lora_activation
+  const void* factor = nullptr;  // [M] rows of N bf16, ldf elements apart
+  int ldf = 0;
+  const void* residual = nullptr;
+  int ldr = 0;
+};
 struct GemmArgs {
   int M, N, K;
   const void* x;  // [M,K]
@@ -237,6 +248,7 @@ struct GemmArgs {
   // delta mode (required there): the map of the delta buffer (encode_tmap_delta), through
   // which the epilogue's delta tile arrives by TMA
   const CUtensorMap* tmap_delta = nullptr;
+  GemmEpilogue ep;
 };
 // tcgen05 / TMEM / TMA kernel (gemm_tc.cu).  tmap_w3 holds the layer's cached maps of the
 // packed weight for N tiles of 256, 128 and 64 rows (in that order); tmap_bx3 the maps of
@@ -281,6 +293,8 @@ GemmPlan gemm_tc_plan(int M, int N, int K, int num_sms, bool allow_split, int sl
                       bool allow_pair = true);
 // Floats of split-K exchange scratch the tcgen05 GEMM needs for an M-row batch with the
 // K split allowed (0 when its plan does not split K).
+// CTAs resident at once in clusters of csize.
+int gemm_tc_resident_ctas(int csize, int num_sms);
 size_t gemm_tc_exchange_floats(int M, int N, int K, int num_sms);
 // The same for a given plan.
 size_t gemm_tc_plan_exchange_floats(const GemmPlan& p, int M, int N);

@@ -562,10 +562,17 @@ static int run_builder(lora_layer_t* L, cudaStream_t stream) {
   return LORA_OK;
 }
 
-// One forward of the current batch.  xq and sx: the caller's e4m3 rows of x with their scales
+// Whether rows of N bf16, ld elements apart, lie on y's memory other than as y itself.
+static bool rows_clash(const lora_layer_t* L, const void* rows, int ld, const void* y, int T) {
+  const char *a = static_cast<const char*>(rows), *b = static_cast<const char*>(y);
+  if (!a || (a == b && ld == L->N)) return false;
+  return a < b + (size_t)T * L->N * 2 && b < a + ((size_t)(T - 1) * ld + L->N) * 2;
+}
+
+// One forward of the current batch.  ep: what lora_forward_fused does with the sums, or null.  xq and sx: the caller's e4m3 rows of x with their scales
 // (lora_forward_e4m3), or null: the layer quantises x itself where its base is e4m3.
 static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, const float* sx,
-                         void* y_dev, int T, void* stream_, const char* name) {
+                         void* y_dev, int T, const lora_epilogue_t* ep, void* stream_, const char* name) {
   if (L->T_batch < 0) return fail(L, LORA_ESTATE, "%s before set_batch_segments", name);
   if (T != L->T_batch)
     return fail(L, LORA_ESTATE, "T=%d differs from the batch's T=%d", T, L->T_batch);
@@ -590,6 +597,21 @@ static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, con
     if (reinterpret_cast<uintptr_t>(xq) % 16 != 0 || reinterpret_cast<uintptr_t>(sx) % 4 != 0)
       return fail(L, LORA_EINVAL, "xq must be 16-byte aligned, sx 4-byte");
     LORA_CUDA(L, encode_tmap_u8(&tmap_rows, xq, T, L->K, kTcTileRows));
+  }
+  GemmEpilogue epilogue;
+  if (ep) {
+    if (L->dtype != LORA_BF16) return fail(L, LORA_EINVAL, "%s needs a bf16 layer", name);
+    if (ep->activation < LORA_ACT_NONE || ep->activation > LORA_ACT_SILU)
+      return fail(L, LORA_EINVAL, "activation %d", ep->activation);
+    if ((ep->factor && (ep->ldf < L->N || ep->ldf % 8)) || (ep->residual && (ep->ldr < L->N || ep->ldr % 8)))
+      return fail(L, LORA_EINVAL, "row distances %d, %d: multiples of 8 from %d up", ep->ldf, ep->ldr, L->N);
+    const uintptr_t all = reinterpret_cast<uintptr_t>(ep->bias) | reinterpret_cast<uintptr_t>(ep->factor) |
+                          reinterpret_cast<uintptr_t>(ep->residual);
+    if (all % 16) return fail(L, LORA_EINVAL, "bias, factor and residual must be 16-byte aligned");
+    if (rows_clash(L, ep->factor, ep->ldf, y_dev, T) || rows_clash(L, ep->residual, ep->ldr, y_dev, T) ||
+        (ep->bias && overlaps_y(ep->bias, (size_t)L->N * 2)))
+      return fail(L, LORA_EINVAL, "bias, factor or residual and y overlap without being the same");
+    epilogue = GemmEpilogue{true, ep->bias, ep->activation, ep->factor, ep->ldf, ep->residual, ep->ldr};
   }
   const bool quantise = L->fp8 && !xq;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
@@ -739,6 +761,7 @@ static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, con
   // the kernel ahead first), so nothing counts them: their loads start as those of a bf16 x do
   ga.q_ready = quantise ? L->q_ready : nullptr;
   ga.tmap_delta = L->delta ? &L->tmap_delta : nullptr;
+  ga.ep = epilogue;
   LORA_CUDA(L, trace_mark(L, 4, stream));
   if (bf16) {
     LORA_CUDA(L, launch_gemm_tc(ga, L->tmap_w, L->Bx_pool ? L->tmap_bx : nullptr, stream,
@@ -759,7 +782,16 @@ static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, con
 
 int lora_forward(lora_layer_t* L, const void* x_dev, void* y_dev, int T, void* stream) {
   if (!L) return LORA_EINVAL;
-  return forward_batch(L, x_dev, nullptr, nullptr, y_dev, T, stream, "lora_forward");
+  return forward_batch(L, x_dev, nullptr, nullptr, y_dev, T, nullptr, stream, "lora_forward");
+}
+
+int lora_forward_fused(lora_layer_t* L, const void* x_dev, const void* xq_dev, const float* sx_dev,
+                       void* y_dev, int T, const lora_epilogue_t* epilogue, void* stream) {
+  if (!L) return LORA_EINVAL;
+  if (!epilogue) return fail(L, LORA_EINVAL, "null epilogue");
+  if ((xq_dev || sx_dev) && (!L->fp8 || !xq_dev || !sx_dev))
+    return fail(L, LORA_EINVAL, "xq and sx go together, with an e4m3 base");
+  return forward_batch(L, x_dev, xq_dev, sx_dev, y_dev, T, epilogue, stream, "lora_forward_fused");
 }
 
 int lora_forward_e4m3(lora_layer_t* L, const void* x_dev, const void* xq_dev, const float* sx_dev,
@@ -767,7 +799,7 @@ int lora_forward_e4m3(lora_layer_t* L, const void* x_dev, const void* xq_dev, co
   if (!L) return LORA_EINVAL;
   if (!L->fp8) return fail(L, LORA_EINVAL, "lora_forward_e4m3 needs a layer with an e4m3 base");
   if (T > 0 && (!xq_dev || !sx_dev)) return fail(L, LORA_EINVAL, "null xq or sx");
-  return forward_batch(L, x_dev, xq_dev, sx_dev, y_dev, T, stream, "lora_forward_e4m3");
+  return forward_batch(L, x_dev, xq_dev, sx_dev, y_dev, T, nullptr, stream, "lora_forward_e4m3");
 }
 
 int lora_forward_host(lora_layer_t* L, const void* x_host, const int32_t* token_slot_host,

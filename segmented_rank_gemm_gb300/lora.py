@@ -35,7 +35,7 @@ LAYER_FUNCTIONS = ("lora_layer_create", "lora_layer_create_pooled", "lora_layer_
                    "lora_get_pool_usage",
                    "load_adapter_slot", "load_adapter_slot_composed",
                    "unload_adapter_slot",
-                   "set_batch_segments", "lora_forward", "lora_forward_e4m3",
+                   "set_batch_segments", "lora_forward", "lora_forward_e4m3", "lora_forward_fused",
                    "lora_forward_host", "lora_get_status", "lora_get_segments",
                    "lora_set_trace_events", "lora_set_gemm_plan", "lora_last_error",
                    "lora_layer_destroy", "lora_build_segments_static",
@@ -68,6 +68,16 @@ class CacheStats(ctypes.Structure):
         return {name: int(getattr(self, name)) for name, _ in self._fields_}
 
 
+class Epilogue(ctypes.Structure):
+    """lora_epilogue_t."""
+    _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int),
+                ("factor", ctypes.c_void_p), ("ldf", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int)]
+
+
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
 class LoraError(RuntimeError):
     def __init__(self, code: int, msg: str = ""):
         self.code = code
@@ -92,6 +102,7 @@ def _load() -> ctypes.CDLL:
     L.set_batch_segments.argtypes = [vp, vp, i32, vp]
     L.lora_forward.argtypes = [vp, vp, vp, i32, vp]
     L.lora_forward_e4m3.argtypes = [vp, vp, vp, vp, vp, i32, vp]
+    L.lora_forward_fused.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp]
     L.lora_forward_host.argtypes = [vp, vp, vp, vp, i32, vp]
     L.lora_get_status.argtypes = [vp, vp]
     L.lora_get_segments.argtypes = [vp, vp, vp, vp, vp, vp, vp]
@@ -303,6 +314,11 @@ def lora_forward_e4m3(layer, x, xq, sx, y, T, stream=None) -> None:
                                          _stream(stream)))
 
 
+def lora_forward_fused(layer, x, y, T, epilogue: Epilogue, xq=None, sx=None, stream=None) -> None:
+    _check(layer, _lib.lora_forward_fused(layer, _ptr(x), _ptr(xq), _ptr(sx), _ptr(y), T,
+                                          ctypes.addressof(epilogue), _stream(stream)))
+
+
 def lora_forward_host(layer, x_host, token_slot_host, y_host, T, stream=None) -> None:
     _check(layer, _lib.lora_forward_host(layer, _ptr(x_host), _ptr(token_slot_host),
                                          _ptr(y_host), T, _stream(stream)))
@@ -391,6 +407,11 @@ def lora_layer_destroy(layer) -> None:
     _lib.lora_layer_destroy(layer)
 
 
+def _dense_rows(name: str, t: torch.Tensor, shape, dtypes) -> None:
+    if not t.is_cuda or t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense CUDA tensor {shape} of {dtypes[0]}")
+
+
 # ---------------------------------------------------------------------------------
 # owner object
 # ---------------------------------------------------------------------------------
@@ -474,14 +495,46 @@ class LoraLayer:
         """forward with the base's e4m3 rows given: ``xq`` [T, K] bytes and ``sx`` [T], as
         ``norm.rms_norm`` writes them; ``x`` feeds the low-rank product."""
         T = int(x.shape[0])
-        for name, t, shape, ok in (("x", x, (T, self.K), (self.dtype,)),
-                                   ("xq", xq, (T, self.K), (torch.uint8, torch.float8_e4m3fn)),
-                                   ("sx", sx, (T,), (torch.float32,))):
-            if not t.is_cuda or t.dtype not in ok or tuple(t.shape) != shape \
-                    or not t.is_contiguous():
-                raise ValueError(f"{name} must be a dense CUDA tensor {shape} of {ok[0]}")
+        _dense_rows("x", x, (T, self.K), (self.dtype,))
+        _dense_rows("xq", xq, (T, self.K), (torch.uint8, torch.float8_e4m3fn))
+        _dense_rows("sx", sx, (T,), (torch.float32,))
         y = self._output(T, y, x.device, stream)
         lora_forward_e4m3(self.handle, x, xq, sx, y, T, stream)
+        return y
+
+    def forward_fused(self, x: torch.Tensor, y: torch.Tensor = None, bias=None, activation=None,
+                      factor=None, residual=None, xq=None, sx=None, stream=None) -> torch.Tensor:
+        """y = act(v + bias) * factor + residual, v the forward's rows before they are rounded
+        (``lora_forward_fused``): ``activation`` None or one of ``ACTIVATIONS``, ``bias`` [N],
+        ``factor`` and ``residual`` [T, N] bf16 (rows may be apart; each may be y).  With ``xq`` and
+        ``sx`` the base takes those e4m3 rows, as ``forward_e4m3``."""
+        T = int(x.shape[0])
+        if self.dtype != torch.bfloat16:
+            raise ValueError("forward_fused needs a bf16 layer")
+        if activation not in ACTIVATIONS:
+            raise ValueError("activation must be one of %s" % sorted(filter(None, ACTIVATIONS)))
+        _dense_rows("x", x, (T, self.K), (self.dtype,))
+        if (xq is None) != (sx is None):
+            raise ValueError("xq and sx go together")
+        if xq is not None:
+            _dense_rows("xq", xq, (T, self.K), (torch.uint8, torch.float8_e4m3fn))
+            _dense_rows("sx", sx, (T,), (torch.float32,))
+        ep = Epilogue(activation=ACTIVATIONS[activation])
+        if bias is not None:
+            _dense_rows("bias", bias, (self.N,), (self.dtype,))
+            ep.bias = bias.data_ptr()
+        for name, t in (("factor", factor), ("residual", residual)):
+            if t is None:
+                continue
+            if t.dtype != self.dtype or not t.is_cuda or t.shape != (T, self.N) \
+                    or (self.N > 1 and t.stride(1) != 1):
+                raise ValueError("%s must be a CUDA tensor %s of %s with dense rows"
+                                 % (name, (T, self.N), self.dtype))
+            ld = t.stride(0) if T > 1 else self.N  # one row has no distance
+            setattr(ep, name, t.data_ptr())
+            setattr(ep, "ldf" if name == "factor" else "ldr", ld)
+        y = self._output(T, y, x.device, stream)
+        lora_forward_fused(self.handle, x, y, T, ep, xq, sx, stream)
         return y
 
     def __call__(self, x, token_slot, y=None, stream=None):

@@ -91,3 +91,16 @@ def test_no_device_is_a_cuda_error_not_a_crash(lib):
     h = ctypes.c_void_p()
     rc = L.lora_layer_create(ctypes.byref(h), 64, 64, 4, 16, 8, lib.LORA_BF16, 16, None)
     assert rc in (lib.LORA_ECUDA, lib.LORA_ENOMEM) and not h.value
+
+
+def test_null_calls_of_the_later_entry_points_are_rejected(lib):
+    L = lib.library()
+    assert L.lora_forward_fused(None, 16, None, None, 32, 4, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_append_rotated(None, *[16] * 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_attend_cross(None, *[16] * 10, 1.0, 16, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_attend_shared(None, *[16] * 15, 1.0, 16, 16, 16, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_shared_workspace(None, 4, 4) == lib.LORA_EINVAL
+    assert L.lora_kv_fork(None, None, 16, 16, 4, 16, 16, 4, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_fork(16, None, 16, 16, 4, 24, 16, 4, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_fork(16, None, 16, 16, 0, 16, 16, 4, 16, None) == lib.LORA_EINVAL
+    assert L.lora_kv_release_shared(16, 16, None, 4, 16, 16, 4, 16, 8, 16, 16, None) == lib.LORA_EINVAL
