@@ -259,8 +259,15 @@ static cudaError_t launch_one(const GemmArgs& a, const GemmPlan& plan, const CUt
   const int ti = gemm_tc_tile_index(plan.pair ? plan.block_n / 2 : plan.block_n);
   const CUtensorMap& tw = tmap_w3[ti];
   const CUtensorMap& tb = tmap_bx3 ? tmap_bx3[ti] : tw;  // unused in delta mode
-  return a.ep.on ? launch_planned_fused(a, plan, tmap_x, tw, tb, stream)
-                 : launch_planned<false>(a, plan, tmap_x, tw, tb, stream);
+  if (!a.ep.on) return launch_planned<kNoEpilogue>(a, plan, tmap_x, tw, tb, stream);
+  switch (a.ep.act) {
+    case LORA_ACT_NONE: return launch_planned_fused<LORA_ACT_NONE>(a, plan, tmap_x, tw, tb, stream);
+    case LORA_ACT_RELU: return launch_planned_fused<LORA_ACT_RELU>(a, plan, tmap_x, tw, tb, stream);
+    case LORA_ACT_GELU: return launch_planned_fused<LORA_ACT_GELU>(a, plan, tmap_x, tw, tb, stream);
+    case LORA_ACT_GELU_TANH: return launch_planned_fused<LORA_ACT_GELU_TANH>(a, plan, tmap_x, tw, tb, stream);
+    case LORA_ACT_SILU: return launch_planned_fused<LORA_ACT_SILU>(a, plan, tmap_x, tw, tb, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace lora

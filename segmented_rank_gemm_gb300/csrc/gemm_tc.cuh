@@ -68,6 +68,7 @@
 namespace lora {
 
 static constexpr int kTcThreads = 192;
+constexpr int kNoEpilogue = -1;  // else the lora_activation of a fused forward
 static constexpr int kBM = 128, kBK = 64;
 static constexpr int kABytes = kBM * kBK * 2;
 
@@ -128,75 +129,151 @@ __device__ __forceinline__ void store_y32(const float (&acc)[32], const GemmArgs
 }
 
 // ---- the epilogue of a fused forward: y = act(sum + bias) * factor + residual ----
-__device__ __forceinline__ uint4 load_global(const uint4* p) {  // (y may be where it loads from)
-  uint4 r;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
-  return r;
-}
-// 32 columns of a row of a factor or residual: 16-byte loads of the thread's own row, zero where y is
-// not written.
-__device__ __forceinline__ void load_row32(uint4 (&v)[4], const void* base, int ld, const GemmArgs& a, int row, int n) {
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + (size_t)row * ld + n);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < a.M && n + q * 8 < a.N) v[q] = load_global(src + q);
+// A warp's 32 rows of the factor and the residual come 32 columns (64 bytes a row) at a time into a
+// buffer of its own, four lanes a row: a thread that loaded its row by itself would touch 32 lines an
+// instruction, a quarter of which it uses.  16-byte piece q of row r lies at q ^ (r >> 1 & 3), so
+// that neither side meets bank conflicts.
+constexpr int kRowTile = 32 * 64;        // bytes of one of them
+constexpr int kRowTiles = 2 * kRowTile;  // of both
+struct RowTiles {
+  uint8_t* buf;  // of this warp
+  int m0, lane;  // its first row
+  // Where piece q of row r is, of the factor (0) or the residual (1).
+  __device__ __forceinline__ uint4* piece(int slot, int which, int r, int q) const {
+    return reinterpret_cast<uint4*>(buf + slot * kRowTiles + which * kRowTile + r * 64 + ((q ^ (r >> 1 & 3)) << 4));
   }
+  // Asks for columns n .. n + 31 of one of them, if it is given (rows past M and columns past N are zero).
+  __device__ __forceinline__ void ask(const GemmArgs& a, int slot, int which, int n) const {
+    const __nv_bfloat16* const rows = static_cast<const __nv_bfloat16*>(which ? a.ep.residual : a.ep.factor);
+    if (!rows) return;
+    const int ld = which ? a.ep.ldr : a.ep.ldf, q = lane & 3, col = n + q * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      const bool there = m0 + r < a.M && col < a.N;
+      cp_async_16_zfill(piece(slot, which, r, q), there ? rows + (size_t)(m0 + r) * ld + col : rows, there ? 16 : 0);
+    }
+  }
+  // A group of what was asked for.
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Stores 32 columns of y from n on by way of a place that is free, four lanes a row as above.
+  __device__ __forceinline__ void store(const float (&acc)[32], const GemmArgs& a, int slot, int which, int n) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *piece(slot, which, lane, q) = make_uint4(pack_bf16x2(acc[q * 8 + 0], acc[q * 8 + 1]),
+                                            pack_bf16x2(acc[q * 8 + 2], acc[q * 8 + 3]),
+                                            pack_bf16x2(acc[q * 8 + 4], acc[q * 8 + 5]),
+                                            pack_bf16x2(acc[q * 8 + 6], acc[q * 8 + 7]));
+    __syncwarp();
+    const int q = lane & 3, col = n + q * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      const uint4 v = *piece(slot, which, r, q);
+      if (m0 + r < a.M && col < a.N)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + (size_t)(m0 + r) * a.N + col) = v;
+    }
+    __syncwarp();
+  }
+};
+template <int PENDING>
+__device__ __forceinline__ void row_tiles_wait() {  // all but the last PENDING fetches have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+  __syncwarp();
 }
-// Its lines into L2, while the tile's main loop runs.
+// The lines of a row into L2, while the tile's main loop runs.
 __device__ __forceinline__ void prefetch_row(const void* base, int ld, const GemmArgs& a, int row, int n, int cols) {
   if (!base || row >= a.M) return;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(base) + (size_t)row * ld;
   for (int c = n; c < min(n + cols, a.N); c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
 }
-// x / (1 + e^-u): SiLU for u = x.  (e^-u overflows to infinity, which gives 0.)
-__device__ __forceinline__ float times_sigmoid(float x, float u) { return __fdividef(x, 1.f + __expf(-u)); }
+// The activations, two sums at once (a warp has a scheduler to itself here, so that instructions count).
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 exp2_of(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp_of(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+// x / (1 + 2^u): SiLU for u = -x log2(e).  (2^u overflows to infinity, which gives 0.)
+__device__ __forceinline__ float2 over_one_plus_exp2(float2 x, float2 u) {
+  return mul2(x, rcp_of(add2(exp2_of(u), splat(1.f))));
+}
+constexpr float kLog2E = 1.44269504088896341f;
+// x Phi(x) by Phi(-|x|) = erfc(z) / 2, z = |x| / sqrt 2, and the Chebyshev fit erfc(z) = t e^(-z^2 + P(t)),
+// t = 1 / (1 + z / 2), of relative error below 1.2e-7 for all z (Press, Teukolsky, Vetterling, Flannery,
+// Numerical Recipes, section 6.2): no branch, and exact in the tails.
+__device__ __forceinline__ float2 gelu(float2 x) {
+  const float2 z = mul2(make_float2(fabsf(x.x), fabsf(x.y)), splat(0.70710678118654752f));
+  const float2 t = rcp_of(fma2(z, splat(0.5f), splat(1.f)));
+  float2 p = fma2(t, splat(0.17087277f), splat(-0.82215223f));
+  p = fma2(t, p, splat(1.48851587f));
+  p = fma2(t, p, splat(-1.13520398f));
+  p = fma2(t, p, splat(0.27886807f));
+  p = fma2(t, p, splat(-0.18628806f));
+  p = fma2(t, p, splat(0.09678418f));
+  p = fma2(t, p, splat(0.37409196f));
+  p = fma2(t, p, splat(1.00002368f));
+  p = fma2(t, p, splat(-1.26551223f));
+  p = fma2(make_float2(-z.x, -z.y), z, p);
+  const float2 below = mul2(mul2(t, splat(0.5f)), exp2_of(mul2(p, splat(kLog2E))));  // Phi(-|x|)
+  const float2 xb = mul2(x, below);
+  return make_float2(x.x > 0.f ? x.x - xb.x : xb.x, x.y > 0.f ? x.y - xb.y : xb.y);
+}
+// x (1 + tanh u) / 2 = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float2 gelu_tanh(float2 x) {
+  constexpr float kTwo = 1.5957691216057308f * kLog2E;
+  return over_one_plus_exp2(x, mul2(x, fma2(mul2(x, x), splat(-kTwo * 0.044715f), splat(-kTwo))));
+}
+__device__ __forceinline__ float2 silu(float2 x) { return over_one_plus_exp2(x, mul2(x, splat(-kLog2E))); }
+__device__ __forceinline__ float2 relu(float2 x) {  // (NaN stays)
+  return make_float2(x.x < 0.f ? 0.f : x.x, x.y < 0.f ? 0.f : x.y);
+}
 template <class F>
 __device__ __forceinline__ void apply32(float (&acc)[32], F f) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = f(acc[i]);
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = f(make_float2(acc[i], acc[i + 1]));
+    acc[i] = y.x;
+    acc[i + 1] = y.y;
+  }
 }
-__device__ __forceinline__ void epilogue32(float (&acc)[32], const GemmArgs& a, int row, int n) {
-  const GemmEpilogue& e = a.ep;
-  uint4 f[4], r[4];
-  if (e.factor) load_row32(f, e.factor, e.ldf, a, row, n);
-  if (e.residual) load_row32(r, e.residual, e.ldr, a, row, n);
-  if (e.bias) {
+// bias: the 32 columns'; factor(q), residual(q): pieces of the row.
+// before_residual: called once before the residual is read.
+template <int ACT, class F, class W, class R>
+__device__ __forceinline__ void epilogue32(float (&acc)[32], const GemmEpilogue& e, const float* bias, const F& factor,
+                                           const W& before_residual, const R& residual) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (n + q * 8 >= a.N) break;
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.bias) + n) + q);
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[8 * q + 2 * i] += bf16_lo(w[i]), acc[8 * q + 2 * i + 1] += bf16_hi(w[i]);
-    }
+  for (int i = 0; i < (e.bias ? 8 : 0); ++i) {
+    const float4 b = reinterpret_cast<const float4*>(bias)[i];
+    acc[4 * i] += b.x;
+    acc[4 * i + 1] += b.y;
+    acc[4 * i + 2] += b.z;
+    acc[4 * i + 3] += b.w;
   }
-  switch (e.act) {
-    case LORA_ACT_RELU: apply32(acc, [](float x) { return x < 0.f ? 0.f : x; }); break;  // (NaN stays)
-    case LORA_ACT_GELU: apply32(acc, [](float x) { return 0.5f * x * (1.f + erff(x * 0.70710678118654752f)); }); break;
-    case LORA_ACT_GELU_TANH:  // 1 + tanh(u) = 2 / (1 + e^-2u)
-      apply32(acc, [](float x) { return times_sigmoid(x, 1.5957691216057308f * (x + 0.044715f * x * x * x)); });
-      break;
-    case LORA_ACT_SILU: apply32(acc, [](float x) { return times_sigmoid(x, x); }); break;
-    default: break;
-  }
+  if constexpr (ACT == LORA_ACT_RELU) apply32(acc, relu);
+  else if constexpr (ACT == LORA_ACT_GELU) apply32(acc, gelu);
+  else if constexpr (ACT == LORA_ACT_GELU_TANH) apply32(acc, gelu_tanh);
+  else if constexpr (ACT == LORA_ACT_SILU) apply32(acc, silu);
   if (e.factor) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t w[4] = {f[q].x, f[q].y, f[q].z, f[q].w};
+      const uint4 v = factor(q);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[8 * q + 2 * i] *= bf16_lo(w[i]), acc[8 * q + 2 * i + 1] *= bf16_hi(w[i]);
     }
   }
+  before_residual();
   if (e.residual) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t w[4] = {r[q].x, r[q].y, r[q].z, r[q].w};
+      const uint4 v = residual(q);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[8 * q + 2 * i] += bf16_lo(w[i]), acc[8 * q + 2 * i + 1] += bf16_hi(w[i]);
     }
   }
 }
+// Shared memory a fused launch takes besides: the tile's bias in fp32 and, where tiles follow one
+// another (v mode), the warps' row tiles; one tile a CTA (delta mode) has them in its idle ring.
+constexpr size_t fused_smem_bytes(int BN, bool vmode) { return (size_t)BN * 4 + (vmode ? 4 * kRowTiles : 0); }
 
 // The row's v (the sum of its K-split planes) at rank columns j0 .. j0 + 7, split into bf16
 // high parts (bf16 of v) and low parts (bf16 of v - high): hi + lo carries v to about 16
@@ -272,7 +349,7 @@ __device__ __forceinline__ bool seg_at(int k, int g, int G, int U, int nkb, int 
 // then holds 128 elements instead of 64, the MMAs are kind::f8f6f4, and the accumulator is
 // scaled by sx[row] sw[col] before the low-rank term is added (delta mode: in the
 // epilogue; v mode: in TMEM, between the base and the expand blocks).
-template <int BN, bool PAIR, bool VMODE, bool FP8 = false, bool FUSED = false>
+template <int BN, bool PAIR, bool VMODE, bool FP8 = false, int EPILOGUE = kNoEpilogue>
 __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
                    const __grid_constant__ CUtensorMap tmap_w,
@@ -589,6 +666,13 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
     uint32_t gpar = 0;  // bit s = parity of stage s's next xgrant phase
     int ring = 0;       // ring blocks (base and expand) of this CTA's earlier tiles
     if (vmode) griddep_wait();  // v and the checked slots come from earlier kernels
+    // a fused forward's bias of the tile, and this warp's row tiles: one place behind it (v mode), or
+    // two in the ring behind what the delta mode's epilogue lands there
+    float* const bias_tile = reinterpret_cast<float*>(bars + 4 * stages + 8);
+    const auto row_tiles = [&](int m0) {
+      uint8_t* const base = vmode ? reinterpret_cast<uint8_t*>(bias_tile + BN) : stage_base + (size_t)BN * kBM * 4;
+      return RowTiles{base + quad * (vmode ? 1 : 2) * kRowTiles, m0 + quad * 32, lane};
+    };
     // stream-K: flags carry the launch's epoch + 1 (the epoch advances when the last CTA of a
     // launch exits, so no flag of an earlier launch matches)
     const int32_t epoch =
@@ -727,10 +811,27 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
         ring += nx;
       }
       ring += nk;
-      if constexpr (FUSED) {
-        const int cols = BN / cs, from = n0 + z * cols;
-        prefetch_row(a.ep.factor, a.ep.ldf, a, row, from, cols);
-        prefetch_row(a.ep.residual, a.ep.ldr, a, row, from, cols);
+      // a fused forward's inputs, while the main loop runs: the bias of this CTA's columns, and the
+      // rows' lines into L2 (v mode: the first of them on their way here)
+      if constexpr (EPILOGUE != kNoEpilogue) {
+        if (!vmode || head) {
+          const int cols = BN / cs, from = n0 + z * cols;
+          prefetch_row(a.ep.factor, a.ep.ldf, a, row, from, cols);
+          prefetch_row(a.ep.residual, a.ep.ldr, a, row, from, cols);
+          if (vmode) {
+            const RowTiles tiles = row_tiles(m0);
+            tiles.ask(a, 0, a.ep.factor ? 0 : 1, from);
+            tiles.commit();
+            if (a.ep.factor) tiles.ask(a, 0, 1, from);
+            tiles.commit();
+          }
+          if (a.ep.bias) {
+            for (int i = et; i < cols; i += 128)
+              bias_tile[i] =
+                  from + i < a.N ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.ep.bias)[from + i]) : 0.f;
+            named_barrier(1, 128);
+          }
+        }
       }
       const bool full_ok = ok && mbar_wait(&tmem_full[b], (uint32_t)kph & 1u, a.err);
       // a split K (one tile per CTA) must still meet its cluster barrier below, whatever
@@ -845,6 +946,13 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
         // (one tile per CTA: every barrier below is in its first phase)
         if (cs > 1 && !mbar_wait(xinfo_bar, 0u, a.err)) ok = false;
         named_barrier(1, 128);  // the column scales staged
+        RowTiles tiles;
+        if constexpr (EPILOGUE != kNoEpilogue) {  // (the ring is free: the accumulator is complete)
+          tiles = row_tiles(m0);
+          tiles.ask(a, 0, 0, n0 + cbase);
+          tiles.ask(a, 0, 1, n0 + cbase);
+          tiles.commit();
+        }
         // While the low-rank kernel may still run: this CTA's columns of the product, the
         // peers' partials added and (e4m3) scaled, back into block 0 (row rt's own entries)
         if (cs > 1) {
@@ -912,8 +1020,20 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
               acc[4 * q + 3] += d.w;
             }
           }
-          if constexpr (FUSED) epilogue32(acc, a, row, cfirst + c);
-          store_y32(acc, a, row, cfirst + c, yrow);
+          if constexpr (EPILOGUE != kNoEpilogue) {
+            const int slot = c >> 5 & 1;
+            if (c + 32 < bnc) {
+              tiles.ask(a, slot ^ 1, 0, cfirst + c + 32);
+              tiles.ask(a, slot ^ 1, 1, cfirst + c + 32);
+            }
+            tiles.commit();
+            row_tiles_wait<1>();
+            epilogue32<EPILOGUE>(acc, a.ep, bias_tile + c, [&](int q) { return *tiles.piece(slot, 0, lane, q); }, [] {},
+                       [&](int q) { return *tiles.piece(slot, 1, lane, q); });
+            tiles.store(acc, a, slot, 1, cfirst + c);
+          } else {
+            store_y32(acc, a, row, cfirst + c, yrow);
+          }
         }
       } else {
         // ---- v mode: a stream-K head adds its tail's partial (one block) ----
@@ -946,8 +1066,27 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
             for (int j = 0; j < n_extra; ++j) add_block32(acc, xin + (size_t)j * nq * kBM + rt, c);
             if (FP8) scale32(acc, sxr_v, sw_tile + c);
           }
-          if constexpr (FUSED) epilogue32(acc, a, row, n0 + cbase + c);
-          store_y32(acc, a, row, n0 + cbase + c, yrow);
+          if constexpr (EPILOGUE != kNoEpilogue) {
+            const RowTiles tiles = row_tiles(m0);
+            // What is there of factor and residual goes to registers, and its next columns are asked
+            // for at once; where both are, the residual waits in its place, through which y leaves.
+            const int held = a.ep.factor ? 0 : 1, next = n0 + cbase + c + 32;
+            uint4 v[4];
+            row_tiles_wait<1>();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = *tiles.piece(0, held, lane, q);
+            __syncwarp();
+            if (c + 32 < bnc) tiles.ask(a, 0, held, next);
+            tiles.commit();
+            epilogue32<EPILOGUE>(acc, a.ep, bias_tile + c, [&](int q) { return v[q]; },
+                                 [&] { if (!held) row_tiles_wait<1>(); },
+                                 [&](int q) { return held ? v[q] : *tiles.piece(0, 1, lane, q); });
+            tiles.store(acc, a, 0, held ^ 1, n0 + cbase + c);
+            if (c + 32 < bnc && !held) tiles.ask(a, 0, 1, next);
+            tiles.commit();
+          } else {
+            store_y32(acc, a, row, n0 + cbase + c, yrow);
+          }
         }
       }
       // this buffer is drained: the MMAs may fill it with tile k + 2 (pairs: both CTAs'
@@ -992,10 +1131,10 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
 
 // Raise (never lower) one kernel variant's dynamic shared-memory limit: one cache per
 // variant, shared by every caller.
-template <int BN, bool PAIR, bool VMODE, bool FP8 = false, bool FUSED = false>
+template <int BN, bool PAIR, bool VMODE, bool FP8 = false, int EPILOGUE = kNoEpilogue>
 static cudaError_t raise_smem_limit(int bytes) {
   static int limit[kAttrDevices] = {};
-  return ensure_smem_limit(gemm_tc_kernel<BN, PAIR, VMODE, FP8, FUSED>, bytes, limit);
+  return ensure_smem_limit(gemm_tc_kernel<BN, PAIR, VMODE, FP8, EPILOGUE>, bytes, limit);
 }
 
 static size_t tc_smem_bytes(int BN, bool pair, bool fp8, int stages, int xscr_bytes) {
@@ -1004,7 +1143,7 @@ static size_t tc_smem_bytes(int BN, bool pair, bool fp8, int stages, int xscr_by
          (4 * stages + 8) * 8;
 }
 
-template <int BN, bool PAIR, bool VMODE, bool FP8, bool FUSED>
+template <int BN, bool PAIR, bool VMODE, bool FP8, int EPILOGUE>
 static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUtensorMap& tmap_x,
                              const CUtensorMap& tmap_w, const CUtensorMap& tmap_bx,
                              cudaStream_t stream) {
@@ -1019,8 +1158,9 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
   if (cs > 1 && (!a.xk || a.xk_floats < gemm_tc_plan_exchange_floats(plan, a.M, a.n_end - a.n_begin)))
     return cudaErrorInvalidValue;
   int stages = 8;
-  while (stages > 2 && tc_smem_bytes(BN, PAIR, FP8, stages, xscr) > budget) --stages;
-  const size_t smem = tc_smem_bytes(BN, PAIR, FP8, stages, xscr);
+  const size_t more = EPILOGUE != kNoEpilogue ? fused_smem_bytes(BN, VMODE) : 0;
+  while (stages > 2 && tc_smem_bytes(BN, PAIR, FP8, stages, xscr) + more > budget) --stages;
+  const size_t smem = tc_smem_bytes(BN, PAIR, FP8, stages, xscr) + more;
   if (smem > budget) return cudaErrorInvalidConfiguration;
   // the epilogue lands its split-K partials and delta rows (128 x BN fp32) in the ring, and
   // counts each 32-column delta box on one of the 2 * stages v-mode stage barriers
@@ -1029,7 +1169,9 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
   if ((cs > 1 || a.ex.mode == kExpandDelta || a.sk_part) &&
       (size_t)stages * stage < (size_t)kBM * BN * 4)
     return cudaErrorInvalidConfiguration;
-  cudaError_t e = raise_smem_limit<BN, PAIR, VMODE, FP8, FUSED>((int)smem);
+  if (EPILOGUE != kNoEpilogue && !VMODE && (size_t)stages * stage < (size_t)kBM * BN * 4 + 4 * 2 * kRowTiles)
+    return cudaErrorInvalidConfiguration;
+  cudaError_t e = raise_smem_limit<BN, PAIR, VMODE, FP8, EPILOGUE>((int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -1075,66 +1217,76 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
       std::max(1, std::min(mtp, (int)((32u << 20) / ((size_t)a.K * band_rows * 2))));
   // delta mode: the delta tile arrives through the delta buffer's map
   if (!VMODE && !a.tmap_delta) return cudaErrorInvalidValue;
-  return cudaLaunchKernelEx(&cfg, gemm_tc_kernel<BN, PAIR, VMODE, FP8, FUSED>, tmap_x, tmap_w, tmap_bx,
+  return cudaLaunchKernelEx(&cfg, gemm_tc_kernel<BN, PAIR, VMODE, FP8, EPILOGUE>, tmap_x, tmap_w, tmap_bx,
                             VMODE ? tmap_w : *a.tmap_delta, a, stages, xscr, group_m, mtp, nt,
                             full_rounds, sk_slots);
 }
 
-template <bool FUSED>
+template <int EPILOGUE>
 static cudaError_t launch_variant_fp8(const GemmArgs& a, const GemmPlan& plan,
                                       const CUtensorMap& tmap_x, const CUtensorMap& tw,
                                       const CUtensorMap& tb, cudaStream_t stream) {
   if (a.ex.mode == kExpandV) {
     if (plan.pair) {
-      if (plan.block_n == 256) return launch_tc<256, true, true, true, FUSED>(a, plan, tmap_x, tw, tb, stream);
-      if (plan.block_n == 128) return launch_tc<128, true, true, true, FUSED>(a, plan, tmap_x, tw, tb, stream);
+      if (plan.block_n == 256) return launch_tc<256, true, true, true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+      if (plan.block_n == 128) return launch_tc<128, true, true, true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
       return cudaErrorInvalidConfiguration;
     }
     switch (plan.block_n) {
-      case 256: return launch_tc<256, false, true, true, FUSED>(a, plan, tmap_x, tw, tb, stream);
-      case 128: return launch_tc<128, false, true, true, FUSED>(a, plan, tmap_x, tw, tb, stream);
-      default: return launch_tc<64, false, true, true, FUSED>(a, plan, tmap_x, tw, tb, stream);
+      case 256: return launch_tc<256, false, true, true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+      case 128: return launch_tc<128, false, true, true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+      default: return launch_tc<64, false, true, true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
     }
   }
   if (plan.pair) {
-    if (plan.block_n == 256) return launch_tc<256, true, false, true, FUSED>(a, plan, tmap_x, tw, tw, stream);
-    if (plan.block_n == 128) return launch_tc<128, true, false, true, FUSED>(a, plan, tmap_x, tw, tw, stream);
+    if (plan.block_n == 256) return launch_tc<256, true, false, true, EPILOGUE>(a, plan, tmap_x, tw, tw, stream);
+    if (plan.block_n == 128) return launch_tc<128, true, false, true, EPILOGUE>(a, plan, tmap_x, tw, tw, stream);
     return cudaErrorInvalidConfiguration;
   }
   switch (plan.block_n) {
-    case 256: return launch_tc<256, false, false, true, FUSED>(a, plan, tmap_x, tw, tw, stream);
-    case 128: return launch_tc<128, false, false, true, FUSED>(a, plan, tmap_x, tw, tw, stream);
-    default: return launch_tc<64, false, false, true, FUSED>(a, plan, tmap_x, tw, tw, stream);
+    case 256: return launch_tc<256, false, false, true, EPILOGUE>(a, plan, tmap_x, tw, tw, stream);
+    case 128: return launch_tc<128, false, false, true, EPILOGUE>(a, plan, tmap_x, tw, tw, stream);
+    default: return launch_tc<64, false, false, true, EPILOGUE>(a, plan, tmap_x, tw, tw, stream);
   }
 }
 
-template <bool VMODE, bool FUSED>
+template <bool VMODE, int EPILOGUE>
 static cudaError_t launch_variant(const GemmArgs& a, const GemmPlan& plan,
                                   const CUtensorMap& tmap_x, const CUtensorMap& tw,
                                   const CUtensorMap& tb, cudaStream_t stream) {
   if (plan.pair) {
-    if (plan.block_n == 256) return launch_tc<256, true, VMODE, false, FUSED>(a, plan, tmap_x, tw, tb, stream);
-    if (plan.block_n == 128) return launch_tc<128, true, VMODE, false, FUSED>(a, plan, tmap_x, tw, tb, stream);
+    if (plan.block_n == 256) return launch_tc<256, true, VMODE, false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+    if (plan.block_n == 128) return launch_tc<128, true, VMODE, false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
     return cudaErrorInvalidConfiguration;
   }
   switch (plan.block_n) {
-    case 256: return launch_tc<256, false, VMODE, false, FUSED>(a, plan, tmap_x, tw, tb, stream);
-    case 128: return launch_tc<128, false, VMODE, false, FUSED>(a, plan, tmap_x, tw, tb, stream);
-    default: return launch_tc<64, false, VMODE, false, FUSED>(a, plan, tmap_x, tw, tb, stream);
+    case 256: return launch_tc<256, false, VMODE, false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+    case 128: return launch_tc<128, false, VMODE, false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+    default: return launch_tc<64, false, VMODE, false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
   }
 }
 
 // A launch of the variant that the plan and the base's type ask for.
-template <bool FUSED>
+template <int EPILOGUE>
 static cudaError_t launch_planned(const GemmArgs& a, const GemmPlan& plan, const CUtensorMap& tmap_x,
                                   const CUtensorMap& tw, const CUtensorMap& tb, cudaStream_t stream) {
-  if (a.fp8) return launch_variant_fp8<FUSED>(a, plan, tmap_x, tw, tb, stream);
-  return a.ex.mode == kExpandV ? launch_variant<true, FUSED>(a, plan, tmap_x, tw, tb, stream)
-                               : launch_variant<false, FUSED>(a, plan, tmap_x, tw, tb, stream);
+  if (a.fp8) return launch_variant_fp8<EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
+  return a.ex.mode == kExpandV ? launch_variant<true, EPILOGUE>(a, plan, tmap_x, tw, tb, stream)
+                               : launch_variant<false, EPILOGUE>(a, plan, tmap_x, tw, tb, stream);
 }
 
-// The variants with an epilogue (gemm_tc_fused.cu).
+// The variants with an epilogue, a translation unit for each activation (gemm_tc_*.cu).  They are
+// variants, and not a branch, because one activation's code in the instruction cache is what a decode
+// forward's epilogue waits for: with a switch over all of them gate projections of 512 rows took 82
+// (bf16) and 85 us (e4m3) without any activation, 77 and 76 so (the plain forward 78 and 73).
+template <int ACT>
 cudaError_t launch_planned_fused(const GemmArgs& a, const GemmPlan& plan, const CUtensorMap& tmap_x,
                                  const CUtensorMap& tw, const CUtensorMap& tb, cudaStream_t stream);
+#define LORA_FUSED_VARIANTS(ACT)                                                                           \
+  template <>                                                                                              \
+  cudaError_t launch_planned_fused<ACT>(const GemmArgs& a, const GemmPlan& plan, const CUtensorMap& tmap_x, \
+                                        const CUtensorMap& tw, const CUtensorMap& tb, cudaStream_t stream) { \
+    return launch_planned<ACT>(a, plan, tmap_x, tw, tb, stream);                                           \
+  }
 
 }  // namespace lora
