@@ -370,6 +370,7 @@ int lora_kv_append_rotated(lora_kv_cache_t* c, const void* q, int ldq, int q_hea
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;
   a.err = c->err;
+  a.num_sms = c->num_sms;
   KV_CUDA(c, launch_kv_rotate(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;
 }

@@ -140,6 +140,7 @@ struct KvRotateArgs {
   int max_position, rotary, interleaved;
   float k_scale, v_scale;
   int32_t* err;
+  int num_sms;
 };
 cudaError_t launch_kv_rotate(const KvRotateArgs& a, cudaStream_t stream);
 // Joins the results of rows with a shared prefix (kv_share.cu).

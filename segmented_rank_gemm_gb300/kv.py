@@ -225,12 +225,14 @@ class KvCache:
         if angles.dtype is not torch.float32 or angles.get_device() != dev or not angles.is_contiguous() \
                 or angles.shape != (rotary.max_position, rotary.rotary_dim // 2, 2):
             _bad("the angles must be fp32 [max_position, rotary_dim / 2, 2] on the current CUDA device")
-        position, kv_slot = _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev)
+        # (names of their own: a tensor that only the caller's expression held would be freed here, and
+        # its memory could become q_out's)
+        position_at, slot_at = _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev)
         if q_out is None:
             q_out = empty(q_shape, _BF16, q.device, stream)
         self._check(_lib.lora_kv_append_rotated(
             self.handle, q.data_ptr(), ldq, q_heads, q_out.data_ptr(), _rows("q_out", q_out, q_shape, dev),
-            k.data_ptr(), ldk, v.data_ptr(), ldv, position, kv_slot, T, angles.data_ptr(),
+            k.data_ptr(), ldk, v.data_ptr(), ldv, position_at, slot_at, T, angles.data_ptr(),
             rotary.max_position, rotary.rotary_dim, rotary.interleaved, _stream(stream, dev)))
         return q_out
 

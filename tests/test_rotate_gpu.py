@@ -154,6 +154,20 @@ def test_packed_rows_in_place_on_a_stream_and_in_a_graph():
         assert torch.equal(x, y)
 
 
+def test_positions_and_slots_that_only_the_call_holds():
+    # tensors made in the call's expression stay until it has been made: an output that the call
+    # allocates is not their memory
+    from segmented_rank_gemm_gb300.kv import KvCache, Rotary
+    q, k, v = _case(1, 8, 2, 128, 1)
+    table, cache = Rotary(1000, 128), KvCache(1, 64, 2, 128, 1)
+    want = _bf16(ref.rotated(_np(q), *_angles(table, [999]), False))
+    for _ in range(20):
+        torch.cuda.empty_cache()
+        out = cache.append_rotated(q.to(DEV), k.to(DEV), v.to(DEV), _ints([999]), _ints([5]), table)
+        assert cache.status() == 0 and torch.equal(out.cpu(), want)
+    cache.close()
+
+
 def test_positions_and_slots_outside_are_flagged_and_left_alone():
     from segmented_rank_gemm_gb300.kv import KvCache, Rotary
     from segmented_rank_gemm_gb300.lora import LORA_EID
