@@ -150,8 +150,8 @@ int lora_kv_append(lora_kv_cache_t* cache, const void* k_dev, int ldk, const voi
  *                   (with ldqo = ldq), or else does not overlap it; nor k and v, whose columns may
  *                   lie beside it in the same rows.  1 <= q_heads <= 16384.
  *   position [T]    each row's position, 0 .. max_position - 1.
- *   angles          [max_position, rotary_dim / 2] pairs (cos, sin) fp32, 16-byte aligned: row p, pair
- *                   i is the cosine and sine of p times pair i's frequency.
+ *   angles          [max_position, 2, rotary_dim / 2] fp32, 16-byte aligned: row p has the cosines of p
+ *                   times the pairs' frequencies, then the sines.
  *   rotary_dim      the first dimensions of a head, which are turned: a multiple of 32 up to
  *                   head_dim.  Pair i is dimensions i and i + rotary_dim / 2, or 2 i and 2 i + 1 if
  *                   `interleaved`.

@@ -363,7 +363,7 @@ int lora_kv_append_rotated(lora_kv_cache_t* c, const void* q, int ldq, int q_hea
   a.position = position;
   a.slots = slots;
   a.T = T;
-  a.angles = reinterpret_cast<const float2*>(angles);
+  a.angles = angles;
   a.max_position = max_position;
   a.rotary = rotary_dim;
   a.interleaved = interleaved != 0;

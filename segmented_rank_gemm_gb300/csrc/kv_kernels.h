@@ -136,7 +136,7 @@ struct KvRotateArgs {
   int ldq, ldqo, ldk, ldv, q_heads;
   const int32_t *position, *slots;
   int T;
-  const float2* angles;  // [max_position][rotary / 2] (cos, sin)
+  const float* angles;  // [max_position][2][rotary / 2]: cosines, sines
   int max_position, rotary, interleaved;
   float k_scale, v_scale;
   int32_t* err;

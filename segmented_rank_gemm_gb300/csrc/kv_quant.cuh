@@ -96,12 +96,14 @@ __device__ __forceinline__ void write_group(const uint4 lo, const uint4 hi, floa
 // Writes the group of fp32 pairs x.
 template <bool IS_V>
 __device__ __forceinline__ void write_group(const float2 (&x)[8], float g, uint8_t* codes, uint8_t* scale) {
-  float top = 0.f;
-  bool nan = false;
+  float top = 0.f;  // a NaN if there is one
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    top = fmaxf(top, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));  // (NaN elements drop out)
-    nan = nan || x[j].x != x[j].x || x[j].y != x[j].y;
+  for (int j = 0; j < 8; ++j) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x[j].x), "f"(x[j].y));
+  const bool nan = top != top;
+  if (nan) {
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
   }
   write_codes<IS_V>([&](int j) { return x[j]; }, top, nan, g, codes, scale);
 }

@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "kv_decode.cuh"
 #include "kv_kernels.h"
 #include "kv_quant.cuh"
@@ -27,37 +29,36 @@ constexpr int kThreads = 256;
 constexpr int kQHeads = 4;
 constexpr int kCtasPerSm = 4;
 
-// a b + c d of two floats at once.  The sums are scalar: packed ones are fused with the packed products
-// before them, which spares the product's rounding (seen in results where the terms cancel).
-__device__ __forceinline__ float2 sum_of_products(float2 a, float2 b, float2 c, float2 d) {
-  const float2 x = mul2(a, b), y = mul2(c, d);
+__device__ __forceinline__ float2 bf16x2_values(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+// a c - b s and b c + a s of two pairs at once.  The sums are scalar: packed ones are fused with the packed
+// products before them, which spares a product's rounding (seen in results where the terms cancel).
+__device__ __forceinline__ float2 turned_a(float2 a, float2 b, float2 c, float2 s) {
+  const float2 x = mul2(a, c), y = mul2(b, s);
+  return make_float2(__fsub_rn(x.x, y.x), __fsub_rn(x.y, y.y));
+}
+__device__ __forceinline__ float2 turned_b(float2 a, float2 b, float2 c, float2 s) {
+  const float2 x = mul2(b, c), y = mul2(a, s);
   return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
-__device__ __forceinline__ float2 bf16x2_values(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
-
-// Word i of two pairs' first elements a and second ones b, turned by two angles (c, s, c, s).
-__device__ __forceinline__ float2 turned_a(uint32_t a, uint32_t b, const float4& cs) {
-  return sum_of_products(bf16x2_values(a), make_float2(cs.x, cs.z), bf16x2_values(b), make_float2(-cs.y, -cs.w));
-}
-__device__ __forceinline__ float2 turned_b(uint32_t a, uint32_t b, const float4& cs) {
-  return sum_of_products(bf16x2_values(b), make_float2(cs.x, cs.z), bf16x2_values(a), make_float2(cs.y, cs.w));
-}
-// A word that is a pair, turned by (c, s).
-__device__ __forceinline__ float2 turned_pair(uint32_t w, float c, float s) {
-  const float2 ab = bf16x2_values(w);
-  return sum_of_products(ab, make_float2(c, c), make_float2(ab.y, ab.x), make_float2(-s, s));
+// One pair, its elements beside each other.
+__device__ __forceinline__ float2 turned_pair(float2 ab, float c, float s) {
+  const float2 x = mul2(ab, make_float2(c, c)), y = mul2(make_float2(ab.y, ab.x), make_float2(s, s));
+  return make_float2(__fsub_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
 
-// Two angles from another lane.  A row's angles are loaded once by the lanes of a warp, a piece (two of
-// them) each, and exchanged where they are used: loaded by each thread, 64 or 128 bytes a lane, they
-// took three quarters of the L1's cycles (8192 rows of 32 and 8 heads of 128 38 us, 31 exchanged).
+// Four cosines or sines from another lane.  A row's angles are loaded once by the lanes of a warp, four
+// of them each, and exchanged where they are used: loaded by each thread, 64 or 128 bytes a lane, they
+// took three quarters of the L1's cycles (8192 rows of 32 and 8 heads of 128 40 us, 33 exchanged).
 __device__ __forceinline__ float4 from_lane(const float4& v, int lane) {
   return make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
                      __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
 }
-__device__ __forceinline__ float4 load_piece(const float2* row, int i) {
+__device__ __forceinline__ float4 load_piece(const float* row, int i) {
   return __ldg(reinterpret_cast<const float4*>(row) + i);
 }
+__device__ __forceinline__ float flip(float x, uint32_t sign) { return __uint_as_float(__float_as_uint(x) ^ sign); }
+__device__ __forceinline__ float2 low(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 high(const float4& v) { return make_float2(v.z, v.w); }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
@@ -69,11 +70,6 @@ __device__ __forceinline__ void write_one(const KvRotateArgs& a, unsigned i, uns
   const KvPages& pg = a.pages;
   const unsigned per = pg.heads * kGroups;  // of a token
   const bool some = i < a.T * per;
-  if (i + ahead < a.T * per && (i & 3) == 0) {  // a line of a block to come
-    const unsigned t = (i + ahead) / per, e = (i + ahead - t * per) * 16;
-    prefetch_l2(IS_V ? static_cast<const __nv_bfloat16*>(a.v) + static_cast<size_t>(t) * a.ldv + e
-                     : static_cast<const __nv_bfloat16*>(a.k) + static_cast<size_t>(t) * a.ldk + e);
-  }
   if (!some) i = a.T * per - kGroups + i % kGroups;  // (for its lane's sake: what it has is not written)
   const unsigned t = i / per, r = i - t * per;
   const int head = r / kGroups, g = r % kGroups, lane = threadIdx.x & 31;
@@ -81,6 +77,8 @@ __device__ __forceinline__ void write_one(const KvRotateArgs& a, unsigned i, uns
   const __nv_bfloat16* const src =
       (IS_V ? static_cast<const __nv_bfloat16*>(a.v) + static_cast<size_t>(t) * a.ldv
             : static_cast<const __nv_bfloat16*>(a.k) + static_cast<size_t>(t) * a.ldk) + head * D + g * 16;
+  if (t + ahead < static_cast<unsigned>(a.T) && (i & 3) == 0)  // a line of a block to come
+    prefetch_l2(src + static_cast<size_t>(ahead) * (IS_V ? a.ldv : a.ldk));
   const uint4 lo = load_in_order(reinterpret_cast<const uint4*>(src));
   const uint4 hi = load_in_order(reinterpret_cast<const uint4*>(src) + 1);
   const bool there = static_cast<unsigned>(slot) < static_cast<unsigned>(pg.num_pages) << pg.page_shift;
@@ -96,24 +94,30 @@ __device__ __forceinline__ void write_one(const KvRotateArgs& a, unsigned i, uns
     return;
   }
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const float2* const row = a.angles + static_cast<size_t>(known ? pos : 0) * (a.rotary / 2);
-  const int last = a.rotary / 4 - 1, half = a.rotary / 32;  // pieces of a row - 1, groups of half a rotation
+  const float* const row = a.angles + static_cast<size_t>(known ? pos : 0) * a.rotary;
+  const int sines = a.rotary / 8, half = a.rotary / 32;  // the sines' first piece, groups of half a rotation
   const bool rotated = g * 16 < a.rotary, second = APART && rotated && g >= half;
   const bool one = __all_sync(0xffffffffu, t == __shfl_sync(0xffffffffu, t, 0));  // one token's lanes
-  const float4 mine = load_piece(row, min(lane, last));
-  const int piece0 = APART ? (second ? g - half : g) * 8 : g * 4;
+  const float4 mine = load_piece(row, min(lane, 2 * sines - 1));
+  const int piece0 = !rotated ? 0 : APART ? (second ? g - half : g) * 4 : g * 2;
+  const int partner = !rotated ? lane : second ? lane - half : lane + half;
+  const uint32_t turn = second ? 0u : 0x80000000u;  // the first elements take the sine's product off
   float2 x[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!APART && (j & 1)) continue;
-    const int k = piece0 + (APART ? j : j / 2);
-    const float4 cs = one ? from_lane(mine, k & 31) : load_piece(row, min(k, last));
+  for (int j = 0; j < 8; j += APART ? 2 : 4) {  // four angles
+    const int k = piece0 + j / (APART ? 2 : 4);
+    float4 c = one ? from_lane(mine, k) : load_piece(row, k);
+    float4 sn = one ? from_lane(mine, sines + k) : load_piece(row, sines + k);
     if constexpr (APART) {
-      const uint32_t other = __shfl_sync(0xffffffffu, w[j], !rotated ? lane : second ? lane - half : lane + half);
-      x[j] = second ? turned_b(other, w[j], cs) : turned_a(w[j], other, cs);
+      sn = make_float4(flip(sn.x, turn), flip(sn.y, turn), flip(sn.z, turn), flip(sn.w, turn));
+      const uint32_t o0 = __shfl_sync(0xffffffffu, w[j], partner), o1 = __shfl_sync(0xffffffffu, w[j + 1], partner);
+      x[j] = turned_b(bf16x2_values(o0), bf16x2_values(w[j]), low(c), low(sn));
+      x[j + 1] = turned_b(bf16x2_values(o1), bf16x2_values(w[j + 1]), high(c), high(sn));
     } else {
-      x[j] = turned_pair(w[j], cs.x, cs.y);
-      x[j + 1] = turned_pair(w[j + 1], cs.z, cs.w);
+      x[j] = turned_pair(bf16x2_values(w[j]), c.x, sn.x);
+      x[j + 1] = turned_pair(bf16x2_values(w[j + 1]), c.y, sn.y);
+      x[j + 2] = turned_pair(bf16x2_values(w[j + 2]), c.z, sn.z);
+      x[j + 3] = turned_pair(bf16x2_values(w[j + 3]), c.w, sn.w);
     }
   }
   if (!write) return;
@@ -129,18 +133,18 @@ __device__ __forceinline__ void turn_queries(const KvRotateArgs& a, unsigned i, 
   const unsigned chunks = (a.q_heads + kQHeads * kLanes - 1) / (kQHeads * kLanes);
   const unsigned warp = i / 32, t = warp / chunks, lane = i % 32;
   if (t >= static_cast<unsigned>(a.T)) return;
-  const unsigned next = (warp + ahead / 32) / chunks;
-  if (next < static_cast<unsigned>(a.T)) {  // the lines of a warp to come, and its angles
-    const unsigned chunk = warp + ahead / 32 - next * chunks;
+  // a warp to come: its lines, and its angles
+  const unsigned next = t + ahead, chunk = warp - t * chunks;
+  if (next < static_cast<unsigned>(a.T)) {
     const int e = chunk * (kQHeads * kLanes * D) + lane * 64;
     if (e < a.q_heads * D) prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + static_cast<size_t>(next) * a.ldq + e);
     const int pos = load_in_order(a.position + next);
-    if (chunk == 0 && static_cast<int>(lane) * 16 < a.rotary / 2 &&
+    if (chunk == 0 && static_cast<int>(lane) * 32 < a.rotary &&
         static_cast<unsigned>(pos) < static_cast<unsigned>(a.max_position))
-      prefetch_l2(a.angles + static_cast<size_t>(pos) * (a.rotary / 2) + lane * 16);
+      prefetch_l2(a.angles + static_cast<size_t>(pos) * a.rotary + lane * 32);
   }
   const int slice = lane % kSlices;
-  const int head0 = (warp - t * chunks) * (kQHeads * kLanes) + lane / kSlices;
+  const int head0 = chunk * (kQHeads * kLanes) + lane / kSlices;
   const int pos = load_in_order(a.position + t);
   const bool rotated = slice * 16 < a.rotary;
   const int d0 = APART && rotated ? slice * 8 : slice * 16, d1 = APART && rotated ? d0 + a.rotary / 2 : d0 + 8;
@@ -158,11 +162,12 @@ __device__ __forceinline__ void turn_queries(const KvRotateArgs& a, unsigned i, 
     if (slice == 0 && head0 == 0) atomicOr(a.err, LORA_ERRF_BAD_ID);
     return;
   }
+  const int sines = a.rotary / 8, piece0 = rotated ? slice * 2 : 0;
   const float4 mine =
-      load_piece(a.angles + static_cast<size_t>(pos) * (a.rotary / 2), min(static_cast<int>(lane), a.rotary / 4 - 1));
-  float4 cs[4];
+      load_piece(a.angles + static_cast<size_t>(pos) * a.rotary, min(static_cast<int>(lane), 2 * sines - 1));
+  float4 c[2], sn[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) cs[i] = from_lane(mine, slice * 4 + i);
+  for (int i = 0; i < 2; ++i) c[i] = from_lane(mine, piece0 + i), sn[i] = from_lane(mine, sines + piece0 + i);
 #pragma unroll
   for (int h = 0; h < kQHeads; ++h) {
     const int head = head0 + h * kLanes;
@@ -171,14 +176,17 @@ __device__ __forceinline__ void turn_queries(const KvRotateArgs& a, unsigned i, 
       uint32_t w0[4] = {v0[h].x, v0[h].y, v0[h].z, v0[h].w}, w1[4] = {v1[h].x, v1[h].y, v1[h].z, v1[h].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_values(w0[k]), v = bf16x2_values(w1[k]);
         float2 x, y;
         if constexpr (APART) {
-          x = turned_a(w0[k], w1[k], cs[k]);
-          y = turned_b(w0[k], w1[k], cs[k]);
-        } else {  // angles 2 k' and 2 k' + 1 of the first words' pairs, then of the second ones'
-          const float4 c0 = cs[k / 2], c1 = cs[2 + k / 2];
-          x = k & 1 ? turned_pair(w0[k], c0.z, c0.w) : turned_pair(w0[k], c0.x, c0.y);
-          y = k & 1 ? turned_pair(w1[k], c1.z, c1.w) : turned_pair(w1[k], c1.x, c1.y);
+          const float2 ck = k & 1 ? high(c[k / 2]) : low(c[k / 2]), sk = k & 1 ? high(sn[k / 2]) : low(sn[k / 2]);
+          x = turned_a(u, v, ck, sk);
+          y = turned_b(u, v, ck, sk);
+        } else {  // the first words' pairs have the first four angles
+          const float ca[4] = {c[0].x, c[0].y, c[0].z, c[0].w}, sa[4] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w};
+          const float cb[4] = {c[1].x, c[1].y, c[1].z, c[1].w}, sb[4] = {sn[1].x, sn[1].y, sn[1].z, sn[1].w};
+          x = turned_pair(u, ca[k], sa[k]);
+          y = turned_pair(v, cb[k], sb[k]);
         }
         w0[k] = pack_bf16x2(x.x, x.y);
         w1[k] = pack_bf16x2(y.x, y.y);
@@ -191,20 +199,21 @@ __device__ __forceinline__ void turn_queries(const KvRotateArgs& a, unsigned i, 
   }
 }
 
-// The kernel behind may start at once: it reads the cache and the queries behind its own wait.
+// kv_share: the share of blocks that keys and values take, times 2^32, rounded up.  The kernel behind may
+// start at once: it reads the cache and the queries behind its own wait.
 template <int D, bool APART>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rotate_kernel(KvRotateArgs a, unsigned kv_blocks, unsigned kv_ahead, unsigned q_ahead) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    kv_rotate_kernel(KvRotateArgs a, uint32_t kv_share, unsigned ahead) {
   griddep_wait();
   griddep_launch_dependents();
   // the blocks of keys and values evenly among those of queries: how many of the former come before
-  const unsigned long long n = 2 * kv_blocks;
-  const unsigned before = static_cast<unsigned>(blockIdx.x * n / gridDim.x);
-  if ((blockIdx.x + 1) * n / gridDim.x == before)
-    turn_queries<D, APART>(a, (blockIdx.x - before) * kThreads + threadIdx.x, q_ahead);
+  const unsigned before = __umulhi(blockIdx.x, kv_share);
+  if (__umulhi(blockIdx.x + 1, kv_share) == before)
+    turn_queries<D, APART>(a, (blockIdx.x - before) * kThreads + threadIdx.x, ahead);
   else if (before & 1)
-    write_one<D, APART, true>(a, (before >> 1) * kThreads + threadIdx.x, kv_ahead);
+    write_one<D, APART, true>(a, (before >> 1) * kThreads + threadIdx.x, ahead);
   else
-    write_one<D, APART, false>(a, (before >> 1) * kThreads + threadIdx.x, kv_ahead);
+    write_one<D, APART, false>(a, (before >> 1) * kThreads + threadIdx.x, ahead);
 }
 
 template <int D, bool APART>
@@ -213,12 +222,12 @@ cudaError_t launch(const KvRotateArgs& a, cudaStream_t stream) {
   constexpr int kWarpHeads = kQHeads * 32 / (D / 16);
   const unsigned kv = blocks(static_cast<long long>(a.T) * a.pages.heads * (D / 16));
   const unsigned q = blocks(static_cast<long long>(a.T) * ((a.q_heads + kWarpHeads - 1) / kWarpHeads) * 32);
-  // what the blocks that follow the resident ones read is asked for a round ahead
-  const long long resident = static_cast<long long>(a.num_sms) * kCtasPerSm, all = 2ll * kv + q;
-  const unsigned kv_ahead = static_cast<unsigned>(resident * kv / all) * kThreads,
-                 q_ahead = static_cast<unsigned>(resident * q / all) * kThreads;
-  return launch_dependent(kv_rotate_kernel<D, APART>, dim3(static_cast<unsigned>(all)), kThreads, 0, stream, a, kv,
-                          kv_ahead, q_ahead);
+  const unsigned long long n = 2ull * kv, all = n + q;
+  // what the blocks that follow the resident ones read is asked for a round, so many tokens, ahead
+  const long long ahead = static_cast<long long>(a.T) * a.num_sms * kCtasPerSm / static_cast<long long>(all);
+  return launch_dependent(kv_rotate_kernel<D, APART>, dim3(static_cast<unsigned>(all)), kThreads, 0, stream, a,
+                          static_cast<uint32_t>(((n << 32) + all - 1) / all),
+                          static_cast<unsigned>(std::min<long long>(ahead + 1, 1 << 30)));
 }
 
 }  // namespace

@@ -35,6 +35,8 @@ def _rows(name: str, t, shape, device: int) -> int:
     if t.dtype is not _BF16 or t.get_device() != device or t.shape != shape:
         _bad("%s must be a bf16 tensor of shape %s on the current CUDA device, not %s %s on %s"
              % (name, shape, t.dtype, tuple(t.shape), t.device))
+    if t.is_contiguous():
+        return shape[1] * shape[2]
     row, head, one = t.stride()
     if (shape[2] > 1 and one != 1) or (shape[1] > 1 and head != shape[2]):
         _bad("%s: the heads of a row must be dense" % name)
@@ -110,7 +112,7 @@ def lora_kv_fork(parent, want, lens, shared, page_size, block_table, status, str
 
 class Rotary:
     """The angles of a rotation of queries and keys by position, for ``KvCache.append_rotated``:
-    ``angles`` [max_position, rotary_dim / 2, 2] fp32, the cosine and sine, computed in 64 bits, of
+    ``angles`` [max_position, 2, rotary_dim / 2] fp32, the cosines and sines, computed in 64 bits, of
     p * frequency[i].  The first ``rotary_dim`` dimensions of a head are turned, a multiple of 32:
     pair i is dimensions i and i + rotary_dim / 2, or 2 i and 2 i + 1 if ``interleaved``.
     ``frequencies`` [rotary_dim / 2] default to theta ** (-2 i / rotary_dim)."""
@@ -126,8 +128,12 @@ class Rotary:
             raise ValueError("frequencies must be [rotary_dim / 2]")
         angle = torch.outer(torch.arange(max_position, dtype=torch.float64, device=device),
                             frequencies.to(device=device, dtype=torch.float64))
-        self.angles = torch.stack((angle.cos(), angle.sin()), -1).float()
+        self._angles = torch.stack((angle.cos(), angle.sin()), 1).float().contiguous()
         self.max_position, self.rotary_dim, self.interleaved = max_position, rotary_dim, interleaved
+
+    @property
+    def angles(self) -> torch.Tensor:
+        return self._angles
 
 
 class PageTable:
@@ -221,10 +227,9 @@ class KvCache:
         T, q_heads, dev = q.shape[0], q.shape[1], torch.cuda.current_device()
         shape, q_shape = (T, self.kv_heads, self.head_dim), (T, q_heads, self.head_dim)
         ldq, ldk, ldv = _rows("q", q, q_shape, dev), _rows("k", k, shape, dev), _rows("v", v, shape, dev)
-        angles = rotary.angles
-        if angles.dtype is not torch.float32 or angles.get_device() != dev or not angles.is_contiguous() \
-                or angles.shape != (rotary.max_position, rotary.rotary_dim // 2, 2):
-            _bad("the angles must be fp32 [max_position, rotary_dim / 2, 2] on the current CUDA device")
+        angles = rotary._angles  # (of its own making: the device is all that can be wrong)
+        if angles.get_device() != dev:
+            _bad("the angles must be on the current CUDA device")
         # (names of their own: a tensor that only the caller's expression held would be freed here, and
         # its memory could become q_out's)
         position_at, slot_at = _i32("position", position, T, dev), _i32("kv_slot", kv_slot, T, dev)

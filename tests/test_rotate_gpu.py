@@ -42,7 +42,7 @@ def _case(T, hq, hkv, D, seed):
 
 def _angles(rotary, position):
     t = rotary.angles.cpu().numpy()[np.asarray(position)]
-    return t[..., 0], t[..., 1]
+    return t[..., 0, :], t[..., 1, :]
 
 
 @pytest.mark.parametrize("D,rotary", [(64, 64), (64, 32), (128, 128), (128, 96), (128, 64), (128, 32)])
@@ -212,8 +212,9 @@ def test_refusals():
     rows = torch.zeros(T, (hq + 2 * hkv) * D, dtype=torch.bfloat16, device=DEV)
     flat = torch.zeros(2 * T * hq * D, dtype=torch.bfloat16, device=DEV)
     ok = dict(q=q, k=k, v=v, position=_ints([0, 1, 2]), kv_slot=_ints([0, 1, 2]), rotary=Rotary(4, 64))
-    wide, other = Rotary(4, 96), Rotary(4, 64)
-    other.angles = other.angles[:3]
+    wide, other = Rotary(4, 96), Rotary(4, 64, device="cpu")
+    with pytest.raises(AttributeError):
+        other.angles = other.angles[:3]
     shifted = flat[8:8 + T * hq * D].view(T, hq, D)
     for change in (dict(q=q.float()), dict(k=k[:2]), dict(v=v.float()), dict(position=_ints([0, 1])),
                    dict(kv_slot=_ints([0, 1, 2]).long()), dict(rotary=wide), dict(rotary=other),

@@ -428,7 +428,7 @@ def test_a_prompt_forked_and_continued():
         assert cache.status() == 0 and pages.status()[3] == 0
         pos = pages.position[:T].cpu().numpy()
         cs = table[pos]
-        kr = ref.held(ref.rotated(_np(k), cs[..., 0], cs[..., 1], False))
+        kr = ref.held(ref.rotated(_np(k), cs[:, 0], cs[:, 1], False))
         row = 0
         for b, m in enumerate(new):
             held[b][0].extend(kr[row:row + m])
