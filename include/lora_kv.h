@@ -222,8 +222,10 @@ int lora_kv_attend_cross(lora_kv_cache_t* cache, const void* q_dev, int ldq, int
  *                   pages (or 0), of the pages in row prefix_row[g] of block_table -- a member's,
  *                   or those of the request that members were forked from (lora_kv_fork).
  *   shared_len [B]  the first shared_len[b] positions of request b are its group's prefix:
- *                   prefix_len[g], all before its new tokens.  With 0 the request, in a group or
- *                   not, is attended as in lora_kv_attend.
+ *                   prefix_len[g], all before its new tokens, and its own row of block_table names
+ *                   their pages too (lora_kv_fork leaves them there; small batches are attended
+ *                   without sharing).  With 0 the request, in a group or not, is attended as in
+ *                   lora_kv_attend.
  *   workspace       lora_kv_shared_workspace bytes of device memory for T rows, 16-byte aligned, for
  *                   the time of the call; it overlaps neither q nor out.
  * Sharing pays where a group has many rows that see few keys of their own; requests whose rows fill

@@ -295,6 +295,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
     }
   }
 
+  if (SPANS && a.alone && blockIdx.x == gridDim.x - 1) {  // (else done by what reads and joins the parts)
+    for (int b = tid; b < a.B; b += kThreads) check_group_of(a, b);
+    for (int v = 0; v < a.groups; ++v) check_prefix_pages(a, v, tid, kThreads);
+  }
   if (span * blockIdx.x >= total) return;
   const long long raw_lo = span * blockIdx.x, raw_hi = min(total, raw_lo + span);
   // A cut within snap of a group's edge moves there, which spares two pieces (512 tokens beside 8
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         for (int j = 0; j < 2; ++j) {
           const long long off = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.ldo);
           if (off < 0) continue;
-          if (SPANS && a.groups && g == 0)
+          if (SPANS && a.groups && !a.alone && g == 0)
             a.part_ml[0][column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D) / D] = kv_row_done();
           const float l = j ? st.l.y : st.l.x;
           const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         *reinterpret_cast<float2*>(to.o + row * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
-      if (SPANS && a.groups && lane == 0)
+      if (SPANS && a.groups && !a.alone && lane == 0)
         a.part_ml[0][static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G] =
             kv_row_done();
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;

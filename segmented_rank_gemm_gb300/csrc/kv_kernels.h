@@ -114,6 +114,7 @@ struct KvAttendArgs {
   const int32_t *group_offsets, *prefix_row, *prefix_len;  // [groups + 1], [groups], [groups] (or null)
   const int32_t* shared;  // [B] (or null)
   int groups;
+  int alone;  // the groups are checked, but every request is attended by itself
   // Unnormalised results that are joined afterwards, of every row and head of T: O [D], and the
   // reference m with the sum l.  [0]: of a request's own positions, [1]: of its group's prefix.
   float* part_o[2];

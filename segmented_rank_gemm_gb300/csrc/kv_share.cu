@@ -75,27 +75,13 @@ __device__ __forceinline__ float2 join_pieces(const KvAttendArgs& a, KvPieces p,
   return make_float2(m, l);
 }
 
-// The groups agree with their requests: one with a prefix is a member, and has its group's.
-__device__ void check_request(const KvAttendArgs& a, int b) {
-  const Span s = load_span(a, a.groups + b, false);
-  if (s.q_len == 0 || s.kind == kSpanWhole) return;
-  int lo = 0, hi = a.groups;  // the last group that starts at b or before
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.group_offsets[mid] <= b) lo = mid;
-    else hi = mid;
-  }
-  if (b < a.group_offsets[lo] || b >= a.group_offsets[lo + 1] || a.shared[b] != a.prefix_len[lo])
-    atomicOr(a.err, LORA_ERRF_BAD_ID);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_share_join_kernel(KvAttendArgs a, int row_blocks) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) >= row_blocks) {
     const int b = (blockIdx.x - row_blocks) * kThreads + threadIdx.x;
-    if (b < a.B) check_request(a, b);
+    if (b < a.B) check_group_of(a, b);
     return;
   }
   const long long at = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);

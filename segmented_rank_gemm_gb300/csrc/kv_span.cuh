@@ -42,7 +42,7 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     s.row0 = load_in_order(a.q_offsets + from);
     const int end = load_in_order(a.q_offsets + to);
     bad = bad || s.row0 < 0 || end < s.row0 || end > a.T;
-    s.q_len = bad || s.kv == 0 ? 0 : end - s.row0;
+    s.q_len = bad || s.kv == 0 || a.alone ? 0 : end - s.row0;
     if (bad) s.kv = s.table_row = 0;
     s.first = 0;
     s.see = s.kv - 1;
@@ -63,7 +63,7 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     }
     // every row of a request sees all of its group's prefix, whose pages are whole
     bad = bad || (s.q_len > 0 && (share < 0 || (share & in_page) || share > max(0, s.kv - s.q_len)));
-    s.first = min(max(share, 0), s.kv) & ~in_page;
+    s.first = a.alone ? 0 : min(max(share, 0), s.kv) & ~in_page;
     s.see = (a.causal ? s.kv - s.q_len : s.kv - 1) - s.first;
     s.slope = a.causal ? 1 : 0;
     s.table_row = b;
@@ -71,6 +71,31 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
   }
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
   return s;
+}
+
+// The groups agree with their requests: one with a prefix is a member, and has its group's.
+__device__ __forceinline__ void check_group_of(const KvAttendArgs& a, int b) {
+  if (load_in_order(a.q_offsets + b + 1) <= load_in_order(a.q_offsets + b)) return;
+  const int share = load_in_order(a.shared + b);
+  if (share <= 0) return;
+  int lo = 0, hi = a.groups;  // the last group that starts at b or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (load_in_order(a.group_offsets + mid) <= b) lo = mid;
+    else hi = mid;
+  }
+  if (b < load_in_order(a.group_offsets + lo) || b >= load_in_order(a.group_offsets + lo + 1) ||
+      share != load_in_order(a.prefix_len + lo))
+    atomicOr(a.err, LORA_ERRF_BAD_ID);
+}
+
+// The pages of group v's prefix are the cache's.
+__device__ __forceinline__ void check_prefix_pages(const KvAttendArgs& a, int v, int first, int step) {
+  const Span s = load_span(a, v, false);
+  for (int j = first; j < s.kv >> a.pages.page_shift; j += step)
+    if (static_cast<unsigned>(load_in_order(a.table + static_cast<size_t>(s.table_row) * a.max_blocks + j)) >=
+        static_cast<unsigned>(a.pages.num_pages))
+      atomicOr(a.err, LORA_ERRF_BAD_ID);
 }
 
 // Pieces of the kernel for many rows (kv_prompt.cu): m [256], l [256], O [256][D]; a CTA has two, and

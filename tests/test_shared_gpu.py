@@ -176,6 +176,19 @@ def test_all_requests_by_themselves_is_attend():
     assert torch.equal(out, b.cache.attend(**a))
 
 
+@pytest.mark.parametrize("wide", [0, 4000])
+def test_small_batches_on_both_sides_of_the_rule(wide):
+    # a wider table (whose entries are not read) makes the longest request possible longer
+    b = Batch([(64, [(30, 1), (50, 4), (1, 1)]), (128, [(9, 2)])], 128, 2, 2, 16, seed=4)
+    table = np.concatenate((b.table, np.full((len(b.table), wide), 2 ** 30, np.int32)), 1)
+    b.check(block_table=table)
+    shared = b.shared + [0, 0]
+    from segmented_rank_gemm_gb300.lora import LORA_EID
+    for change in (dict(shared_len=[64, 32] + shared[2:]), dict(prefix_len=[32, 128]), dict(group_offsets=[0, 2, 4])):
+        b.attend(block_table=table, **change)
+        assert b.cache.status() == LORA_EID
+
+
 def test_scores_far_apart_between_prefix_and_own_positions():
     # all of the weight in the prefix, all of it behind, and both
     b = Batch([(320, [(40, 1), (33, 2), (64, 1)])], 128, 1, 4, 16, seed=11, spread=6.0)
