@@ -237,15 +237,16 @@ __device__ __forceinline__ void apply32(float (&acc)[32], F f) {
 // bias: the 32 columns'; factor(q), residual(q): pieces of the row.
 // before_residual: called once before the residual is read.
 template <int ACT, class F, class W, class R>
-__device__ __forceinline__ void epilogue32(float (&acc)[32], const GemmEpilogue& e, const float* bias, const F& factor,
-                                           const W& before_residual, const R& residual) {
+__device__ __forceinline__ void epilogue32(float (&acc)[32], const GemmEpilogue& e, const __nv_bfloat16* bias,
+                                           const F& factor, const W& before_residual, const R& residual) {
+  if (e.bias) {
 #pragma unroll
-  for (int i = 0; i < (e.bias ? 8 : 0); ++i) {
-    const float4 b = reinterpret_cast<const float4*>(bias)[i];
-    acc[4 * i] += b.x;
-    acc[4 * i + 1] += b.y;
-    acc[4 * i + 2] += b.z;
-    acc[4 * i + 3] += b.w;
+    for (int q = 0; q < 4; ++q) {
+      const uint4 v = reinterpret_cast<const uint4*>(bias)[q];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[8 * q + 2 * i] += bf16_lo(w[i]), acc[8 * q + 2 * i + 1] += bf16_hi(w[i]);
+    }
   }
   if constexpr (ACT == LORA_ACT_RELU) apply32(acc, relu);
   else if constexpr (ACT == LORA_ACT_GELU) apply32(acc, gelu);
@@ -271,9 +272,9 @@ __device__ __forceinline__ void epilogue32(float (&acc)[32], const GemmEpilogue&
     }
   }
 }
-// Shared memory a fused launch takes besides: the tile's bias in fp32 and, where tiles follow one
-// another (v mode), the warps' row tiles; one tile a CTA (delta mode) has them in its idle ring.
-constexpr size_t fused_smem_bytes(int BN, bool vmode) { return (size_t)BN * 4 + (vmode ? 4 * kRowTiles : 0); }
+// Shared memory a fused launch takes besides: the tile's bias.  The warps' row tiles are where a tile's
+// own rows of v were (v mode: the expand blocks have been written by then), or in the idle ring.
+constexpr size_t fused_smem_bytes(int BN) { return (size_t)BN * 2; }
 
 // The row's v (the sum of its K-split planes) at rank columns j0 .. j0 + 7, split into bf16
 // high parts (bf16 of v) and low parts (bf16 of v - high): hi + lo carries v to about 16
@@ -666,12 +667,14 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
     uint32_t gpar = 0;  // bit s = parity of stage s's next xgrant phase
     int ring = 0;       // ring blocks (base and expand) of this CTA's earlier tiles
     if (vmode) griddep_wait();  // v and the checked slots come from earlier kernels
-    // a fused forward's bias of the tile, and this warp's row tiles: one place behind it (v mode), or
-    // two in the ring behind what the delta mode's epilogue lands there
-    float* const bias_tile = reinterpret_cast<float*>(bars + 4 * stages + 8);
+    // a fused forward's bias of the tile, and this warp's row tiles: one place where its rows of v were
+    // (v mode), or two in the ring behind what the delta mode's epilogue lands there
+    __nv_bfloat16* const bias_tile = reinterpret_cast<__nv_bfloat16*>(bars + 4 * stages + 8);
     const auto row_tiles = [&](int m0) {
-      uint8_t* const base = vmode ? reinterpret_cast<uint8_t*>(bias_tile + BN) : stage_base + (size_t)BN * kBM * 4;
-      return RowTiles{base + quad * (vmode ? 1 : 2) * kRowTiles, m0 + quad * 32, lane};
+      static_assert(kRowTiles == 32 * 128, "a warp's rows of one expand block");
+      uint8_t* const buf = vmode ? xscr + (size_t)quad * 32 * xl.nbs * 128
+                                 : stage_base + (size_t)BN * kBM * 4 + quad * 2 * kRowTiles;
+      return RowTiles{buf, m0 + quad * 32, lane};
     };
     // stream-K: flags carry the launch's epoch + 1 (the epoch advances when the last CTA of a
     // launch exits, so no flag of an earlier launch matches)
@@ -819,6 +822,7 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
           prefetch_row(a.ep.factor, a.ep.ldf, a, row, from, cols);
           prefetch_row(a.ep.residual, a.ep.ldr, a, row, from, cols);
           if (vmode) {
+            __syncwarp();  // the rows of v there have been read
             const RowTiles tiles = row_tiles(m0);
             tiles.ask(a, 0, a.ep.factor ? 0 : 1, from);
             tiles.commit();
@@ -827,8 +831,7 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
           }
           if (a.ep.bias) {
             for (int i = et; i < cols; i += 128)
-              bias_tile[i] =
-                  from + i < a.N ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.ep.bias)[from + i]) : 0.f;
+              bias_tile[i] = from + i < a.N ? static_cast<const __nv_bfloat16*>(a.ep.bias)[from + i] : __nv_bfloat16(0.f);
             named_barrier(1, 128);
           }
         }
@@ -1158,7 +1161,7 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
   if (cs > 1 && (!a.xk || a.xk_floats < gemm_tc_plan_exchange_floats(plan, a.M, a.n_end - a.n_begin)))
     return cudaErrorInvalidValue;
   int stages = 8;
-  const size_t more = EPILOGUE != kNoEpilogue ? fused_smem_bytes(BN, VMODE) : 0;
+  const size_t more = EPILOGUE != kNoEpilogue ? fused_smem_bytes(BN) : 0;
   while (stages > 2 && tc_smem_bytes(BN, PAIR, FP8, stages, xscr) + more > budget) --stages;
   const size_t smem = tc_smem_bytes(BN, PAIR, FP8, stages, xscr) + more;
   if (smem > budget) return cudaErrorInvalidConfiguration;
@@ -1166,8 +1169,9 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
   // counts each 32-column delta box on one of the 2 * stages v-mode stage barriers
   if (a.ex.mode == kExpandDelta && 2 * stages < BN / cs / 32) return cudaErrorInvalidConfiguration;
   const size_t stage = (size_t)kABytes + (size_t)(PAIR ? BN / 2 : BN) * kBK * 2;
-  if ((cs > 1 || a.ex.mode == kExpandDelta || a.sk_part) &&
-      (size_t)stages * stage < (size_t)kBM * BN * 4)
+  // (stream-K lands a tail's partial there too; without room for it no tile is cut)
+  const bool room = (size_t)stages * stage >= (size_t)kBM * BN * 4;
+  if ((cs > 1 || a.ex.mode == kExpandDelta || (a.sk_part && EPILOGUE == kNoEpilogue)) && !room)
     return cudaErrorInvalidConfiguration;
   if (EPILOGUE != kNoEpilogue && !VMODE && (size_t)stages * stage < (size_t)kBM * BN * 4 + 4 * 2 * kRowTiles)
     return cudaErrorInvalidConfiguration;
@@ -1198,7 +1202,7 @@ static cudaError_t launch_tc(const GemmArgs& a, const GemmPlan& plan, const CUte
   // the head starts its accumulator with a block of its own
   constexpr int kKE = FP8 ? 2 * kBK : kBK;
   int full_rounds = (units + G - 1) / G, sk_slots = 0;
-  if (a.ex.mode == kExpandV && a.sk_part && a.sk_sync && units > G && (a.K + kKE - 1) / kKE >= 2) {
+  if (a.ex.mode == kExpandV && a.sk_part && a.sk_sync && room && units > G && (a.K + kKE - 1) / kKE >= 2) {
     const int rem = units % G;
     if (rem > 0 && 2 * rem <= G) {
       full_rounds = units / G;

@@ -144,6 +144,18 @@ def test_pooled_and_composed_adapters_and_wide_ranks():
         plain.close()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("R", [8, 32, 40, 64, 72, 128])
+def test_every_width_of_slots(R, e4m3):
+    # the ring and what lies beside it in shared memory change with the slots' width
+    for T, N in ((64, 328), (700, 2056), (2300, 4104)):
+        c = Case(85, T, 256, N, S=3, ranks=[R, 1, max(1, R // 2)], R=R, e4m3=e4m3, base_frac=0.1, layout="runs")
+        for parts in ((1, 1, 1), (0, 1, 0), (0, 0, 1)):
+            c.check("silu", *parts, what="R=%d T=%d" % (R, T))
+        assert c.layer.status() == 0
+        c.layer.close()
+
+
 def test_strided_rows_in_place_and_nothing_beside():
     c = Case(90, 150, 256, 264)
     N, wide = 264, torch.full((150, 2 * 264 + 24), 7.0, dtype=torch.bfloat16, device="cuda")
