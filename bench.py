@@ -426,7 +426,7 @@ def run_stack(args):
         per_shape[name] = {"K": k, "N": n, "gemm_us": us,
                            "gemm_tflops": 2 * T * k * n / (us * 1e-6) / 1e12,
                            "bgmv_us": statistics.mean(bgmv_us[l][p] for l in range(len(st.layers)))}
-    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cu")
+    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cuh")
     out = {
         "metric": METRIC, "value": aggregate(T, args.steps, world, seconds), "unit": UNIT,
         "n_gpus": world, "steps": args.steps, "warmup": args.warmup,
@@ -669,7 +669,7 @@ def run_ours(args):
     pk = peaks()
     gemm_s = kern_us["gemm"] * 1e-6
     achieved = work["gemm_bytes"] / gemm_s / 1e9
-    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cu")
+    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cuh")
     roofline = {"kernel": "gemm_tc_kernel (base GEMM%s + fused expand)"
                           % (", e4m3" if args.fp8 else ""), "bound": "hbm",
                 "achieved": achieved, "peak": pk["hbm_gbs"], "unit": "GB/s",

@@ -11,6 +11,10 @@
 // small ones.  Work split: blocks of keys, of values and of queries in one launch, evenly among one
 // another as the former are bound by instructions and the latter by bytes.  A thread of keys or values
 // takes a group of 16 dimensions, a thread of queries 8 pairs of kQHeads heads, which share angles.
+//
+// Measured (32 query heads over 8 of 128): 8192 tokens at positions over 32768 32 us (181 MB, 5.6 TB/s; it
+// issues in 58% of its cycles), 512 tokens 3.6, one 2.  With a thread for two groups of keys the angles
+// and addresses cost half, but 84 registers leave 16 warps an SM: 42 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

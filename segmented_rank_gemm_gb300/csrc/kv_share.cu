@@ -6,7 +6,8 @@
 // well, by the same rule, with all rows of the batch at once.
 //
 // Bound: bytes (D fp32 twice in, D bf16 out of a row and head, mostly from L2) and, for a decode
-// batch, the launch and one trip to L2.  A warp takes a head of one row.
+// batch, the launch and one trip to L2.  A warp takes a head of one row.  Measured with 32 heads of 128:
+// 512 rows 10 us, 64 rows of 19 pieces each 8.4 (a third of either is the launch).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

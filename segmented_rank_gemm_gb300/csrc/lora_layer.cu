@@ -5,7 +5,7 @@
 //   set_batch_segments -> segment_builder_kernel            (builder.cu)
 //   lora_forward       -> bgmv_delta_kernel (decode: BGMV shrink + expand)  (lora_tile.cu)
 //                         or lora_tile_kernel (SGMV shrink per segment tile)
-//                      -> gemm_tc_kernel (bf16, tcgen05)                    (gemm_tc.cu)  or
+//                      -> gemm_tc_kernel (bf16, tcgen05)                    (gemm_tc.cuh) or
 //                         gemm_simt_f32_kernel (fp32)                       (gemm_simt.cu)
 // Two regimes.  bf16 batches of at most kDeltaMaxT rows (decode) use delta mode: the BGMV
 // kernel gathers each row's A and B by its slot id and writes the expanded low-rank term to
