@@ -12,8 +12,8 @@
 // another as the former are bound by instructions and the latter by bytes.  A thread of keys or values
 // takes a group of 16 dimensions, a thread of queries 8 pairs of kQHeads heads, which share angles.
 //
-// Measured (32 query heads over 8 of 128): 8192 tokens at positions over 32768 32 us (181 MB, 5.6 TB/s; it
-// issues in 58% of its cycles), 512 tokens 3.6, one 2.  With a thread for two groups of keys the angles
+// Measured (32 query heads over 8 of 128): 8192 tokens at positions over 32768 31 us (181 MB, 5.8 TB/s; it
+// issues in 58% of its cycles), 512 tokens 3, one 2.  With a thread for two groups of keys the angles
 // and addresses cost half, but 84 registers leave 16 warps an SM: 42 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,9 +29,10 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
+// (8192 tokens with the read-back 42.9 us with 512 threads a block, 40.4 with 256, 39.0 with 128, 38.8 with 64)
+constexpr int kThreads = 128;
 constexpr int kQHeads = 4;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 8;
 
 __device__ __forceinline__ float2 bf16x2_values(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 // a c - b s and b c + a s of two pairs at once.  The sums are scalar: packed ones are fused with the packed
@@ -227,11 +228,12 @@ cudaError_t launch(const KvRotateArgs& a, cudaStream_t stream) {
   const unsigned kv = blocks(static_cast<long long>(a.T) * a.pages.heads * (D / 16));
   const unsigned q = blocks(static_cast<long long>(a.T) * ((a.q_heads + kWarpHeads - 1) / kWarpHeads) * 32);
   const unsigned long long n = 2ull * kv, all = n + q;
-  // what the blocks that follow the resident ones read is asked for a round, so many tokens, ahead
+  // what the blocks that follow the resident ones read is asked for half a round, so many tokens, ahead
+  // (8192 tokens: 43.4 us not asked for, 41.4 two rounds ahead, 39.0 one, 38.5 half a round)
   const long long ahead = static_cast<long long>(a.T) * a.num_sms * kCtasPerSm / static_cast<long long>(all);
   return launch_dependent(kv_rotate_kernel<D, APART>, dim3(static_cast<unsigned>(all)), kThreads, 0, stream, a,
                           static_cast<uint32_t>(((n << 32) + all - 1) / all),
-                          static_cast<unsigned>(std::min<long long>(ahead + 1, 1 << 30)));
+                          static_cast<unsigned>(std::min<long long>(ahead / 2 + 1, 1 << 30)));
 }
 
 }  // namespace
