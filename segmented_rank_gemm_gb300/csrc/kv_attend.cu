@@ -101,15 +101,15 @@ struct Request {
 
 // Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
 // one before stands ahead of them.)
-template <bool SPANS>
+template <Spans SPANS>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bool report) {
   Request r;
   const int G = a.group;
-  if constexpr (SPANS) {
-    const Span s = load_span(a, b, report);
+  if constexpr (SPANS != kRequests) {
+    const Span s = load_span<SPANS>(a, b, report);
     r = Request{s.row0, s.q_len, s.kv, 0, 0, s.first, s.see, s.slope, s.table_row, s.kind};
     r.tiles = max(1, (r.kv - r.first + kTile - 1) / kTile);
-    r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + kCols - 1) / kCols;
+    r.col_tiles = span_is_few(a, s) ? (r.q_len * G + kCols - 1) / kCols : 0;
     return r;
   }
   r.row0 = load_in_order(a.q_offsets + b);
@@ -140,7 +140,7 @@ __device__ __forceinline__ long long request_units(const Request& r, int heads) 
 
 // A position in the sequence of tiles: request, head, column tile, tile (fastest last), and
 // the tile's unit: a group's tiles come after its kSetup units.
-template <bool SPANS>
+template <Spans SPANS>
 struct Cursor {
   Request r;
   int b, head, col, tile;
@@ -230,7 +230,7 @@ __device__ __forceinline__ void fetch_two(uint32_t mine, uint32_t dst, const uin
       : "memory");
 }
 
-template <int D, bool SPANS>
+template <int D, Spans SPANS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAttendArgs a) {
   constexpr int kBlock = kv_block_bytes(D), kTileBytes = 2 * kBlock;
   constexpr int KT = D / 16;         // 16-wide steps of D
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   if (a.many_follow) griddep_launch_dependents();
 
   // the sequence's length and this CTA's range; where each warp starts
-  const int count_b = SPANS ? a.B + a.groups : a.B;
+  const int count_b = SPANS == kShared ? a.B + a.groups : a.B;
   const int per = (count_b + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, count_b), b1 = min(b0 + per, count_b);
   long long mine = 0;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
     }
   }
 
-  if (SPANS && a.alone && blockIdx.x == gridDim.x - 1) {  // (else done by what reads and joins the parts)
+  if (SPANS == kShared && a.alone && blockIdx.x == gridDim.x - 1) {  // (else done by what reads and joins the parts)
     for (int b = tid; b < a.B; b += kThreads) check_group_of(a, b);
     for (int v = 0; v < a.groups; ++v) check_prefix_pages(a, v, tid, kThreads);
   }
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         st.l.x += __shfl_xor_sync(0xffffffffu, st.l.x, d);
         st.l.y += __shfl_xor_sync(0xffffffffu, st.l.y, d);
       }
-      if (SPANS && whole && at.r.kind != kSpanWhole) {
+      if (SPANS == kShared && whole && at.r.kind != kSpanWhole) {
         // to be joined with the other part of its rows
         const PartRows to(a, at.r.kind);
 #pragma unroll
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         for (int j = 0; j < 2; ++j) {
           const long long off = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.ldo);
           if (off < 0) continue;
-          if (SPANS && a.groups && !a.alone && g == 0)
+          if (SPANS == kShared && !a.alone && g == 0)
             a.part_ml[0][column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D) / D] = kv_row_done();
           const float l = j ? st.l.y : st.l.x;
           const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
 #pragma unroll
       for (int i = 0; i < VL; i += 2)
         *reinterpret_cast<float2*>(dst + 2 * kCols + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
-    } else if (SPANS && gi.kind != kSpanWhole) {
+    } else if (SPANS == kShared && gi.kind != kSpanWhole) {
       const int G = a.group, token = a.token_of(gi.first_col + c);
       const PartRows to(a, gi.kind);
       const size_t row = static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         *reinterpret_cast<float2*>(to.o + row * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
-      if (SPANS && a.groups && !a.alone && lane == 0)
+      if (SPANS == kShared && !a.alone && lane == 0)
         a.part_ml[0][static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G] =
             kv_row_done();
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
   }
 }
 
-template <int D, bool SPANS>
+template <int D, Spans SPANS>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   constexpr int smem = kWarps * kStages * 2 * kv_block_bytes(D);
   static int limit[kAttrDevices] = {};
@@ -830,9 +830,12 @@ size_t kv_attend_workspace_floats(int num_sms, int D) {
   return ctas * 2 * (1 + kWarps) * (D == 128 ? piece_floats<128>() : piece_floats<64>());
 }
 
-cudaError_t launch_kv_attend(const KvAttendArgs& a, bool spans, cudaStream_t stream) {
-  if (spans) return a.pages.D == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
-  return a.pages.D == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
+template <int D>
+static cudaError_t launch_spans(const KvAttendArgs& a, cudaStream_t stream) {
+  return a.groups ? launch<D, kShared>(a, stream) : a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
+}
+cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream) {
+  return a.pages.D == 128 ? launch_spans<128>(a, stream) : launch_spans<64>(a, stream);
 }
 
 }  // namespace lora

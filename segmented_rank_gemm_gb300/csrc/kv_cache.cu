@@ -441,9 +441,9 @@ int attend_args(lora_kv_cache* c, KvAttendArgs& a, const void* q, int ldq, int q
   return LORA_OK;
 }
 
-int launch_attention(lora_kv_cache* c, const KvAttendArgs& a, bool spans, void* stream) {
-  KV_CUDA(c, launch_kv_attend(a, spans, static_cast<cudaStream_t>(stream)));
-  if (a.many_follow) KV_CUDA(c, launch_kv_prompt(a, spans, static_cast<cudaStream_t>(stream)));
+int launch_attention(lora_kv_cache* c, const KvAttendArgs& a, void* stream) {
+  KV_CUDA(c, launch_kv_attend(a, static_cast<cudaStream_t>(stream)));
+  if (a.many_follow) KV_CUDA(c, launch_kv_prompt(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;
 }
 
@@ -461,7 +461,7 @@ int lora_kv_attend(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, cons
   KvAttendArgs a;
   const int rc = attend_args(c, a, q, ldq, q_heads, q_offsets, kv_len, block_table, max_blocks, B, T, max_q,
                              scale, out, ldo);
-  return rc != LORA_OK || a.T == 0 ? rc : launch_attention(c, a, false, stream);
+  return rc != LORA_OK || a.T == 0 ? rc : launch_attention(c, a, stream);
 }
 
 int lora_kv_attend_cross(lora_kv_cache_t* c, const void* q, int ldq, int q_heads, const int32_t* q_offsets,
@@ -473,7 +473,7 @@ int lora_kv_attend_cross(lora_kv_cache_t* c, const void* q, int ldq, int q_heads
                              scale, out, ldo);
   if (rc != LORA_OK || a.T == 0) return rc;
   a.causal = 0;
-  return launch_attention(c, a, true, stream);
+  return launch_attention(c, a, stream);
 }
 
 int64_t lora_kv_shared_workspace(const lora_kv_cache_t* c, int T, int q_heads) {
@@ -521,11 +521,11 @@ int lora_kv_attend_shared(lora_kv_cache_t* c, const void* q, int ldq, int q_head
   const long long tiles = (static_cast<long long>(max_blocks) << c->pages.page_shift) / 32 + 1;
   if (!a.many_follow && (static_cast<long long>(T) * a.group / 8 + B) * c->pages.heads * tiles <= kAloneTiles * 16ll * c->num_sms) {
     a.alone = 1;
-    return launch_attention(c, a, true, stream);
+    return launch_attention(c, a, stream);
   }
   // (a group's rows are many where its requests' are not)
   a.many_follow = static_cast<long long>(T) * a.group > kFewRows;
-  rc = launch_attention(c, a, true, stream);
+  rc = launch_attention(c, a, stream);
   if (rc != LORA_OK) return rc;
   KV_CUDA(c, launch_kv_share_join(a, static_cast<cudaStream_t>(stream)));
   return LORA_OK;

@@ -110,7 +110,7 @@ struct KvAttendArgs {
   int32_t* err;
   int num_sms;
   // What the kernels' span variants (kv_span.cuh) read besides.
-  int causal;  // 0: a row sees everything its request has cached
+  int causal;  // 0: a row sees everything its request has cached (no groups then)
   const int32_t *group_offsets, *prefix_row, *prefix_len;  // [groups + 1], [groups], [groups] (or null)
   const int32_t* shared;  // [B] (or null)
   int groups;
@@ -125,11 +125,10 @@ constexpr int kKvMaxCtas = 1024;
 
 // Floats of the partial results' workspace.
 size_t kv_attend_workspace_floats(int num_sms, int D);
-// spans: the variant over kv_span.cuh's spans instead of whole causal requests.
-cudaError_t launch_kv_attend(const KvAttendArgs& a, bool spans, cudaStream_t stream);
+cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream);
 // The kernel for requests of many rows (kv_prompt.cu); it leaves the other rows alone.
 size_t kv_prompt_workspace_floats(int num_sms, int D);
-cudaError_t launch_kv_prompt(const KvAttendArgs& a, bool spans, cudaStream_t stream);
+cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream);
 struct KvRotateArgs {
   KvPages pages;
   const void *q, *k, *v;

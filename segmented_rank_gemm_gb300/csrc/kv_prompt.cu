@@ -146,13 +146,13 @@ struct Request {
 
 // Request b; one that is not for this kernel has 0 rows.  (Bad ones are reported by the other
 // kernel, which runs on every call.)
-template <bool SPANS>
+template <Spans SPANS>
 __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b) {
   Request r;
-  if constexpr (SPANS) {
-    const Span s = load_span(a, b, false);
+  if constexpr (SPANS != kRequests) {
+    const Span s = load_span<SPANS>(a, b, false);
     r = Request{s.row0, s.q_len, s.kv, s.q_len * a.group, 0, s.first, s.see, s.slope, s.table_row, s.kind};
-    if (r.rows <= a.few_rows) r.rows = 0;
+    if (span_is_few(a, s)) r.rows = 0;
     r.parts = (r.rows + kRows - 1) / kRows;
     return r;
   }
@@ -216,7 +216,7 @@ __device__ __forceinline__ int2 bucket_parts(const KvAttendArgs& a, const Reques
 }
 
 // A position in the sequence of tiles, and the tile's unit.
-template <bool SPANS>
+template <Spans SPANS>
 struct Cursor {
   Request r;
   int b, head, part, tile, tiles;
@@ -277,7 +277,7 @@ struct Cursor {
 
 // A CTA's range of the sequence, walked a segment (one group's tiles tile .. tile + count - 1) at a
 // time.
-template <bool SPANS>
+template <Spans SPANS>
 struct Walk {
   Cursor<SPANS> at;
   long long end;
@@ -347,7 +347,7 @@ struct Barriers {
   uint64_t meet, idle[3];                              // (256) (commit)
 };
 
-template <int D, bool SPANS>
+template <int D, Spans SPANS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) {
   using L = Smem<D>;
   extern __shared__ uint8_t raw[];
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   // The sequence's length and this CTA's cuts.  A thread sums a run of consecutive requests; those
   // with many groups are summed by its warp, one after the other (16 requests of 7 groups each, which
   // are one warp's, took 4 us longer when a thread summed 4 groups at most).
-  const int count_b = SPANS ? a.B + a.groups : a.B;
+  const int count_b = SPANS == kShared ? a.B + a.groups : a.B;
   const int per = (count_b + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, count_b), b1 = min(b0 + per, count_b);
   int most = 0;  // tiles of the largest group
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       const int k = __ffs(big) - 1;
       Request x;
       x.see = __shfl_sync(0xffffffffu, r.see, k);
-      x.slope = SPANS ? __shfl_sync(0xffffffffu, r.slope, k) : 1;
+      x.slope = SPANS != kRequests ? __shfl_sync(0xffffffffu, r.slope, k) : 1;
       x.rows = __shfl_sync(0xffffffffu, r.rows, k);
       x.parts = __shfl_sync(0xffffffffu, r.parts, k);
       const long long sum = head_units(a, x, lane);
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
     most = max(most, warp_most[w]);
   }
   const long long span = max(static_cast<long long>(kSetup + 4), quotient(total + gridDim.x - 1, gridDim.x));
-  const bool later = SPANS && a.groups > 0;  // pieces of rows in two parts are joined with those
+  const bool later = SPANS == kShared;  // pieces of rows in two parts are joined with those
   const int snap = snap_of(span, later);
   // Whole groups, claimed one by one, unless the largest would outlast the rest by more than its
   // cutting costs.
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (active) {
         // the last position this row sees, from the segment's first tile on (a row past the
         // last is written nowhere)
-        const int lim = g.see + (SPANS ? g.slope : 1) * a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) -
+        const int lim = g.see + (SPANS != kRequests ? g.slope : 1) * a.token_of(g.first_row + min(half * 128 + row, g.rows - 1)) -
                         g.tile * kTile;
         uint32_t at = (step + half) % 3;  // S's place
         for (int j = 0; j < g.count; ++j, ++n) {
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (active) {
         // 128 bytes of every row at a time, from one row a lane to 8 lanes a row
         // (raw: fp32 as it is, to a piece or to be joined with the other part of its rows)
-        const bool part = SPANS && whole && g.kind != kSpanWhole, raw = !whole || part;
+        const bool part = SPANS == kShared && whole && g.kind != kSpanWhole, raw = !whole || part;
         const float f = raw ? 1.f : l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
         const float2 by = make_float2(f, f), none = make_float2(0.f, 0.f);
         const auto at = [&](int x, int k) {  // 16-byte piece k of row x
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           piece[kRows + half * 128 + row] = l;
         }
         // (a group that is cut names its pieces for each of its rows, in the CTA with the first one)
-        if (SPANS && a.groups && (whole || g.tile == 0) && half * 128 + row < g.rows) {
+        if (SPANS == kShared && (whole || g.tile == 0) && half * 128 + row < g.rows) {
           const int c = g.first_row + half * 128 + row, token = a.token_of(c);
           const int first_cut = whole ? 0 : static_cast<int>(quotient(g.unit + snap, span)) + 1;
           const int last_cut = whole ? 0 : static_cast<int>(quotient(g.unit + g.tiles - snap + span - 1, span)) - 1;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
                                    : KvPieces(first_cut, last_cut - first_cut + 2, half * 128 + row).packed();
         }
       }
-      if (!whole && (!SPANS || g.kind == kSpanWhole)) {
+      if (!whole && (SPANS != kShared || g.kind == kSpanWhole)) {
         // The cuts within the group, as their CTAs see them, and the pieces between them: the
         // first cut's CTA before it (piece 1), then pieces 0.
         const int first_cut = static_cast<int>(quotient(g.unit + snap, span)) + 1;
@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
   griddep_wait();
 }
 
-template <int D, bool SPANS>
+template <int D, Spans SPANS>
 cudaError_t launch(const KvAttendArgs& a, cudaStream_t stream) {
   static int limit[kAttrDevices] = {};
   cudaError_t e = ensure_smem_limit(kv_prompt_kernel<D, SPANS>, Smem<D>::kBytes, limit);
@@ -1177,9 +1177,12 @@ size_t kv_prompt_workspace_floats(int num_sms, int D) {
          (D == 128 ? piece_floats<128>() : piece_floats<64>());
 }
 
-cudaError_t launch_kv_prompt(const KvAttendArgs& a, bool spans, cudaStream_t stream) {
-  if (spans) return a.pages.D == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
-  return a.pages.D == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
+template <int D>
+static cudaError_t launch_spans(const KvAttendArgs& a, cudaStream_t stream) {
+  return a.groups ? launch<D, kShared>(a, stream) : a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
+}
+cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream) {
+  return a.pages.D == 128 ? launch_spans<128>(a, stream) : launch_spans<64>(a, stream);
 }
 
 }  // namespace lora

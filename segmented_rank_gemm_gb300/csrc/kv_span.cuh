@@ -17,6 +17,12 @@
 
 namespace lora {
 
+// What a variant of the attention kernels runs over.
+enum Spans {
+  kRequests = 0,  // whole causal requests
+  kEncoder = 1,   // requests whose rows see all of them
+  kShared = 2     // groups' prefixes and requests
+};
 enum SpanKind { kSpanWhole = 0, kSpanTail = 1, kSpanPrefix = 2 };
 
 struct Span {
@@ -27,12 +33,13 @@ struct Span {
   SpanKind kind;
 };
 
-// Span v of a call's groups + B, checked.
+// Span v of a call's groups + B (or B), checked.
+template <Spans S>
 __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool report) {
   Span s;
   const int cap = a.max_blocks << a.pages.page_shift, in_page = (1 << a.pages.page_shift) - 1;
   bool bad;
-  if (v < a.groups) {
+  if (S == kShared && v < a.groups) {
     int from = load_in_order(a.group_offsets + v), to = load_in_order(a.group_offsets + v + 1);
     bad = from < 0 || to < from || to > a.B;
     s.table_row = load_in_order(a.prefix_row + v);
@@ -49,11 +56,11 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     s.slope = 0;
     s.kind = kSpanPrefix;
   } else {
-    const int b = v - a.groups;
+    const int b = S == kShared ? v - a.groups : v;
     s.row0 = load_in_order(a.q_offsets + b);
     const int end = load_in_order(a.q_offsets + b + 1);
     s.kv = load_in_order(a.kv_len + b);
-    const int share = a.groups ? load_in_order(a.shared + b) : 0;
+    const int share = S == kShared ? load_in_order(a.shared + b) : 0;
     // (in this order: the difference of any two offsets need not be an int)
     bad = s.row0 < 0 || end < s.row0 || end > a.T || end - s.row0 > a.max_q;
     s.q_len = bad ? 0 : end - s.row0;
@@ -64,13 +71,27 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     // every row of a request sees all of its group's prefix, whose pages are whole
     bad = bad || (s.q_len > 0 && (share < 0 || (share & in_page) || share > max(0, s.kv - s.q_len)));
     s.first = a.alone ? 0 : min(max(share, 0), s.kv) & ~in_page;
-    s.see = (a.causal ? s.kv - s.q_len : s.kv - 1) - s.first;
-    s.slope = a.causal ? 1 : 0;
+    s.see = (S == kShared ? s.kv - s.q_len : s.kv - 1) - s.first;
+    s.slope = S == kShared ? 1 : 0;
     s.table_row = b;
     s.kind = s.first > 0 ? kSpanTail : kSpanWhole;
   }
   if (bad && report) atomicOr(a.err, LORA_ERRF_BAD_ID);
   return s;
+}
+
+// Whether a span is the kernel for few rows' (kv_attend.cu), which costs by 8 rows and 32 positions and
+// has little to set up, or the one for many's (kv_prompt.cu), where a change of groups costs as much as
+// six tiles of 64.  A part of rows with two spans is the first one's also with more rows than a.few_rows
+// as long as it is short, by what either kernel's units were measured to cost (24 rows over 1024
+// positions are even): up to 32 rows 12 tiles of 32 positions, up to 40 6, 48 4, 56 3 and 64 2.  61 requests
+// of 4 to 7 tokens behind shared prefixes take 72.4 us by rows alone, 67.4 so.  (A span that is all of its
+// request goes by rows alone, as in lora_kv_attend, and gives the same bits.)
+__device__ __forceinline__ bool span_is_few(const KvAttendArgs& a, const Span& s) {
+  const int rows = s.q_len * a.group;
+  if (rows <= a.few_rows) return true;
+  if (s.kind == kSpanWhole || rows > 64) return false;
+  return s.kv - s.first <= 32 * (0x2346C >> (rows + 7 & ~7) / 2 - 16 & 15);
 }
 
 // The groups agree with their requests: one with a prefix is a member, and has its group's.
@@ -91,7 +112,7 @@ __device__ __forceinline__ void check_group_of(const KvAttendArgs& a, int b) {
 
 // The pages of group v's prefix are the cache's.
 __device__ __forceinline__ void check_prefix_pages(const KvAttendArgs& a, int v, int first, int step) {
-  const Span s = load_span(a, v, false);
+  const Span s = load_span<kShared>(a, v, false);
   for (int j = first; j < s.kv >> a.pages.page_shift; j += step)
     if (static_cast<unsigned>(load_in_order(a.table + static_cast<size_t>(s.table_row) * a.max_blocks + j)) >=
         static_cast<unsigned>(a.pages.num_pages))
