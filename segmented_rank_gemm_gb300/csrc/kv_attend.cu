@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
     }
   }
 
-  if (SPANS == kShared && a.alone && blockIdx.x == gridDim.x - 1) {  // (else done by what reads and joins the parts)
+  if (SPANS == kAlone && blockIdx.x == gridDim.x - 1) {  // (else done by what reads and joins the parts)
     for (int b = tid; b < a.B; b += kThreads) check_group_of(a, b);
     for (int v = 0; v < a.groups; ++v) check_prefix_pages(a, v, tid, kThreads);
   }
@@ -620,14 +620,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         st.l.x += __shfl_xor_sync(0xffffffffu, st.l.x, d);
         st.l.y += __shfl_xor_sync(0xffffffffu, st.l.y, d);
       }
-      if (SPANS == kShared && whole && at.r.kind != kSpanWhole) {
-        // to be joined with the other part of its rows
+      if (SPANS == kShared && whole) {  // to be joined with the other part of its rows
         const PartRows to(a, at.r.kind);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const long long row = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D);
           if (row < 0) continue;
-          if (g == 0) to.ml[row / D] = make_float2(-(j ? st.minus.y : st.minus.x), j ? st.l.y : st.l.x);
+          if (g == 0) to.put(a, row / D, -(j ? st.minus.y : st.minus.x), j ? st.l.y : st.l.x);
           float* o = to.o + row + g * LD;
 #pragma unroll
           for (int m = 0; m < KT; m += 2)
@@ -640,8 +639,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         for (int j = 0; j < 2; ++j) {
           const long long off = column_offset(a, at.r, at.head, at.col, 2 * t + j, a.ldo);
           if (off < 0) continue;
-          if (SPANS == kShared && !a.alone && g == 0)
-            a.part_ml[0][column_offset(a, at.r, at.head, at.col, 2 * t + j, a.q_heads * D) / D] = kv_row_done();
           const float l = j ? st.l.y : st.l.x;
           const float f = l == 0.f ? 0.f : back / l, f16 = f * 0x1p-4f;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + g * LD);
@@ -734,19 +731,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
 #pragma unroll
       for (int i = 0; i < VL; i += 2)
         *reinterpret_cast<float2*>(dst + 2 * kCols + c * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
-    } else if (SPANS == kShared && gi.kind != kSpanWhole) {
+    } else if (SPANS == kShared) {
       const int G = a.group, token = a.token_of(gi.first_col + c);
       const PartRows to(a, gi.kind);
       const size_t row = static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G;
-      if (lane == 0) to.ml[row] = make_float2(m, l);
+      if (lane == 0) to.put(a, row, m, l);
 #pragma unroll
       for (int i = 0; i < VL; i += 2)
         *reinterpret_cast<float2*>(to.o + row * D + lane * VL + i) = make_float2(o[i], o[i + 1]);
     } else {
       const int G = a.group, token = a.token_of(gi.first_col + c);
-      if (SPANS == kShared && !a.alone && lane == 0)
-        a.part_ml[0][static_cast<size_t>(gi.row0 + token) * a.q_heads + gi.head * G + gi.first_col + c - token * G] =
-            kv_row_done();
       const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
       uint32_t* out = reinterpret_cast<uint32_t*>(
           static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(gi.row0 + token) * a.ldo +
@@ -832,7 +826,7 @@ size_t kv_attend_workspace_floats(int num_sms, int D) {
 
 template <int D>
 static cudaError_t launch_spans(const KvAttendArgs& a, cudaStream_t stream) {
-  return a.groups ? launch<D, kShared>(a, stream) : a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
+  return a.alone ? launch<D, kAlone>(a, stream) : a.groups ? launch<D, kShared>(a, stream) : a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
 }
 cudaError_t launch_kv_attend(const KvAttendArgs& a, cudaStream_t stream) {
   return a.pages.D == 128 ? launch_spans<128>(a, stream) : launch_spans<64>(a, stream);

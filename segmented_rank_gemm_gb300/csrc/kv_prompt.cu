@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
       if (active) {
         // 128 bytes of every row at a time, from one row a lane to 8 lanes a row
         // (raw: fp32 as it is, to a piece or to be joined with the other part of its rows)
-        const bool part = SPANS == kShared && whole && g.kind != kSpanWhole, raw = !whole || part;
+        const bool part = SPANS == kShared && whole, raw = SPANS == kShared || !whole;
         const float f = raw ? 1.f : l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
         const float2 by = make_float2(f, f), none = make_float2(0.f, 0.f);
         const auto at = [&](int x, int k) {  // 16-byte piece k of row x
@@ -681,13 +681,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
           const int c = g.first_row + half * 128 + row, token = a.token_of(c);
           const int first_cut = whole ? 0 : static_cast<int>(quotient(g.unit + snap, span)) + 1;
           const int last_cut = whole ? 0 : static_cast<int>(quotient(g.unit + g.tiles - snap + span - 1, span)) - 1;
-          to.ml[first_row + static_cast<size_t>(token - first_token) * a.q_heads + c - token * G] =
-              g.kind == kSpanWhole ? kv_row_done()
-              : whole              ? make_float2(m, l)
-                                   : KvPieces(first_cut, last_cut - first_cut + 2, half * 128 + row).packed();
+          const size_t at_row = first_row + static_cast<size_t>(token - first_token) * a.q_heads + c - token * G;
+          if (whole) to.put(a, at_row, m, l);
+          else to.ml[at_row] = KvPieces(first_cut, last_cut - first_cut + 2, half * 128 + row).packed(to.all);
         }
       }
-      if (!whole && (SPANS != kShared || g.kind == kSpanWhole)) {
+      if (SPANS != kShared && !whole) {
         // The cuts within the group, as their CTAs see them, and the pieces between them: the
         // first cut's CTA before it (piece 1), then pieces 0.
         const int first_cut = static_cast<int>(quotient(g.unit + snap, span)) + 1;

@@ -95,12 +95,20 @@ __global__ void __launch_bounds__(kThreads) kv_share_join_kernel(KvAttendArgs a,
   float o0[VL], o1[VL];
   load_o<VL>(a.part_o[0] + at * D + lane * VL, o0);
   load_o<VL>(a.part_o[1] + at * D + lane * VL, o1);
-  if (row < lo || row >= hi || kv_is_row_done(ml0)) return;
+  if (row < lo || row >= hi) return;
+  const bool one = kv_is_row_times(ml0) || KvPieces::only(ml0);
   if (KvPieces::are(ml0)) ml0 = join_pieces<D>(a, KvPieces(ml0), lane, o0);
-  if (KvPieces::are(ml1)) ml1 = join_pieces<D>(a, KvPieces(ml1), lane, o1);
-  const float m = fmaxf(ml0.x, ml1.x), w0 = ex2(ml0.x - m), w1 = ex2(ml1.x - m);
-  const float l = w0 * ml0.y + w1 * ml1.y;
-  const float f = l == 0.f ? 0.f : kKvUnit * a.v_scale / l, f0 = w0 * f, f1 = w1 * f;
+  float f0, f1 = 0.f;
+  if (one) {
+    f0 = kv_is_row_times(ml0) ? ml0.x : kv_factor(a, ml0.y);
+#pragma unroll
+    for (int k = 0; k < VL; ++k) o1[k] = 0.f;
+  } else {
+    if (KvPieces::are(ml1)) ml1 = join_pieces<D>(a, KvPieces(ml1), lane, o1);
+    const float m = fmaxf(ml0.x, ml1.x), w0 = ex2(ml0.x - m), w1 = ex2(ml1.x - m);
+    const float f = kv_factor(a, w0 * ml0.y + w1 * ml1.y);
+    f0 = w0 * f, f1 = w1 * f;
+  }
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(row) * a.ldo +
                                               head * D + lane * VL);
 #pragma unroll

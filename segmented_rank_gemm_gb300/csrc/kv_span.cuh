@@ -21,7 +21,8 @@ namespace lora {
 enum Spans {
   kRequests = 0,  // whole causal requests
   kEncoder = 1,   // requests whose rows see all of them
-  kShared = 2     // groups' prefixes and requests
+  kShared = 2,    // groups' prefixes and requests, whose results are joined
+  kAlone = 3      // whole causal requests, with groups that are checked but not used
 };
 enum SpanKind { kSpanWhole = 0, kSpanTail = 1, kSpanPrefix = 2 };
 
@@ -49,7 +50,7 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     s.row0 = load_in_order(a.q_offsets + from);
     const int end = load_in_order(a.q_offsets + to);
     bad = bad || s.row0 < 0 || end < s.row0 || end > a.T;
-    s.q_len = bad || s.kv == 0 || a.alone ? 0 : end - s.row0;
+    s.q_len = bad || s.kv == 0 ? 0 : end - s.row0;
     if (bad) s.kv = s.table_row = 0;
     s.first = 0;
     s.see = s.kv - 1;
@@ -60,7 +61,7 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     s.row0 = load_in_order(a.q_offsets + b);
     const int end = load_in_order(a.q_offsets + b + 1);
     s.kv = load_in_order(a.kv_len + b);
-    const int share = S == kShared ? load_in_order(a.shared + b) : 0;
+    const int share = S != kEncoder ? load_in_order(a.shared + b) : 0;
     // (in this order: the difference of any two offsets need not be an int)
     bad = s.row0 < 0 || end < s.row0 || end > a.T || end - s.row0 > a.max_q;
     s.q_len = bad ? 0 : end - s.row0;
@@ -70,9 +71,9 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
     }
     // every row of a request sees all of its group's prefix, whose pages are whole
     bad = bad || (s.q_len > 0 && (share < 0 || (share & in_page) || share > max(0, s.kv - s.q_len)));
-    s.first = a.alone ? 0 : min(max(share, 0), s.kv) & ~in_page;
-    s.see = (S == kShared ? s.kv - s.q_len : s.kv - 1) - s.first;
-    s.slope = S == kShared ? 1 : 0;
+    s.first = S == kAlone ? 0 : min(max(share, 0), s.kv) & ~in_page;
+    s.see = (S != kEncoder ? s.kv - s.q_len : s.kv - 1) - s.first;
+    s.slope = S != kEncoder ? 1 : 0;
     s.table_row = b;
     s.kind = s.first > 0 ? kSpanTail : kSpanWhole;
   }
@@ -110,9 +111,9 @@ __device__ __forceinline__ void check_group_of(const KvAttendArgs& a, int b) {
     atomicOr(a.err, LORA_ERRF_BAD_ID);
 }
 
-// The pages of group v's prefix are the cache's.
+// Group v is as it should be, and its prefix's pages are the cache's.
 __device__ __forceinline__ void check_prefix_pages(const KvAttendArgs& a, int v, int first, int step) {
-  const Span s = load_span<kShared>(a, v, false);
+  const Span s = load_span<kShared>(a, v, true);
   for (int j = first; j < s.kv >> a.pages.page_shift; j += step)
     if (static_cast<unsigned>(load_in_order(a.table + static_cast<size_t>(s.table_row) * a.max_blocks + j)) >=
         static_cast<unsigned>(a.pages.num_pages))
@@ -126,7 +127,8 @@ __host__ __device__ constexpr int kv_prompt_piece_floats(int D) { return kKvProm
 __host__ __device__ constexpr int kv_prompt_piece(int first_cut, int i) {
   return i == 0 ? (first_cut - 1) * 2 + 1 : (first_cut + i - 1) * 2;
 }
-// In the place of a row's (m, l): its group's result is `count` pieces, where it is row `row`.
+// In the place of a row's (m, l), told apart by l (a sum is not negative): its group's result is `count`
+// pieces, where it is row `row`; with `only`, there is no other part of the row.
 struct KvPieces {
   int first_cut, count, row;
   __device__ __forceinline__ KvPieces(int first_cut_, int count_, int row_)
@@ -135,22 +137,31 @@ struct KvPieces {
     const uint32_t v = __float_as_uint(ml.x);
     first_cut = v >> 21, count = v >> 10 & 0x7FF, row = v & 0x3FF;
   }
-  static __device__ __forceinline__ bool are(float2 ml) { return ml.y == -1.f; }  // (a sum is not negative)
-  __device__ __forceinline__ float2 packed() const {
-    return make_float2(__uint_as_float(static_cast<uint32_t>(first_cut) << 21 | count << 10 | row), -1.f);
+  static __device__ __forceinline__ bool are(float2 ml) { return ml.y == -1.f || ml.y == -2.f; }
+  static __device__ __forceinline__ bool only(float2 ml) { return ml.y == -2.f; }
+  __device__ __forceinline__ float2 packed(bool only) const {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(first_cut) << 21 | count << 10 | row), only ? -2.f : -1.f);
   }
 };
-// In the place of a request's (m, l): its row has no second part and is written already.
-__device__ __forceinline__ float2 kv_row_done() { return make_float2(0.f, -2.f); }
-__device__ __forceinline__ bool kv_is_row_done(float2 ml) { return ml.y == -2.f; }
+// Or O is all of the row's result, and the output is it times f.
+__device__ __forceinline__ float2 kv_row_times(float f) { return make_float2(f, -3.f); }
+__device__ __forceinline__ bool kv_is_row_times(float2 ml) { return ml.y == -3.f; }
 static_assert(kKvMaxCtas < 1 << 11 && kKvPromptRows <= 1 << 10, "what KvPieces holds");
 
+// A result's factor: what O times is the output.
+__device__ __forceinline__ float kv_factor(const KvAttendArgs& a, float l) {
+  return l == 0.f ? 0.f : kKvUnit * a.v_scale / l;
+}
 // Where a span's unnormalised results go: row r's head h at index r q_heads + h.
 struct PartRows {
   float* o;    // [.][D]
   float2* ml;  // m, l
   __device__ __forceinline__ PartRows(const KvAttendArgs& a, SpanKind kind)
-      : o(a.part_o[kind == kSpanPrefix]), ml(a.part_ml[kind == kSpanPrefix]) {}
+      : o(a.part_o[kind == kSpanPrefix]), ml(a.part_ml[kind == kSpanPrefix]), all(kind == kSpanWhole) {}
+  bool all;  // the span is all of its rows
+  __device__ __forceinline__ void put(const KvAttendArgs& a, size_t row, float m, float l) const {
+    ml[row] = all ? kv_row_times(kv_factor(a, l)) : make_float2(m, l);
+  }
 };
 
 }  // namespace lora
