@@ -1178,7 +1178,8 @@ size_t kv_prompt_workspace_floats(int num_sms, int D) {
 
 template <int D>
 static cudaError_t launch_spans(const KvAttendArgs& a, cudaStream_t stream) {
-  return a.groups ? launch<D, kShared>(a, stream) : a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
+  if (a.groups) return launch<D, kShared>(a, stream);
+  return a.causal ? launch<D, kRequests>(a, stream) : launch<D, kEncoder>(a, stream);
 }
 cudaError_t launch_kv_prompt(const KvAttendArgs& a, cudaStream_t stream) {
   return a.pages.D == 128 ? launch_spans<128>(a, stream) : launch_spans<64>(a, stream);
