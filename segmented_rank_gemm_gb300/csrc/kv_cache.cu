@@ -517,7 +517,7 @@ int lora_kv_attend_shared(lora_kv_cache_t* c, const void* q, int ldq, int q_head
   }
   // Where the batch is so small that every warp has at most kAloneTiles tiles, however long its requests
   // are, they are attended by themselves: sharing spares work that nothing waits for, and joining costs
-  // a launch (4 requests of 1056 positions, 1024 of them shared: 17.3 us joined, 16.1 alone).
+  // a launch (4 requests of 1056 positions, 1024 of them shared: 17.3 us joined, 15.5 alone).
   const long long tiles = (static_cast<long long>(max_blocks) << c->pages.page_shift) / 32 + 1;
   if (!a.many_follow && (static_cast<long long>(T) * a.group / 8 + B) * c->pages.heads * tiles <= kAloneTiles * 16ll * c->num_sms) {
     a.alone = 1;

@@ -86,7 +86,8 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
 // six tiles of 64.  A part of rows with two spans is the first one's also with more rows than a.few_rows
 // as long as it is short, by what either kernel's units were measured to cost (24 rows over 1024
 // positions are even): up to 32 rows 12 tiles of 32 positions, up to 40 6, 48 4, 56 3 and 64 2.  61 requests
-// of 4 to 7 tokens behind shared prefixes take 72.4 us by rows alone, 67.4 so.  (A span that is all of its
+// of 4 to 7 tokens behind shared prefixes take 72.7 us by rows alone, 67.2 so; 512
+// single tokens, whose spans the rule does not move, 91.4 and 92.1.  (A span that is all of its
 // request goes by rows alone, as in lora_kv_attend, and gives the same bits.)
 __device__ __forceinline__ bool span_is_few(const KvAttendArgs& a, const Span& s) {
   const int rows = s.q_len * a.group;
