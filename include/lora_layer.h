@@ -233,7 +233,8 @@ int lora_forward_e4m3(lora_layer_t* layer, const void* x_dev, const void* xq_dev
  *   factor, residual  T rows of N bf16, ldf and ldr elements apart (multiples of 8 from N up).  Each
  *                   may be y itself (the same address and ld = N), and else does not overlap it.
  * All 16-byte aligned.  GELU is x (1 + erf(x / sqrt 2)) / 2, GELU_TANH its approximation
- * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2, SILU x / (1 + e^-x).
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2, SILU x / (1 + e^-x).  An infinite sum gives what
+ * these say: +inf for +inf in each, and for -inf 0 in RELU and NaN in GELU, GELU_TANH and SILU.
  */
 enum lora_activation { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3,
                        LORA_ACT_SILU = 4 };

@@ -201,12 +201,15 @@ __device__ __forceinline__ float2 over_one_plus_exp2(float2 x, float2 u) {
   return mul2(x, rcp_of(add2(exp2_of(u), splat(1.f))));
 }
 constexpr float kLog2E = 1.44269504088896341f;
-// x Phi(x) by Phi(-|x|) = erfc(z) / 2, z = |x| / sqrt 2, and the Chebyshev fit erfc(z) = t e^(-z^2 + P(t)),
-// t = 1 / (1 + z / 2), of relative error below 1.2e-7 for all z (Press, Teukolsky, Vetterling, Flannery,
-// Numerical Recipes, section 6.2): no branch, and exact in the tails.
+// x Phi(x) = max(x, 0) - |x| Phi(-|x|), with Phi(-|x|) = erfc(z) / 2, z = |x| / sqrt 2, and the Chebyshev fit
+// erfc(z) = t e^(-z^2 + P(t)), t = 1 / (1 + z / 2), of relative error below 1.2e-7 for all z (Press, Teukolsky,
+// Vetterling, Flannery, Numerical Recipes, section 6.2): no branch.  The exponent is rounded in fp32, some
+// 2^-24 of it, so that the tail's relative error grows with z^2, to below 2^-14 where Phi(-|x|) is still above
+// 2^-126; beyond (|x| > 13) it counts as 0.  |x| is bounded where that 0 is multiplied by it, for +inf to stay;
+// -inf is NaN by max(x, 0) = x / 2 + |x| / 2, as in the definition (-inf times 0).
 __device__ __forceinline__ float2 gelu(float2 x) {
-  const float2 z = mul2(make_float2(fabsf(x.x), fabsf(x.y)), splat(0.70710678118654752f));
-  const float2 t = rcp_of(fma2(z, splat(0.5f), splat(1.f)));
+  const float2 ax = make_float2(fabsf(x.x), fabsf(x.y));
+  const float2 t = rcp_of(fma2(ax, splat(0.35355339059327376f), splat(1.f)));
   float2 p = fma2(t, splat(0.17087277f), splat(-0.82215223f));
   p = fma2(t, p, splat(1.48851587f));
   p = fma2(t, p, splat(-1.13520398f));
@@ -216,10 +219,10 @@ __device__ __forceinline__ float2 gelu(float2 x) {
   p = fma2(t, p, splat(0.37409196f));
   p = fma2(t, p, splat(1.00002368f));
   p = fma2(t, p, splat(-1.26551223f));
-  p = fma2(make_float2(-z.x, -z.y), z, p);
-  const float2 below = mul2(mul2(t, splat(0.5f)), exp2_of(mul2(p, splat(kLog2E))));  // Phi(-|x|)
-  const float2 xb = mul2(x, below);
-  return make_float2(x.x > 0.f ? x.x - xb.x : xb.x, x.y > 0.f ? x.y - xb.y : xb.y);
+  p = fma2(x, mul2(x, splat(-0.5f)), p);
+  const float2 minus = mul2(mul2(t, splat(-0.5f)), exp2_of(mul2(p, splat(kLog2E))));  // -Phi(-|x|)
+  const float2 top = fma2(x, splat(0.5f), mul2(ax, splat(0.5f)));                     // max(x, 0)
+  return fma2(make_float2(fminf(ax.x, 0x1p64f), fminf(ax.y, 0x1p64f)), minus, top);
 }
 // x (1 + tanh u) / 2 = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
 __device__ __forceinline__ float2 gelu_tanh(float2 x) {
