@@ -20,6 +20,15 @@ from .lora import ACTIVATIONS, LoraLayer, empty, on_stream
 from .norm import lora_rms_norm
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the memory from the first to the last element of two arrays of rows meets."""
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + t.element_size() * (
+        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))) for t in (a, b))
+    return a0 < b1 and b0 < a1
+
+
 class AttentionBlock:
     """``q``, ``k``, ``v`` and ``o`` are LoraLayers: hidden -> q_heads head_dim,
     hidden -> kv_heads head_dim (k and v) and q_heads head_dim -> hidden, in bf16; q, k and v
@@ -147,20 +156,27 @@ class MlpBlock:
     def forward(self, x: torch.Tensor, h: torch.Tensor, token_slot: torch.Tensor, y=None,
                 residual: bool = False, stream=None) -> torch.Tensor:
         """x and the running residual ``h`` [T, hidden] (overwritten by h + x), and the rows' adapter
-        slots.  Returns y, or h + y with ``residual`` (y may then be h)."""
+        slots.  Returns y, or h + y with ``residual`` (y may then be h, and else does not overlap it)."""
         T = x.shape[0]
+        # (whatever can be refused is, before h changes; x and h by the norm)
         if T > self.max_tokens or token_slot.shape[0] < T:
             raise ValueError("more rows than max_tokens or than adapter slots")
+        ids = token_slot[:T]
+        if ids.dtype != torch.int32 or ids.device != x.device or ids.dim() != 1 or not ids.is_contiguous():
+            raise ValueError("token_slot must be a dense int32 tensor on x's device")
+        if residual and (h.data_ptr() % 16 or (h.dim() == 2 and T > 1 and h.stride(0) % 8)):
+            raise ValueError("the rows of a residual must be 16-byte aligned")
         if y is None:
             y = empty(x.shape, x.dtype, x.device, stream)
-        elif y.dtype != torch.bfloat16 or y.shape != (T, self.down.N) or not y.is_cuda \
-                or not y.is_contiguous():
-            raise ValueError("y must be a dense CUDA bf16 tensor of x's shape")
+        elif y.dtype != torch.bfloat16 or y.shape != (T, self.down.N) or y.device != x.device \
+                or not y.is_contiguous() or y.data_ptr() % 16:
+            raise ValueError("y must be a dense, 16-byte aligned bf16 tensor of x's shape on x's device")
+        elif _overlap(y, h) and not (residual and y.data_ptr() == h.data_ptr() and h.is_contiguous()):
+            raise ValueError("y and h overlap (y may be h itself in a pass with residual)")
         n, mid, nq, sn = self.n[:T], self.mid[:T], None, None
         if self.nq is not None:
             nq, sn = self.nq[:T], self.sn[:T]
         lora_rms_norm(x, self.norm_weight, self.eps, h, h, n, nq, sn, stream)
-        ids = token_slot[:T]
         for layer in (self.up, self.gate, self.down):
             layer.set_batch(ids, stream)
         self.up.forward_fused(n, mid, xq=nq, sx=sn, stream=stream)
