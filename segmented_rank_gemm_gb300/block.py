@@ -52,8 +52,9 @@ class AttentionBlock:
             raise ValueError("the projections must be bf16 layers")
         if not q.K == k.K == v.K or len({layer.fp8_base for layer in (q, k, v)}) != 1:
             raise ValueError("q, k and v must take the same rows")
-        if rotary is not None and (rotate is not None or rotary.rotary_dim > D):
-            raise ValueError("rotate or a rotary of at most the head's dimensions")
+        if rotary is not None and (rotate is not None or rotary.rotary_dim > D
+                                   or rotary.angles.device != norm_weight.device):
+            raise ValueError("rotate or a rotary of at most the head's dimensions, on the block's device")
         self.q, self.k, self.v, self.o = q, k, v, o
         self.norm_weight, self.cache, self.eps, self.rotate = norm_weight, cache, eps, rotate
         self.rotary = rotary
@@ -72,7 +73,8 @@ class AttentionBlock:
     def forward(self, x: torch.Tensor, h: torch.Tensor, pages: PageTable, max_q: int, y=None,
                 stream=None, groups=None) -> torch.Tensor:
         """x and the running residual ``h`` [T, hidden] (overwritten by h + x) of the batch that
-        ``pages.step`` mapped last; ``max_q`` bounds a request's new tokens.  Returns y.
+        ``pages.step`` mapped last; ``max_q`` bounds a request's new tokens.  Returns y, which does not
+        overlap h.
         ``groups``: (group_offsets, prefix_row, prefix_len) of ``KvCache.attend_shared``, whose
         members' prefixes are ``pages.shared_len``."""
         T = x.shape[0]
@@ -83,13 +85,17 @@ class AttentionBlock:
             raise ValueError("the page table does not fit the cache")
         if max_q < 1:
             raise ValueError("max_q must be positive")
-        if groups is not None and self.parts is None:
-            raise ValueError("groups need a block made with share")
+        if groups is not None:
+            if self.parts is None:
+                raise ValueError("groups need a block made with share")
+            self.cache.check_groups(pages.max_requests, *groups)
         if y is None:
             y = empty(x.shape, x.dtype, x.device, stream)
-        elif y.dtype != torch.bfloat16 or y.shape != (T, self.o.N) or not y.is_cuda \
-                or not y.is_contiguous():
-            raise ValueError("y must be a dense CUDA bf16 tensor of x's shape")
+        elif y.dtype != torch.bfloat16 or y.shape != (T, self.o.N) or y.device != x.device \
+                or not y.is_contiguous() or y.data_ptr() % 16:
+            raise ValueError("y must be a dense, 16-byte aligned bf16 tensor of x's shape on x's device")
+        elif _overlap(y, h):
+            raise ValueError("y and h overlap")
         n, nq, sn = self.n[:T], None, None
         if self.nq is not None:
             nq, sn = self.nq[:T], self.sn[:T]

@@ -293,6 +293,19 @@ class KvCache:
             _bad("tokens=%d, q_heads=%d" % (tokens, q_heads))
         return torch.empty(n, dtype=torch.uint8, device="cuda")
 
+    @staticmethod
+    def check_groups(requests: int, group_offsets, prefix_row=None, prefix_len=None):
+        """Refuses groups that ``attend_shared`` would for so many requests (the tensors themselves: what
+        they hold is checked on the GPU).  Their addresses, and their number."""
+        dev = torch.cuda.current_device()
+        if prefix_row is None or prefix_len is None:
+            _bad("groups are group_offsets, prefix_row and prefix_len")
+        groups = group_offsets.numel() - 1
+        if not 1 <= groups <= requests:
+            _bad("%d groups of %d requests" % (groups, requests))
+        return (_i32("group_offsets", group_offsets, 2, dev), _i32("prefix_row", prefix_row, groups, dev),
+                _i32("prefix_len", prefix_len, groups, dev), groups)
+
     def attend_shared(self, q, q_offsets, kv_len, block_table, max_q: int, group_offsets, prefix_row,
                       prefix_len, shared_len, scale: float = None, out=None, workspace=None,
                       stream=None):
@@ -301,18 +314,17 @@ class KvCache:
         ``group_offsets[g + 1] - 1``; the first ``shared_len[b]`` positions of a member are
         ``prefix_len[g]`` (whole pages, those in row ``prefix_row[g]`` of the table), or 0: it is
         attended by itself."""
-        B, dev, groups = kv_len.shape[0], torch.cuda.current_device(), group_offsets.shape[0] - 1
-        group_at = _i32("group_offsets", group_offsets, 2, dev)
-        prefix_at = _i32("prefix_row", prefix_row, groups, dev), _i32("prefix_len", prefix_len, groups, dev)
-        shared_at = _i32("shared_len", shared_len, B, dev)
+        B, dev = kv_len.shape[0], torch.cuda.current_device()
+        before = (*self.check_groups(B, group_offsets, prefix_row, prefix_len),
+                  _i32("shared_len", shared_len, B, dev))
         if workspace is None:
             n = _lib.lora_kv_shared_workspace(self.handle, q.shape[0], q.shape[1])
             workspace = empty((max(n, 0),), torch.uint8, q.device, stream)
         if workspace.get_device() != dev or not workspace.is_contiguous():
             _bad("workspace must be a contiguous tensor on the current CUDA device")
         return self._attend(_lib.lora_kv_attend_shared, q, q_offsets, kv_len, block_table, max_q, scale,
-                            out, stream, ((group_at, *prefix_at, groups, shared_at),
-                                          (workspace.data_ptr(), workspace.numel() * workspace.element_size())))
+                            out, stream,
+                            (before, (workspace.data_ptr(), workspace.numel() * workspace.element_size())))
 
     def status(self, stream=None) -> int:
         """LORA_OK, LORA_EID or LORA_ETIMEOUT since the last call (synchronises)."""

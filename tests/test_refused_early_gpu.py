@@ -62,3 +62,41 @@ def test_mlp_block_takes_strided_residual_rows():
     want = mlp.forward(x, dense, ids, residual=True)
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(h, dense) and not wide[:, HIDDEN:].any()
+
+
+def test_attention_block():
+    from segmented_rank_gemm_gb300.kv import KvCache, PageTable, Rotary
+    from segmented_rank_gemm_gb300.lora import LoraError
+    B, page = 3, 16
+    cache, pages = KvCache(12, page, KV, D, B), PageTable(12, page, B, 4, 8)
+    block = _attention(8, cache, share=True, rotary=Rotary(64, D))
+    pages.step(_ints([4, 2, 1]))
+    x, h = _rows(7, 1), _in_the_middle(7, 2)
+    before = h.clone()
+    good = (_ints([0, 2]), _ints([0]), _ints([0]))
+    odd = torch.empty(7 * HIDDEN + 8, dtype=BF16, device=DEV)[4:4 + 7 * HIDDEN].view(7, HIDDEN)
+    bad = [dict(groups=(g.long(), r, n)) for g, r, n in (good,)]
+    bad += [dict(groups=g) for g in (
+        (good[0].cpu(), *good[1:]), (good[0], good[1].long(), good[2]), (good[0], good[1], good[2].cpu()),
+        (_ints([0]), *good[1:]), (_ints([0, 1, 2, 3, 3]), _ints([0] * 4), _ints([0] * 4)),
+        (_ints([0, 1, 2]), *good[1:]), (good[0], good[1], good[2][:0]),
+        (_ints([0, 0, 2, 0])[::2], *good[1:]), good[:2])]
+    bad += [dict(y=_across(h)), dict(y=h), dict(y=odd), dict(y=torch.empty(7, HIDDEN, dtype=BF16))]
+    slots = torch.arange(12 * page, dtype=torch.int32, device=DEV)
+    for change in bad:
+        with pytest.raises((ValueError, LoraError)):
+            block.forward(x, h, pages, 4, **change)
+        torch.cuda.synchronize()
+        assert torch.equal(h, before), list(change)
+        k, v = cache.read(slots)
+        assert not k.any() and not v.any(), list(change)
+    block.forward(x, h, pages, 4, groups=good)
+    torch.cuda.synchronize()
+    assert not torch.equal(h, before) and cache.status() == 0
+
+
+def test_a_rotary_of_another_device():
+    from segmented_rank_gemm_gb300.kv import KvCache, Rotary
+    cache = KvCache(4, 16, KV, D, 2)
+    with pytest.raises(ValueError):
+        _attention(8, cache, rotary=Rotary(64, D, device="cpu"))
