@@ -104,8 +104,8 @@ int lora_kv_release(const int32_t* done_dev, int32_t* len_dev, int B, int page_s
  *   status_dev [1]  0, or 1 (a parent below -1, from B up or with a parent in the call, its length
  *                   negative or past max_blocks pages, a negative want_dev[b], or a request b that
  *                   holds something: its length must be 0); then nothing is changed.
- * The pages stay its parent's: they are valid
- * while the parent holds them, and lora_kv_release_shared returns only what lies behind them.
+ * The pages stay its parent's: lora_kv_release_shared returns only what lies behind them, and the
+ * parent's pages not before its children are released, or with them.
  * Errors: LORA_EINVAL, LORA_ECUDA.
  */
 int lora_kv_fork(const int32_t* parent_dev, const int32_t* want_dev, int32_t* len_dev,
@@ -115,7 +115,8 @@ int lora_kv_fork(const int32_t* parent_dev, const int32_t* want_dev, int32_t* le
 /*
  * lora_kv_release for requests that may have been forked: a request's first shared_dev[b] positions
  * are not its own, so the pages behind them alone go back; shared_dev[b] becomes 0 with len_dev[b].
- * status_dev is 1 also where shared_dev[b] is negative, not whole pages or above len_dev[b].
+ * status_dev is 1 also where shared_dev[b] is negative, not whole pages or above len_dev[b], and 4
+ * where a request that stays shares pages of one that is done; nothing is released then either.
  */
 int lora_kv_release_shared(const int32_t* done_dev, int32_t* len_dev, int32_t* shared_dev, int B,
                            int page_size, const int32_t* block_table, int max_blocks,

@@ -172,7 +172,7 @@ class PageTable:
     def fork(self, parent, want=None, stream=None) -> None:
         """Request b starts with the whole pages of request ``parent[b]`` (-1: unchanged), up to
         ``want[b]`` positions if given; it must be empty.  ``shared_len`` then says how many
-        positions that are.  The parent has to outlive it: it goes on holding the pages."""
+        positions that are.  The pages stay the parent's, which is released with it or later."""
         lora_kv_fork(parent, want, self.kv_len, self.shared_len, self.page_size, self.block_table,
                      self._fork_status, stream)
 
@@ -182,7 +182,7 @@ class PageTable:
 
     def release(self, done, stream=None) -> None:
         """The pages of requests with ``done[b] != 0`` (but for those that are another's) are free
-        again, their length 0."""
+        again, their length 0; nothing changes where one that stays shares them (``status``: 4)."""
         lora_kv_release_shared(done, self.kv_len, self.shared_len, self.page_size,
                                self.block_table, self.free_pages, self.n_free, self._status, stream)
 
