@@ -110,6 +110,12 @@ def lora_kv_fork(parent, want, lens, shared, page_size, block_table, status, str
     _check(rc, "lora_kv_fork")
 
 
+def _ready(t) -> None:
+    """What an object's constructor enqueued is done: a call on any stream may be its first."""
+    if t.is_cuda:
+        torch.cuda.current_stream(t.device).synchronize()
+
+
 class Rotary:
     """The angles of a rotation of queries and keys by position, for ``KvCache.append_rotated``:
     ``angles`` [max_position, 2, rotary_dim / 2] fp32, the cosines and sines, computed in 64 bits, of
@@ -129,6 +135,7 @@ class Rotary:
         angle = torch.outer(torch.arange(max_position, dtype=torch.float64, device=device),
                             frequencies.to(device=device, dtype=torch.float64))
         self._angles = torch.stack((angle.cos(), angle.sin()), 1).float().contiguous()
+        _ready(self._angles)
         self.max_position, self.rotary_dim, self.interleaved = max_position, rotary_dim, interleaved
 
     @property
@@ -161,6 +168,7 @@ class PageTable:
         self.token_slot = zeros(max_tokens)
         self.shared_len = zeros(max_requests)  # positions that are another request's pages
         self._status, self._fork_status = zeros(1), zeros(1)
+        _ready(self.free_pages)
 
     def step(self, new, adapter=None, stream=None) -> None:
         """``new`` [max_requests] int32 (CUDA): tokens each request adds, 0 for idle ones;
