@@ -181,6 +181,14 @@ struct RowTiles {
     __syncwarp();
   }
 };
+// This warp's row tiles: one place where the tile's rows of v were (v mode), or two in the ring behind what
+// the delta mode's epilogue lands there.  (A function, not a lambda of the kernel's: one that captures its
+// variables cost the plain e4m3 variants registers, which spilled: 64 rows 4096 -> 4096 17.4 us, 16.9 so.)
+template <bool VMODE>
+__device__ __forceinline__ RowTiles row_tiles(uint8_t* xscr, int nbs, uint8_t* ring, int m0, int quad, int lane) {
+  static_assert(kRowTiles == 32 * 128, "a warp's rows of one expand block");
+  return RowTiles{VMODE ? xscr + (size_t)quad * 32 * nbs * 128 : ring + quad * 2 * kRowTiles, m0 + quad * 32, lane};
+}
 template <int PENDING>
 __device__ __forceinline__ void row_tiles_wait() {  // all but the last PENDING fetches have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
@@ -675,15 +683,8 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
     uint32_t gpar = 0;  // bit s = parity of stage s's next xgrant phase
     int ring = 0;       // ring blocks (base and expand) of this CTA's earlier tiles
     if (vmode) griddep_wait();  // v and the checked slots come from earlier kernels
-    // a fused forward's bias of the tile, and this warp's row tiles: one place where its rows of v were
-    // (v mode), or two in the ring behind what the delta mode's epilogue lands there
+    // a fused forward's bias of the tile
     __nv_bfloat16* const bias_tile = reinterpret_cast<__nv_bfloat16*>(bars + 4 * stages + 8);
-    const auto row_tiles = [&](int m0) {
-      static_assert(kRowTiles == 32 * 128, "a warp's rows of one expand block");
-      uint8_t* const buf = vmode ? xscr + (size_t)quad * 32 * xl.nbs * 128
-                                 : stage_base + (size_t)BN * kBM * 4 + quad * 2 * kRowTiles;
-      return RowTiles{buf, m0 + quad * 32, lane};
-    };
     // stream-K: flags carry the launch's epoch + 1 (the epoch advances when the last CTA of a
     // launch exits, so no flag of an earlier launch matches)
     const int32_t epoch =
@@ -831,7 +832,7 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
           prefetch_row(a.ep.residual, a.ep.ldr, a, row, from, cols);
           if (vmode) {
             __syncwarp();  // the rows of v there have been read
-            const RowTiles tiles = row_tiles(m0);
+            const RowTiles tiles = row_tiles<VMODE>(xscr, xl.nbs, stage_base + (size_t)BN * kBM * 4, m0, quad, lane);
             tiles.ask(a, 0, a.ep.factor ? 0 : 1, from);
             tiles.commit();
             if (a.ep.factor) tiles.ask(a, 0, 1, from);
@@ -959,7 +960,7 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
         named_barrier(1, 128);  // the column scales staged
         RowTiles tiles;
         if constexpr (EPILOGUE != kNoEpilogue) {  // (the ring is free: the accumulator is complete)
-          tiles = row_tiles(m0);
+          tiles = row_tiles<VMODE>(xscr, xl.nbs, stage_base + (size_t)BN * kBM * 4, m0, quad, lane);
           tiles.ask(a, 0, 0, n0 + cbase);
           tiles.ask(a, 0, 1, n0 + cbase);
           tiles.commit();
@@ -1078,7 +1079,7 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
             if (FP8) scale32(acc, sxr_v, sw_tile + c);
           }
           if constexpr (EPILOGUE != kNoEpilogue) {
-            const RowTiles tiles = row_tiles(m0);
+            const RowTiles tiles = row_tiles<VMODE>(xscr, xl.nbs, stage_base + (size_t)BN * kBM * 4, m0, quad, lane);
             // What is there of factor and residual goes to registers, and its next columns are asked
             // for at once; where both are, the residual waits in its place, through which y leaves.
             const int held = a.ep.factor ? 0 : 1, next = n0 + cbase + c + 32;
