@@ -96,7 +96,11 @@ struct Request {
   int row0, q_len, kv, tiles, col_tiles;
   int first, see, slope, table_row;
   SpanKind kind;
-  __device__ __forceinline__ int last_seen(int token) const { return see + slope * token; }
+  template <Spans SPANS>
+  __device__ __forceinline__ int last_seen(int token) const {
+    if (SPANS == kShared) return see + slope * token;
+    return SPANS == kEncoder ? kv - 1 : kv - q_len + token;  // (held anyway: fewer registers)
+  }
 };
 
 // Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         src_b = in.b;
         src_tile = in.tile & ~31;
         const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
-        const int32_t* row = a.table + static_cast<size_t>(in.r.table_row) * a.max_blocks;
+        const int32_t* row = a.table + static_cast<size_t>(SPANS == kShared ? in.r.table_row : in.b) * a.max_blocks;
         const int pos = in.r.first + (src_tile + lane) * kTile;
         const bool some = in.r.kv > in.r.first;
         int id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
@@ -460,13 +464,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
       for (int j = 0; j < 2; ++j) {
         // (a column past the last has zero queries and is not written: any limit does)
         const int c = at.col * kCols + 2 * t + j;
-        lim[j] = at.r.last_seen(min(a.token_of(c), at.r.q_len - 1));
+        lim[j] = at.r.template last_seen<SPANS>(min(a.token_of(c), at.r.q_len - 1));
       }
       st.minus = make_float2(-kNone, -kNone);
       st.l = make_float2(0.f, 0.f);
-      const int lim_lo = at.r.last_seen(a.token_of(at.col * kCols));
+      const int lim_lo = at.r.template last_seen<SPANS>(a.token_of(at.col * kCols));
       const int lim_hi =
-          at.r.last_seen(a.token_of(min(at.r.q_len * G - 1, at.col * kCols + kCols - 1)));
+          at.r.template last_seen<SPANS>(a.token_of(min(at.r.q_len * G - 1, at.col * kCols + kCols - 1)));
 #pragma unroll
       for (int m = 0; m < KT; ++m)
 #pragma unroll
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
         if (lane == 0)
           info[warp * 2 + slot] =
               PieceInfo{group, at.r.tiles, min(kCols, at.r.q_len * G - at.col * kCols), at.r.row0,
-                        at.head, at.col * kCols, at.r.kind, piece};
+                        at.head, at.col * kCols, SPANS == kShared ? at.r.kind : kSpanWhole, piece};
       }
       if (at.unit + (at.r.tiles - at.tile) + kSetup >= w_hi) break;
       at.next_group(a);
