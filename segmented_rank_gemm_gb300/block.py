@@ -185,7 +185,12 @@ class MlpBlock:
         lora_rms_norm(x, self.norm_weight, self.eps, h, h, n, nq, sn, stream)
         for layer in (self.up, self.gate, self.down):
             layer.set_batch(ids, stream)
-        self.up.forward_fused(n, mid, xq=nq, sx=sn, stream=stream)
+        if nq is None:
+            self.up.forward(n, mid, stream)
+        else:
+            self.up.forward_e4m3(n, nq, sn, mid, stream)
         self.gate.forward_fused(n, mid, activation=self.activation, factor=mid, xq=nq, sx=sn,
                                 stream=stream)
-        return self.down.forward_fused(mid, y, residual=h if residual else None, stream=stream)
+        if residual:
+            return self.down.forward_fused(mid, y, residual=h, stream=stream)
+        return self.down.forward(mid, y, stream)
