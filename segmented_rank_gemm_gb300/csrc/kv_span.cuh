@@ -88,7 +88,8 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
 // positions are even): up to 32 rows 12 tiles of 32 positions, up to 40 6, 48 4, 56 3 and 64 2.  61 requests
 // of 4 to 7 tokens behind shared prefixes take 72.7 us by rows alone, 67.2 so; 512
 // single tokens, whose spans the rule does not move, 91.4 and 92.1.  (A span that is all of its
-// request goes by rows alone, as in lora_kv_attend, and gives the same bits.)
+// request goes by rows alone, as in lora_kv_attend, and gives the same bits where neither call cuts it:
+// the cuts go by all spans of a call, and those of the kernel for many rows by rules of their own here.)
 __device__ __forceinline__ bool span_is_few(const KvAttendArgs& a, const Span& s) {
   const int rows = s.q_len * a.group;
   if (rows <= a.few_rows) return true;
