@@ -1112,6 +1112,8 @@ __global__ void __maxnreg__(VMODE ? 168 : (FP8 ? 80 : 136))
           mbar_arrive(&tmem_empty[b]);
       }
     }
+    // (a tile that was given up after a wait ran out leaves fetches that write this CTA's memory)
+    if constexpr (EPILOGUE != kNoEpilogue) cp_async_wait_all();
   }
 
   // split K: the producer and MMA warps meet the epilogue warps' cluster barrier
