@@ -103,6 +103,10 @@ struct Request {
   }
 };
 
+__device__ __forceinline__ int tiles_of(int positions) {  // (up to 2^31 - 1 of them)
+  return max(1u, (static_cast<unsigned>(positions) + kTile - 1) / kTile);
+}
+
 // Request b, checked: one with bad offsets has q_len 0.  (Loads in order: the kernel's wait for the
 // one before stands ahead of them.)
 template <Spans SPANS>
@@ -112,7 +116,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   if constexpr (SPANS != kRequests) {
     const Span s = load_span<SPANS>(a, b, report);
     r = Request{s.row0, s.q_len, s.kv, 0, 0, s.first, s.see, s.slope, s.table_row, s.kind};
-    r.tiles = max(1, (r.kv - r.first + kTile - 1) / kTile);
+    r.tiles = tiles_of(r.kv - r.first);
     r.col_tiles = span_is_few(a, s) ? (r.q_len * G + kCols - 1) / kCols : 0;
     return r;
   }
@@ -133,7 +137,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b, bo
   r.slope = 1;
   r.table_row = b;
   r.kind = kSpanWhole;
-  r.tiles = max(1, (r.kv + kTile - 1) / kTile);
+  r.tiles = tiles_of(r.kv);
   r.col_tiles = r.q_len * G > a.few_rows ? 0 : (r.q_len * G + kCols - 1) / kCols;
   return r;
 }
@@ -366,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attend_kernel(KvAtten
       } else {
         src_b = in.b;
         src_tile = in.tile & ~31;
-        const int last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
+        const unsigned last = max(0, (in.r.kv - 1) >> shift);  // the request's last page
         const int32_t* row = a.table + static_cast<size_t>(SPANS == kShared ? in.r.table_row : in.b) * a.max_blocks;
-        const int pos = in.r.first + (src_tile + lane) * kTile;
+        const unsigned pos = in.r.first + (src_tile + lane) * static_cast<unsigned>(kTile);  // (past 2^31, maybe)
         const bool some = in.r.kv > in.r.first;
         int id0 = some ? __ldg(row + min(pos >> shift, last)) : 0;
         int id1 = some ? __ldg(row + min((pos + kKvBlock) >> shift, last)) : 0;

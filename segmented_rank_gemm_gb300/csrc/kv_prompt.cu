@@ -176,7 +176,7 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int b) {
 // Tiles of a request's group `part`: up to the last position its last row sees.
 __device__ __forceinline__ int group_tiles(const KvAttendArgs& a, const Request& r, int part) {
   const int last = r.see + r.slope * a.token_of(min((part + 1) * kRows, r.rows) - 1);
-  return max(1, (last + kTile) / kTile);
+  return max(last, 0) / kTile + 1;  // (last may be next to 2^31)
 }
 // Units of one head of a request, and of the first parts of it, by the lanes of a warp.
 __device__ __forceinline__ int part_units(const KvAttendArgs& a, const Request& r, int part) {
@@ -1102,11 +1102,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttendArgs a) 
                            G * D * 2);
       }
       const int32_t* const pages = a.table + static_cast<size_t>(c.r.table_row) * a.max_blocks;
-      const int last = max(0, (c.r.kv - 1) >> shift);  // the request's last page
+      const unsigned last_page = max(0, (c.r.kv - 1) >> shift);  // the request's
       // the page of a tile's position (of the last page past the end: masked, and within the cache)
       const auto page_of = [&](int j) {
-        const int pos = c.r.first + (c.tile + j) * kTile + lane * kKvBlock;
-        return copies && c.r.kv > c.r.first ? __ldg(pages + min(pos >> shift, last)) : 0;
+        const unsigned pos = c.r.first + (c.tile + j) * kTile + lane * static_cast<unsigned>(kKvBlock);
+        return copies && c.r.kv > c.r.first ? __ldg(pages + min(pos >> shift, last_page)) : 0;
       };
       int id = page_of(0);
       for (int j = 0; j < walk.count; ++j, ++n) {
