@@ -81,20 +81,13 @@ __device__ __forceinline__ Span load_span(const KvAttendArgs& a, int v, bool rep
   return s;
 }
 
-// Whether a span is the kernel for few rows' (kv_attend.cu), which costs by 8 rows and 32 positions and
-// has little to set up, or the one for many's (kv_prompt.cu), where a change of groups costs as much as
-// six tiles of 64.  A part of rows with two spans is the first one's also with more rows than a.few_rows
-// as long as it is short, by what either kernel's units were measured to cost (24 rows over 1024
-// positions are even): up to 32 rows 12 tiles of 32 positions, up to 40 6, 48 4, 56 3 and 64 2.  61 requests
-// of 4 to 7 tokens behind shared prefixes take 72.7 us by rows alone, 67.2 so; 512
-// single tokens, whose spans the rule does not move, 91.4 and 92.1.  (A span that is all of its
-// request goes by rows alone, as in lora_kv_attend, and gives the same bits where neither call cuts it:
-// the cuts go by all spans of a call, and those of the kernel for many rows by rules of their own here.)
+// Whether a span is the kernel for few rows' (kv_attend.cu) or the one for many's (kv_prompt.cu): by rows, as
+// the requests of lora_kv_attend are.  (Parts of rows with two spans to the former also with up to 64 rows where
+// they are short spare the latter changes of groups, but fill the former: 61 requests of 4 to 7 tokens behind
+// shared prefixes 67.2 us so and 72.8 by rows, but 64 requests of 7 tokens over 384 positions of their own 91 and
+// 62, and 40 batches drawn with 2 to 49 requests of 4 to 7 tokens 12% longer by their mean.)
 __device__ __forceinline__ bool span_is_few(const KvAttendArgs& a, const Span& s) {
-  const int rows = s.q_len * a.group;
-  if (rows <= a.few_rows) return true;
-  if (s.kind == kSpanWhole || rows > 64) return false;
-  return s.kv - s.first <= 32 * (0x2346C >> (rows + 7 & ~7) / 2 - 16 & 15);
+  return s.q_len * a.group <= a.few_rows;
 }
 
 // The groups agree with their requests: one with a prefix is a member, and has its group's.
