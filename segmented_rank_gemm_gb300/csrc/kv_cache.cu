@@ -194,7 +194,13 @@ constexpr int kMaxRequests = 16384;
 // over 8 heads of 128 (us, few / many): 64 requests of 1024 positions, 16 rows 50 / 67, 24 rows
 // 66 / 67, 32 rows 82 / 67; 8 of 4096, 39 / 42 at 24 and 45 / 42 at 32; 256 of 300, 79 / 97 and 89 / 97.
 constexpr int kFewRows = 24;
-constexpr int kAloneTiles = 2;
+// Tiles a warp of the kernel for few rows up to which a batch with shared prefixes is attended without sharing
+// them: that spares work that little waits for, while the kernel for prefixes and the join cost two launches.
+// Measured (us, alone / shared), 4 query heads a cache head, 8 cache heads of 128: 4 requests of 3200 positions
+// (2 tiles) 18 / 24, 6400 (4) 21 / 26, 12928 (8) 28 / 29, 25856 (16) 40 / 37; 64 requests of 320 (4) 21 / 30,
+// 768 (8) 27 / 38, 2368 (24) 48 / 42.  With 1 query head a cache head: 4 requests of 4288 (2) 18 / 20, 8576 (4)
+// 22.5 / 22.1, 17216 (8) 32 / 25; 64 of 448 (4) 22 / 29, 1536 (12) 35 / 36.
+constexpr int kAloneTiles = 4;
 
 int fail(lora_kv_cache* c, int code, const char* fmt, ...) {
   if (c) {
@@ -515,9 +521,7 @@ int lora_kv_attend_shared(lora_kv_cache_t* c, const void* q, int ldq, int q_head
     a.part_o[i] = part + i * rows * c->pages.D;
     a.part_ml[i] = reinterpret_cast<float2*>(part + 2 * rows * c->pages.D) + i * rows;
   }
-  // Where the batch is so small that every warp has at most kAloneTiles tiles, however long its requests
-  // are, they are attended by themselves: sharing spares work that nothing waits for, and joining costs
-  // a launch (4 requests of 1056 positions, 1024 of them shared: 17.3 us joined, 15.5 alone).
+  // (by the table's width: the lengths are not known here)
   const long long tiles = (static_cast<long long>(max_blocks) << c->pages.page_shift) / 32 + 1;
   if (!a.many_follow && (static_cast<long long>(T) * a.group / 8 + B) * c->pages.heads * tiles <= kAloneTiles * 16ll * c->num_sms) {
     a.alone = 1;

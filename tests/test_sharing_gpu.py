@@ -52,7 +52,9 @@ def cut_whole_requests(ws, rows, D):
 @pytest.mark.parametrize("D,G,page", [(64, 1, 16), (128, 4, 64), (64, 3, 32), (128, 8, 16), (128, 5, 128),
                                       (64, 11, 256)])
 def test_single_tokens(D, G, page):
-    groups = [(page, [(1, 1), (2, 1)]), (3 * page, [(n, 1) for n in (1, 16, 17, 33, 65)]), (7 * page, [(40, 1)])]
+    rng = np.random.default_rng(D + G)
+    groups = [(page, [(1, 1), (2, 1)]), (3 * page, [(n, 1) for n in (1, 15, 16, 17, 31, 33, 64, 65, 100)]),
+              (7 * page, [(40, 1)]), (20 * page, [(int(rng.integers(1, 90)), 1) for _ in range(70)])]
     Sharing(groups, D, 2, G, page, seed=G).check()
 
 
