@@ -226,10 +226,26 @@ def aggregate(units_per_rank: int, steps: int, world: int, max_seconds: float) -
 # our implementation
 # ------------------------------------------------------------------------------------
 
-def traffic_from_profile(kernel_src: str, config: str):
+def gemm_sources():
+    """The sources that decide what the base GEMM reads and writes: the kernel, and the host's
+    tile shapes, K splits, pairs and launches."""
+    csrc = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc")
+    return [os.path.join(csrc, name) for name in ("gemm_tc.cuh", "gemm_tc.cu")]
+
+
+def source_hash(paths) -> str:
+    """16 hex digits of the SHA-256 of the files' bytes, one file's behind another's."""
+    h = hashlib.sha256()
+    for path in [paths] if isinstance(paths, str) else paths:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def traffic_from_profile(kernel_src, config: str):
     """DRAM bytes per launch of the dominant kernel from the committed ncu summary, if it
-    was taken on the current kernel source (else None); e4m3-base runs look up
-    ``<config>_fp8``."""
+    was taken on the current kernel source (a file, or several: else None); e4m3-base runs
+    look up ``<config>_fp8``."""
     path = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(path):
         return None
@@ -238,9 +254,7 @@ def traffic_from_profile(kernel_src: str, config: str):
     entry = rec.get(config)
     if not entry:
         return None
-    with open(kernel_src, "rb") as f:
-        h = hashlib.sha256(f.read()).hexdigest()[:16]
-    if entry.get("kernel_sha256_16") != h:
+    if entry.get("kernel_sha256_16") != source_hash(kernel_src):
         return None
     return entry.get("dram_bytes_per_launch")
 
@@ -426,7 +440,7 @@ def run_stack(args):
         per_shape[name] = {"K": k, "N": n, "gemm_us": us,
                            "gemm_tflops": 2 * T * k * n / (us * 1e-6) / 1e12,
                            "bgmv_us": statistics.mean(bgmv_us[l][p] for l in range(len(st.layers)))}
-    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cuh")
+    kernel_src = gemm_sources()
     out = {
         "metric": METRIC, "value": aggregate(T, args.steps, world, seconds), "unit": UNIT,
         "n_gpus": world, "steps": args.steps, "warmup": args.warmup,
@@ -669,7 +683,7 @@ def run_ours(args):
     pk = peaks()
     gemm_s = kern_us["gemm"] * 1e-6
     achieved = work["gemm_bytes"] / gemm_s / 1e9
-    kernel_src = os.path.join(ROOT, "segmented_rank_gemm_gb300", "csrc", "gemm_tc.cuh")
+    kernel_src = gemm_sources()
     roofline = {"kernel": "gemm_tc_kernel (base GEMM%s + fused expand)"
                           % (", e4m3" if args.fp8 else ""), "bound": "hbm",
                 "achieved": achieved, "peak": pk["hbm_gbs"], "unit": "GB/s",
