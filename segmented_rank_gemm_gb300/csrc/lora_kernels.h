@@ -291,10 +291,10 @@ struct GemmPlan {
 // measured slower).
 GemmPlan gemm_tc_plan(int M, int N, int K, int num_sms, bool allow_split, int slots,
                       bool allow_pair = true);
+// CTAs of the tcgen05 GEMM resident at once in clusters of csize.
+int gemm_tc_resident_ctas(int csize, int num_sms);
 // Floats of split-K exchange scratch the tcgen05 GEMM needs for an M-row batch with the
 // K split allowed (0 when its plan does not split K).
-// CTAs resident at once in clusters of csize.
-int gemm_tc_resident_ctas(int csize, int num_sms);
 size_t gemm_tc_exchange_floats(int M, int N, int K, int num_sms);
 // The same for a given plan.
 size_t gemm_tc_plan_exchange_floats(const GemmPlan& p, int M, int N);

@@ -569,8 +569,9 @@ static bool rows_clash(const lora_layer_t* L, const void* rows, int ld, const vo
   return a < b + (size_t)T * L->N * 2 && b < a + ((size_t)(T - 1) * ld + L->N) * 2;
 }
 
-// One forward of the current batch.  ep: what lora_forward_fused does with the sums, or null.  xq and sx: the caller's e4m3 rows of x with their scales
-// (lora_forward_e4m3), or null: the layer quantises x itself where its base is e4m3.
+// One forward of the current batch.  ep: what lora_forward_fused does with the sums, or null.
+// xq and sx: the caller's e4m3 rows of x with their scales (lora_forward_e4m3), or null: the
+// layer quantises x itself where its base is e4m3.
 static int forward_batch(lora_layer_t* L, const void* x_dev, const void* xq, const float* sx,
                          void* y_dev, int T, const lora_epilogue_t* ep, void* stream_, const char* name) {
   if (L->T_batch < 0) return fail(L, LORA_ESTATE, "%s before set_batch_segments", name);
