@@ -230,7 +230,9 @@ int lora_kv_attend_cross(lora_kv_cache_t* cache, const void* q_dev, int ldq, int
  *   workspace       lora_kv_shared_workspace bytes of device memory for T rows, 16-byte aligned, for
  *                   the time of the call; it overlaps neither q nor out.
  * Sharing pays where a group has many rows that see few keys of their own; requests whose rows fill
- * the kernel's tiles by themselves (256 query rows a cache head) gain nothing by it.
+ * the kernel's tiles by themselves (256 query rows a cache head) gain nothing by it.  Every row of a
+ * call that shares passes the workspace, also those of requests without a prefix: long prompts that
+ * share nothing are faster in a call of their own.
  * What lora_kv_attend flags is flagged, and prefixes that are not as above; results of the requests
  * concerned, and of their group, are unspecified.  Limits and errors: as lora_kv_attend.
  */

@@ -12,8 +12,8 @@
 // another as the former are bound by instructions and the latter by bytes.  A thread of keys or values
 // takes a group of 16 dimensions, a thread of queries 8 pairs of kQHeads heads, which share angles.
 //
-// Measured (32 query heads over 8 of 128): 8192 tokens at positions over 32768 31 us (181 MB, 5.8 TB/s; it
-// issues in 58% of its cycles), 512 tokens 3, one 2.  With a thread for two groups of keys the angles
+// Measured (32 query heads over 8 of 128): 8192 tokens at positions over 32768 30 us (181 MB, 6.0 TB/s; it
+// issues in 61% of its cycles), 512 tokens 3, one 2.  With a thread for two groups of keys the angles
 // and addresses cost half, but 84 registers leave 16 warps an SM: 42 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
