@@ -29,6 +29,17 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     return a0 < b1 and b0 < a1
 
 
+def _product(layer: LoraLayer, x, y, xq, sx, stream) -> torch.Tensor:
+    """A product with nothing in its epilogue.  Rows of an e4m3 base leave by whole lines in a fused
+    forward's epilogue, which pays beyond decode batches (8192 rows 4096 -> 14336 419 us, 431 by the plain
+    forward; 512 rows 75 and 72).  A bf16 base's take 2% less by the plain one, the same at 512 rows."""
+    if layer.fp8_base and x.shape[0] > 512:
+        return layer.forward_fused(x, y, xq=xq, sx=sx, stream=stream)
+    if xq is None:
+        return layer.forward(x, y, stream)
+    return layer.forward_e4m3(x, xq, sx, y, stream)
+
+
 class AttentionBlock:
     """``q``, ``k``, ``v`` and ``o`` are LoraLayers: hidden -> q_heads head_dim,
     hidden -> kv_heads head_dim (k and v) and q_heads head_dim -> hidden, in bf16; q, k and v
@@ -185,12 +196,9 @@ class MlpBlock:
         lora_rms_norm(x, self.norm_weight, self.eps, h, h, n, nq, sn, stream)
         for layer in (self.up, self.gate, self.down):
             layer.set_batch(ids, stream)
-        if nq is None:
-            self.up.forward(n, mid, stream)
-        else:
-            self.up.forward_e4m3(n, nq, sn, mid, stream)
+        _product(self.up, n, mid, nq, sn, stream)
         self.gate.forward_fused(n, mid, activation=self.activation, factor=mid, xq=nq, sx=sn,
                                 stream=stream)
         if residual:
             return self.down.forward_fused(mid, y, residual=h, stream=stream)
-        return self.down.forward(mid, y, stream)
+        return _product(self.down, mid, y, None, None, stream)
